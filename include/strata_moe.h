@@ -86,7 +86,8 @@ typedef enum {
     STRATA_ECUDA = 2,         /* a CUDA launch or query failed             */
     STRATA_EUNSUPPORTED = 3,  /* valid request this build does not handle  */
     STRATA_ETIMEOUT = 4,      /* a bounded device wait ran out (latched)   */
-    STRATA_EBADROUTE = 5,     /* a forced expert id was out of range (latched) */
+    STRATA_EBADROUTE = 5,     /* a forced expert id, a group's offsets or a source row
+                                 was out of range (latched) */
     STRATA_ERANGE = 6         /* a tensor-core fp16 operand overflowed (latched) */
 } strata_status;
 
@@ -380,6 +381,136 @@ STRATA_API strata_status moe_layer_bucketing(const strata_moe_dims* dims, int32_
                                              int32_t* counts_dev, int32_t* offsets_dev,
                                              int32_t* perm_dev, int32_t* inv_perm_dev,
                                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Products grouped by expert, and the 4-bit block formats.
+ *
+ * These calls work on the slot space of moe_permute: M rows, of which group e
+ * (e in [0, E)) holds rows offsets[e] .. offsets[e + 1].  Groups may be empty;
+ * rows before offsets[0] and behind offsets[E] belong to no group: they are
+ * not read, and outputs keep what they held there.  offsets_dev stays on the
+ * device (int32 [E + 1], non-decreasing, within [0, M]); a group whose
+ * offsets run backwards or leave [0, M] is treated as empty and latches
+ * STRATA_EBADROUTE (rows that two such groups name are then undefined).
+ *   - E in [1, 1024], M >= 0, K and N in [1, 2^20] unless a call says less.
+ *     M == 0 launches nothing, except that moe_grouped_mm_dw still writes
+ *     its zeros.
+ *   - Every tensor is contiguous, 16-byte aligned (offsets and alpha 4);
+ *     outputs must not overlap inputs.
+ *   - ws_dev: at least moe_grouped_workspace_bytes() bytes, with the rules
+ *     above (256-byte aligned, zero-filled once, not shared by calls that may
+ *     run at the same time); any workspace of that size serves, a layer's
+ *     too.  Captured graphs that may run at the same time need one each.
+ *   - No call allocates, synchronises or copies to the host, so all can be
+ *     captured into a graph and replayed with other offsets.
+ *   - fp32 sums, one rounding to nearest even into the output's type;
+ *     infinities and NaNs in a row (a column of W) stay in that row (column).
+ */
+typedef enum { STRATA_BF16 = 0, STRATA_F16 = 1, STRATA_F32 = 2 } strata_dtype;
+
+/* Workspace of the calls below. */
+STRATA_API size_t moe_grouped_workspace_bytes(void);
+
+/* y[s][n] = sum_k x[s][k] W[e][n][k] for every row s of every group e.
+ * The forward product of bf16 / fp16 experts, as moe_expert_gate_up and
+ * moe_expert_down are of the int4 ones.
+ * dtype: STRATA_BF16 or STRATA_F16, of x_dev [M][K] and w_dev [E][N][K].
+ * y_dtype: dtype or STRATA_F32, of y_dev [M][N] (out). */
+STRATA_API strata_status moe_grouped_mm(int32_t dtype, const void* x_dev, const void* w_dev,
+                                        int32_t M, int32_t K, int32_t N, int32_t E,
+                                        const int32_t* offsets_dev, int32_t y_dtype, void* y_dev,
+                                        void* ws_dev, size_t ws_bytes, void* stream);
+
+/* Its gradient by x:  dx[s][k] = sum_n dy[s][n] W[e][n][k].
+ * dy_dev [M][N] and w_dev [E][N][K] in dtype; dx_dev [M][K] (out) in dtype or
+ * STRATA_F32. */
+STRATA_API strata_status moe_grouped_mm_dx(int32_t dtype, const void* dy_dev, const void* w_dev,
+                                           int32_t M, int32_t K, int32_t N, int32_t E,
+                                           const int32_t* offsets_dev, int32_t dx_dtype,
+                                           void* dx_dev, void* ws_dev, size_t ws_bytes,
+                                           void* stream);
+
+/* Its gradient by W:  dw[e][n][k] = sum over the group's rows s of
+ * dy[s][n] x[s][k]; zeros for an empty group.  dy_dev [M][N] and x_dev [M][K]
+ * in dtype; dw_dev [E][N][K] (out, written whole) in dtype or STRATA_F32.
+ * The order of the sums is fixed: the same inputs give the same bits. */
+STRATA_API strata_status moe_grouped_mm_dw(int32_t dtype, const void* dy_dev, const void* x_dev,
+                                           int32_t M, int32_t K, int32_t N, int32_t E,
+                                           const int32_t* offsets_dev, int32_t dw_dtype,
+                                           void* dw_dev, void* ws_dev, size_t ws_bytes,
+                                           void* stream);
+
+/* The 4-bit block formats: elements e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; two a byte, the first in the low half), and one scale byte
+ * for V consecutive elements of a row.
+ *   STRATA_FP4_MX  V = 32, scale 2^(byte - 127) (ue8m0; 255 is NaN)
+ *   STRATA_FP4_NV  V = 16, scale an e4m3 value, times 2^scale_exp for the
+ *                  whole tensor
+ * Scales lie in 512-byte tiles of 128 rows by 4 consecutive scales of a row:
+ * the 4 bytes of the tile's row r at (r % 32) * 16 + (r / 32) * 4.  Tiles of
+ * one block of 128 rows follow each other along the row (the last one filled
+ * with zeros); row blocks follow each other, and every non-empty group starts
+ * a row block of its own, so group e's first block is
+ * sum over e' < e of ceil(rows(e') / 128). */
+typedef enum { STRATA_FP4_MX = 0, STRATA_FP4_NV = 1 } strata_fp4_format;
+
+/* Bytes of the scales of `rows` rows by `cols` columns in n_groups groups:
+ * ragged != 0 for groups given by offsets (the most any offsets need:
+ * rows / 128 + min(n_groups, rows) row blocks), 0 for groups of
+ * rows / n_groups rows each.  0 for arguments that the calls refuse. */
+STRATA_API size_t moe_fp4_scale_bytes(int32_t format, int32_t rows, int32_t cols,
+                                      int32_t n_groups, int32_t ragged);
+
+/* Rows quantised to a 4-bit block format.  Destination row s takes source row
+ * perm[s] / top_k of x_dev (perm_dev as moe_permute writes it; NULL: row s).
+ * For each block with largest magnitude m:
+ *   MX  scale 2^max(floor(log2 m) - 2, -127)
+ *   NV  scale = e4m3(min(m 2^-scale_exp / 6, 448))
+ *   element = e2m1(x / (scale 2^scale_exp)), at most 6 in magnitude
+ * all rounded to nearest even, each decision that of exact arithmetic; a
+ * block of zeros, or whose scale rounds to 0, gets scale byte 0 and zeros; a
+ * block that holds an infinity or a NaN gets the NaN scale (its values all
+ * read as NaN).
+ * x_dev [x_rows][cols] in dtype (STRATA_BF16, _F16 or _F32); cols a multiple
+ * of 32; q_dev uint8 [rows][cols / 2] and scales_dev (scale_bytes at least
+ * moe_fp4_scale_bytes) (out).  offsets_dev NULL: n_groups groups of
+ * rows / n_groups rows (n_groups divides rows), as expert weights [E][N][K]
+ * are with rows = E N.  scale_exp in [-64, 64], 0 for MX.  A source row out
+ * of range latches STRATA_EBADROUTE and reads as zeros. */
+STRATA_API strata_status moe_fp4_quantize(int32_t format, int32_t dtype, const void* x_dev,
+                                          int32_t x_rows, int32_t cols, const int32_t* perm_dev,
+                                          int32_t top_k, int32_t rows, const int32_t* offsets_dev,
+                                          int32_t n_groups, int32_t scale_exp, uint8_t* q_dev,
+                                          uint8_t* scales_dev, size_t scale_bytes, void* ws_dev,
+                                          size_t ws_bytes, void* stream);
+
+/* The values of quantised rows: out[s][c] = element * scale * 2^scale_exp
+ * (exact in bf16 and fp32 within their range), out_dev [rows][cols] in
+ * out_dtype (STRATA_BF16, _F16 or _F32); the rest as moe_fp4_quantize. */
+STRATA_API strata_status moe_fp4_dequantize(int32_t format, const uint8_t* q_dev,
+                                            const uint8_t* scales_dev, size_t scale_bytes,
+                                            int32_t rows, int32_t cols,
+                                            const int32_t* offsets_dev, int32_t n_groups,
+                                            int32_t scale_exp, int32_t out_dtype, void* out_dev,
+                                            void* ws_dev, size_t ws_bytes, void* stream);
+
+/* The grouped product of two 4-bit operands:
+ *   p[s][n] = alpha[e] * sum_k x[s][k] W[e][n][k]       (scales applied)
+ *   y = p, or with swiglu != 0 (N even, rows 2i gate and 2i + 1 up as in the
+ *   packed layer) y[s][i] = p[s][2i] / (1 + exp(-p[s][2i])) * p[s][2i + 1]
+ * xq_dev uint8 [M][K / 2] and its scales in groups by offsets_dev; wq_dev
+ * uint8 [E][N][K / 2] and its scales in E equal groups of N rows; K a multiple
+ * of 32.  Both operands in `format`; the powers of two of NV operands go into
+ * alpha (2^(x's scale_exp + W's)).  alpha_dev fp32 [E], or NULL for 1.
+ * y_dev [M][N] (N / 2 with swiglu) in y_dtype (STRATA_BF16, _F16 or _F32). */
+STRATA_API strata_status moe_grouped_mm_fp4(int32_t format, const uint8_t* xq_dev,
+                                            const uint8_t* xs_dev, size_t xs_bytes,
+                                            const uint8_t* wq_dev, const uint8_t* wsc_dev,
+                                            size_t wsc_bytes, int32_t M, int32_t K, int32_t N,
+                                            int32_t E, const int32_t* offsets_dev,
+                                            const float* alpha_dev, int32_t swiglu,
+                                            int32_t y_dtype, void* y_dev, void* ws_dev,
+                                            size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, returns the status latched in the workspace's error
  * word (STRATA_OK when none) and clears the word.  For tests and debugging;

@@ -4,6 +4,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "grouped.h"
 #include "internal.h"
 
 namespace strata {
@@ -1007,6 +1008,190 @@ strata_status moe_layer_bucketing(const strata_moe_dims* dims, int32_t T, const 
     STRATA_TRY(cudaMemcpyAsync(inv_dev, at<int32_t>(w, W.inv), TK * 4,
                                cudaMemcpyDeviceToDevice, s));
     return STRATA_OK;
+}
+
+// ------------------------------------------------- products grouped by expert
+namespace {
+
+constexpr int kGroupedDimMax = 1 << 20;
+
+bool grouped_ws_ok(const void* ws, size_t bytes) {
+    return ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 &&
+           bytes >= kGroupedWsBytes;
+}
+
+strata_status grouped_mm(GroupedMode mode, int32_t dtype, const void* a, const void* b, int32_t M,
+                         int32_t K, int32_t N, int32_t E, const int32_t* offsets,
+                         int32_t out_dtype, void* out, void* ws, size_t ws_bytes, void* stream) {
+    if ((dtype != STRATA_BF16 && dtype != STRATA_F16) ||
+        (out_dtype != dtype && out_dtype != STRATA_F32))
+        return STRATA_EINVAL;
+    if (M < 0 || K < 1 || N < 1 || K > kGroupedDimMax || N > kGroupedDimMax || E < 1 ||
+        E > kMaxExperts)
+        return STRATA_EINVAL;
+    if (M == 0 && mode != kGmmDw) return STRATA_OK;
+    // an empty slot space has no rows to point at
+    const bool rows = M > 0;
+    if ((rows && !al16(a)) || ((rows || mode != kGmmDw) && !al16(b)) || !al16(out) ||
+        !al4(offsets) || !grouped_ws_ok(ws, ws_bytes))
+        return STRATA_EINVAL;
+    GmmArgs g{};
+    g.a = a;
+    g.b = b;
+    g.out = out;
+    g.offsets = offsets;
+    g.err = &at<Ctl>(ws, 0)->err;
+    g.M = M;
+    g.K = K;
+    g.N = N;
+    g.E = E;
+    g.dtype = dtype;
+    g.out_dtype = out_dtype;
+    return cuda_status(launch_grouped_mm(mode, g, static_cast<cudaStream_t>(stream)));
+}
+
+bool fp4_shape_ok(int32_t format, int32_t rows, int32_t cols, int32_t n_groups, bool ragged) {
+    if (format != STRATA_FP4_MX && format != STRATA_FP4_NV) return false;
+    if (rows < 0 || cols < 32 || cols > kGroupedDimMax || cols % 32 != 0) return false;
+    if (n_groups < 1 || n_groups > kMaxExperts) return false;
+    return ragged || rows % n_groups == 0;
+}
+bool fp4_exp_ok(int32_t format, int32_t scale_exp) {
+    return format == STRATA_FP4_MX ? scale_exp == 0 : scale_exp >= -64 && scale_exp <= 64;
+}
+bool dtype_ok(int32_t t) { return t == STRATA_BF16 || t == STRATA_F16 || t == STRATA_F32; }
+
+}  // namespace
+
+size_t moe_grouped_workspace_bytes(void) { return kGroupedWsBytes; }
+
+strata_status moe_grouped_mm(int32_t dtype, const void* x_dev, const void* w_dev, int32_t M,
+                             int32_t K, int32_t N, int32_t E, const int32_t* offsets_dev,
+                             int32_t y_dtype, void* y_dev, void* ws_dev, size_t ws_bytes,
+                             void* stream) {
+    return grouped_mm(kGmmFwd, dtype, x_dev, w_dev, M, K, N, E, offsets_dev, y_dtype, y_dev,
+                      ws_dev, ws_bytes, stream);
+}
+
+strata_status moe_grouped_mm_dx(int32_t dtype, const void* dy_dev, const void* w_dev, int32_t M,
+                                int32_t K, int32_t N, int32_t E, const int32_t* offsets_dev,
+                                int32_t dx_dtype, void* dx_dev, void* ws_dev, size_t ws_bytes,
+                                void* stream) {
+    return grouped_mm(kGmmDx, dtype, dy_dev, w_dev, M, K, N, E, offsets_dev, dx_dtype, dx_dev,
+                      ws_dev, ws_bytes, stream);
+}
+
+strata_status moe_grouped_mm_dw(int32_t dtype, const void* dy_dev, const void* x_dev, int32_t M,
+                                int32_t K, int32_t N, int32_t E, const int32_t* offsets_dev,
+                                int32_t dw_dtype, void* dw_dev, void* ws_dev, size_t ws_bytes,
+                                void* stream) {
+    return grouped_mm(kGmmDw, dtype, dy_dev, x_dev, M, K, N, E, offsets_dev, dw_dtype, dw_dev,
+                      ws_dev, ws_bytes, stream);
+}
+
+size_t moe_fp4_scale_bytes(int32_t format, int32_t rows, int32_t cols, int32_t n_groups,
+                           int32_t ragged) {
+    if (!fp4_shape_ok(format, rows, cols, n_groups, ragged != 0)) return 0;
+    return fp4_scale_bytes(format, rows, cols, n_groups, ragged != 0);
+}
+
+strata_status moe_fp4_quantize(int32_t format, int32_t dtype, const void* x_dev, int32_t x_rows,
+                               int32_t cols, const int32_t* perm_dev, int32_t top_k, int32_t rows,
+                               const int32_t* offsets_dev, int32_t n_groups, int32_t scale_exp,
+                               uint8_t* q_dev, uint8_t* scales_dev, size_t scale_bytes,
+                               void* ws_dev, size_t ws_bytes, void* stream) {
+    const bool ragged = offsets_dev != nullptr;
+    if (!fp4_shape_ok(format, rows, cols, n_groups, ragged) || !dtype_ok(dtype) ||
+        !fp4_exp_ok(format, scale_exp) || x_rows < 0 || top_k < 1 ||
+        (perm_dev == nullptr && x_rows != rows))
+        return STRATA_EINVAL;
+    if (rows == 0) return STRATA_OK;
+    if (!al16(x_dev) || !opt4(perm_dev) || !opt4(offsets_dev) || !al16(q_dev) ||
+        !al16(scales_dev) ||
+        scale_bytes < fp4_scale_bytes(format, rows, cols, n_groups, ragged) ||
+        !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    Fp4QuantArgs a{};
+    a.x = x_dev;
+    a.x_rows = x_rows;
+    a.dtype = dtype;
+    a.perm = perm_dev;
+    a.top_k = top_k;
+    a.q = q_dev;
+    a.scales = scales_dev;
+    a.offsets = offsets_dev;
+    a.err = &at<Ctl>(ws_dev, 0)->err;
+    a.rows = rows;
+    a.cols = cols;
+    a.n_groups = n_groups;
+    a.fmt = format;
+    a.scale_exp = scale_exp;
+    return cuda_status(launch_fp4_quantize(a, static_cast<cudaStream_t>(stream)));
+}
+
+strata_status moe_fp4_dequantize(int32_t format, const uint8_t* q_dev, const uint8_t* scales_dev,
+                                 size_t scale_bytes, int32_t rows, int32_t cols,
+                                 const int32_t* offsets_dev, int32_t n_groups, int32_t scale_exp,
+                                 int32_t out_dtype, void* out_dev, void* ws_dev, size_t ws_bytes,
+                                 void* stream) {
+    const bool ragged = offsets_dev != nullptr;
+    if (!fp4_shape_ok(format, rows, cols, n_groups, ragged) || !dtype_ok(out_dtype) ||
+        !fp4_exp_ok(format, scale_exp))
+        return STRATA_EINVAL;
+    if (rows == 0) return STRATA_OK;
+    if (!al16(q_dev) || !al16(scales_dev) || !opt4(offsets_dev) || !al16(out_dev) ||
+        scale_bytes < fp4_scale_bytes(format, rows, cols, n_groups, ragged) ||
+        !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    Fp4DequantArgs a{};
+    a.q = q_dev;
+    a.scales = scales_dev;
+    a.out = out_dev;
+    a.out_dtype = out_dtype;
+    a.offsets = offsets_dev;
+    a.err = &at<Ctl>(ws_dev, 0)->err;
+    a.rows = rows;
+    a.cols = cols;
+    a.n_groups = n_groups;
+    a.fmt = format;
+    a.scale_exp = scale_exp;
+    return cuda_status(launch_fp4_dequantize(a, static_cast<cudaStream_t>(stream)));
+}
+
+strata_status moe_grouped_mm_fp4(int32_t format, const uint8_t* xq_dev, const uint8_t* xs_dev,
+                                 size_t xs_bytes, const uint8_t* wq_dev, const uint8_t* wsc_dev,
+                                 size_t wsc_bytes, int32_t M, int32_t K, int32_t N, int32_t E,
+                                 const int32_t* offsets_dev, const float* alpha_dev,
+                                 int32_t swiglu, int32_t y_dtype, void* y_dev, void* ws_dev,
+                                 size_t ws_bytes, void* stream) {
+    if (!fp4_shape_ok(format, M, K, E, true) || N < 1 || N > kGroupedDimMax ||
+        (swiglu != 0 && N % 2 != 0) || !dtype_ok(y_dtype))
+        return STRATA_EINVAL;
+    if (M == 0) return STRATA_OK;
+    if (!al16(xq_dev) || !al16(xs_dev) || !al16(wq_dev) || !al16(wsc_dev) || !al4(offsets_dev) ||
+        !opt4(alpha_dev) || !al16(y_dev) ||
+        xs_bytes < fp4_scale_bytes(format, M, K, E, true) ||
+        wsc_bytes < fp4_scale_bytes(format, int64_t(E) * N, K, E, false) ||
+        !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    Fp4GmmArgs g{};
+    g.xq = xq_dev;
+    g.xs = xs_dev;
+    g.wq = wq_dev;
+    g.wsc = wsc_dev;
+    g.alpha = alpha_dev;
+    g.out = y_dev;
+    g.out_dtype = y_dtype;
+    g.offsets = offsets_dev;
+    g.err = &at<Ctl>(ws_dev, 0)->err;
+    g.M = M;
+    g.K = K;
+    g.N = N;
+    g.E = E;
+    g.fmt = format;
+    g.swiglu = swiglu != 0;
+    g.xs_bytes = xs_bytes;
+    return cuda_status(launch_grouped_mm_fp4(g, static_cast<cudaStream_t>(stream)));
 }
 
 void strata_set_grid_wait_limit(uint32_t polls) { set_grid_wait_limit(polls); }

@@ -1,0 +1,114 @@
+// grouped.cuh -- device helpers of the grouped products: the table of
+// groups a CTA builds from the offsets, and typed loads and stores.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace strata {
+
+// The groups as a CTA sees them: first row, rows, and the exclusive prefix
+// sum of their row blocks (pre[E] = all blocks).  A group whose offsets leave
+// [0, M] or run backwards has no rows (STRATA_EBADROUTE is latched).
+struct GroupTable {
+    int row[kMaxExperts];
+    int cnt[kMaxExperts];
+    int pre[kMaxExperts + 1];
+    int part[32];
+};
+
+// Built by all threads of the CTA (a multiple of 32, at most 1024); ends
+// with a barrier.  offsets NULL: E equal groups of M / E rows.
+__device__ __forceinline__ void build_groups(GroupTable& t, const int32_t* offsets, int E, int M,
+                                             int block_rows, uint32_t* err) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int carry = 0;
+    for (int base = 0; base < E; base += int(blockDim.x)) {
+        const int e = base + tid;
+        int row = 0, cnt = 0;
+        if (e < E) {
+            if (offsets != nullptr) {
+                row = offsets[e];
+                const int end = offsets[e + 1];
+                cnt = end - row;
+                if (row < 0 || end > M || cnt < 0) {
+                    latch(err, STRATA_EBADROUTE);
+                    row = min(max(row, 0), M);
+                    cnt = 0;
+                }
+            } else {
+                cnt = M / E;
+                row = e * cnt;
+            }
+        }
+        const int n = (cnt + block_rows - 1) / block_rows;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) t.part[warp] = incl;
+        __syncthreads();
+        int before = carry, all = carry;
+        for (int w = 0; w < int(blockDim.x) >> 5; ++w) {
+            if (w < warp) before += t.part[w];
+            all += t.part[w];
+        }
+        if (e < E) {
+            t.row[e] = row;
+            t.cnt[e] = cnt;
+            t.pre[e] = before + incl - n;
+        }
+        carry = all;
+        __syncthreads();
+    }
+    if (tid == 0) t.pre[E] = carry;
+    __syncthreads();
+}
+
+// The group that holds row block b (b < pre[E]): the last e with pre[e] <= b
+// that is not empty.
+__device__ __forceinline__ int group_of_block(const GroupTable& t, int E, int b) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.pre[mid] <= b) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// The group that holds row r, or -1: the last one whose first row is not
+// behind r (empty groups share their first row with the group after them).
+__device__ __forceinline__ int group_of_row(const GroupTable& t, int E, int r) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.row[mid] <= r) lo = mid; else hi = mid;
+    }
+    return (r >= t.row[lo] && r < t.row[lo] + t.cnt[lo]) ? lo : -1;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// One rounding, to nearest even, from the fp32 sum to the output's type.
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+
+}  // namespace strata

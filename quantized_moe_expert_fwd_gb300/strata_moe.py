@@ -99,6 +99,16 @@ def load() -> ctypes.CDLL:
             "moe_layer_profile": (I32, [D, L, P, I32, P, P, SZ, P, P, I32, P]),
             "moe_layer_path": (I32, [D, I32, I32]),
             "moe_layer_bucketing": (I32, [D, I32, P, SZ, P, P, P, P, P]),
+            "moe_grouped_workspace_bytes": (SZ, []),
+            "moe_grouped_mm": (I32, [I32, P, P, I32, I32, I32, I32, P, I32, P, P, SZ, P]),
+            "moe_grouped_mm_dx": (I32, [I32, P, P, I32, I32, I32, I32, P, I32, P, P, SZ, P]),
+            "moe_grouped_mm_dw": (I32, [I32, P, P, I32, I32, I32, I32, P, I32, P, P, SZ, P]),
+            "moe_fp4_scale_bytes": (SZ, [I32, I32, I32, I32, I32]),
+            "moe_fp4_quantize": (I32, [I32, I32, P, I32, I32, P, I32, I32, P, I32, I32, P, P, SZ,
+                                       P, SZ, P]),
+            "moe_fp4_dequantize": (I32, [I32, P, P, SZ, I32, I32, P, I32, I32, I32, P, P, SZ, P]),
+            "moe_grouped_mm_fp4": (I32, [I32, P, P, SZ, P, P, SZ, I32, I32, I32, I32, P, P, I32,
+                                         I32, P, P, SZ, P]),
             "moe_get_device_status": (I32, [P, P]),
             "strata_set_grid_wait_limit": (None, [ctypes.c_uint32]),
             "strata_px_trace_read": (I32, [P, SZ]),
@@ -120,7 +130,10 @@ EXPORTED = ("moe_workspace_bytes", "moe_decode_max_tokens", "moe_layer_decode_ma
             "moe_layer_forward_tail_skip",
             "moe_block_forward", "moe_stack_forward", "moe_decode_route", "moe_decode_gate_up",
             "moe_decode_down_combine", "moe_layer_forward_static", "moe_layer_profile",
-            "moe_layer_path", "moe_layer_bucketing", "moe_get_device_status",
+            "moe_layer_path", "moe_layer_bucketing", "moe_grouped_workspace_bytes",
+            "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw", "moe_fp4_scale_bytes",
+            "moe_fp4_quantize", "moe_fp4_dequantize", "moe_grouped_mm_fp4",
+            "moe_get_device_status",
             "strata_set_grid_wait_limit", "strata_px_trace_read",
             "strata_status_str", "strata_last_cuda_error")
 
@@ -384,6 +397,166 @@ def moe_layer_bucketing(dims, T: int, ws, counts, offsets, perm, inv, stream=Non
     _check("moe_layer_bucketing", load().moe_layer_bucketing(
         ctypes.byref(d), int(T), _ptr(ws), ws.numel(), _ptr(counts), _ptr(offsets), _ptr(perm),
         _ptr(inv), _stream(stream)))
+
+
+# ------------------------------------- products grouped by expert, 4-bit blocks
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+FP4_MX, FP4_NV = 0, 1
+
+
+def make_grouped_workspace(device="cuda") -> torch.Tensor:
+    """A workspace of the grouped products and the 4-bit block formats."""
+    return torch.zeros(moe_grouped_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def moe_grouped_workspace_bytes() -> int:
+    return int(load().moe_grouped_workspace_bytes())
+
+
+def _grouped(ws, stream, *tensors):
+    """Checks that the tensors are the binding's to pass on (the library sees
+    pointers only): contiguous, on one CUDA device, the current one.  Returns
+    the stream handle and the workspace's size."""
+    dev = ws.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError("the workspace must be on the current CUDA device")
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError("tensors must be on the workspace's device")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to strata_moe must be contiguous")
+    if not ws.is_contiguous() or ws.dtype != torch.uint8:
+        raise ValueError("the workspace must be a contiguous uint8 tensor")
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream, ws.numel()
+
+
+def _dtype(t, what, *allowed):
+    if t.dtype not in allowed:
+        raise TypeError(f"{what} must be one of {', '.join(map(str, allowed))}, not {t.dtype}")
+    return _DTYPES.get(t.dtype)
+
+
+def _offsets(offsets, groups=None):
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be an int32 vector of groups + 1 entries")
+    if groups is not None and offsets.numel() != groups + 1:
+        raise ValueError(f"offsets must have {groups + 1} entries, not {offsets.numel()}")
+    return offsets.numel() - 1
+
+
+def _shape(t, shape, what):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _grouped_mm(fn, a, b, offsets, out, ws, stream, M, K, N, E):
+    st, n = _grouped(ws, stream, a, b, offsets, out)
+    dt = _dtype(a, "the operands", torch.bfloat16, torch.float16)
+    _dtype(b, "the second operand", a.dtype)
+    od = _dtype(out, "the output", a.dtype, torch.float32)
+    _offsets(offsets, E)
+    _check(fn, getattr(load(), fn)(dt, a.data_ptr(), b.data_ptr(), M, K, N, E,
+                                   offsets.data_ptr(), od, out.data_ptr(), ws.data_ptr(), n, st))
+
+
+def moe_grouped_mm(x, w, offsets, y, ws, stream=None):
+    """y[s] = w[e] x[s] for the rows s of each group e (x [M][K], w [E][N][K],
+    offsets int32 [E + 1], y [M][N] in x's type or fp32)."""
+    E, N, K = w.shape
+    _shape(x, (x.shape[0], K), "x")
+    _shape(y, (x.shape[0], N), "y")
+    _grouped_mm("moe_grouped_mm", x, w, offsets, y, ws, stream, x.shape[0], K, N, E)
+
+
+def moe_grouped_mm_dx(dy, w, offsets, dx, ws, stream=None):
+    """dx[s] = w[e]^T dy[s]: moe_grouped_mm's gradient by x."""
+    E, N, K = w.shape
+    _shape(dy, (dy.shape[0], N), "dy")
+    _shape(dx, (dy.shape[0], K), "dx")
+    _grouped_mm("moe_grouped_mm_dx", dy, w, offsets, dx, ws, stream, dy.shape[0], K, N, E)
+
+
+def moe_grouped_mm_dw(dy, x, offsets, dw, ws, stream=None):
+    """dw[e] = sum over e's rows s of dy[s] x[s]^T: moe_grouped_mm's gradient
+    by w (every expert written, zeros for an empty group)."""
+    E, N, K = dw.shape
+    _shape(dy, (dy.shape[0], N), "dy")
+    _shape(x, (dy.shape[0], K), "x")
+    _grouped_mm("moe_grouped_mm_dw", dy, x, offsets, dw, ws, stream, dy.shape[0], K, N, E)
+
+
+def moe_fp4_scale_bytes(fmt: int, rows: int, cols: int, n_groups: int = 1,
+                        ragged: bool = False) -> int:
+    return int(load().moe_fp4_scale_bytes(int(fmt), int(rows), int(cols), int(n_groups),
+                                          1 if ragged else 0))
+
+
+def _fp4_rows(q, scales, offsets, n_groups, cols):
+    if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError("codes and scales must be uint8")
+    _shape(q, (q.shape[0], cols // 2), "the codes")
+    return int(n_groups) if offsets is None else _offsets(offsets)
+
+
+def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1,
+                     scale_exp: int = 0, perm=None, top_k: int = 1, stream=None):
+    """x [.][C] (bf16, fp16 or fp32) to codes q uint8 [rows][C / 2] and tiled
+    scales, in groups by offsets, or n_groups equal ones; row s from x's row
+    perm[s] / top_k where perm (int32) is given, which may be shorter than q
+    when offsets end with it."""
+    st, n = _grouped(ws, stream, x, q, scales, offsets, perm)
+    dt = _dtype(x, "x", torch.bfloat16, torch.float16, torch.float32)
+    groups = _fp4_rows(q, scales, offsets, n_groups, x.shape[1])
+    rows = q.shape[0]
+    if perm is not None:
+        if perm.dtype != torch.int32 or perm.dim() != 1 or perm.numel() > rows:
+            raise ValueError("perm must be an int32 vector of at most q's rows")
+        rows = perm.numel()
+    _check("moe_fp4_quantize", load().moe_fp4_quantize(
+        int(fmt), dt, x.data_ptr(), x.shape[0], x.shape[1],
+        None if perm is None else perm.data_ptr(), int(top_k), rows,
+        None if offsets is None else offsets.data_ptr(), groups, int(scale_exp), q.data_ptr(),
+        scales.data_ptr(), scales.numel(), ws.data_ptr(), n, st))
+
+
+def moe_fp4_dequantize(q, scales, out, fmt: int, ws, offsets=None, n_groups: int = 1,
+                       scale_exp: int = 0, stream=None):
+    """The values of quantised rows into out [rows][C] (bf16, fp16 or fp32)."""
+    st, n = _grouped(ws, stream, q, scales, out, offsets)
+    od = _dtype(out, "out", torch.bfloat16, torch.float16, torch.float32)
+    groups = _fp4_rows(q, scales, offsets, n_groups, out.shape[1])
+    _shape(out, (q.shape[0], out.shape[1]), "out")
+    _check("moe_fp4_dequantize", load().moe_fp4_dequantize(
+        int(fmt), q.data_ptr(), scales.data_ptr(), scales.numel(), q.shape[0], out.shape[1],
+        None if offsets is None else offsets.data_ptr(), groups, int(scale_exp), od,
+        out.data_ptr(), ws.data_ptr(), n, st))
+
+
+def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
+                       swiglu: bool = False, stream=None):
+    """y[s] = alpha[e] W[e] x[s] of two 4-bit operands (xq uint8 [M][K / 2] in
+    groups by offsets, wq uint8 [E][N][K / 2]; scales tiled), or the SwiGLU of
+    its interleaved gate/up rows (y [M][N / 2])."""
+    st, n = _grouped(ws, stream, xq, xs, wq, wsc, offsets, y, alpha)
+    E, N, half = wq.shape
+    _fp4_rows(xq, xs, offsets, E, 2 * half)
+    if wq.dtype != torch.uint8 or wsc.dtype != torch.uint8:
+        raise TypeError("codes and scales must be uint8")
+    _offsets(offsets, E)
+    od = _dtype(y, "y", torch.bfloat16, torch.float16, torch.float32)
+    _shape(y, (xq.shape[0], N // 2 if swiglu else N), "y")
+    if alpha is not None:
+        _dtype(alpha, "alpha", torch.float32)
+        _shape(alpha, (E,), "alpha")
+    _check("moe_grouped_mm_fp4", load().moe_grouped_mm_fp4(
+        int(fmt), xq.data_ptr(), xs.data_ptr(), xs.numel(), wq.data_ptr(), wsc.data_ptr(),
+        wsc.numel(), xq.shape[0], 2 * half, N, E, offsets.data_ptr(),
+        None if alpha is None else alpha.data_ptr(), 1 if swiglu else 0, od, y.data_ptr(),
+        ws.data_ptr(), n, st))
 
 
 def strata_px_trace_read(nbytes: int = 1024 * 4 * 16 * 8):
