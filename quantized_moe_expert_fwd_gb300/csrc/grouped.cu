@@ -115,6 +115,7 @@ cudaError_t pick_simt(const GmmArgs& g, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_grouped_mm(GroupedMode mode, const GmmArgs& g, cudaStream_t s) {
+    if (grouped_tc_takes(mode, g)) return launch_grouped_tc(mode, g, s);
     switch (mode) {
         case kGmmFwd: return pick_simt<kGmmFwd>(g, s);
         case kGmmDx: return pick_simt<kGmmDx>(g, s);

@@ -26,6 +26,9 @@ struct GmmArgs {
     int dtype, out_dtype;            // strata_dtype
 };
 cudaError_t launch_grouped_mm(GroupedMode mode, const GmmArgs& g, cudaStream_t s);
+// The tensor-core kernels, and whether they take this shape.
+bool grouped_tc_takes(GroupedMode mode, const GmmArgs& g);
+cudaError_t launch_grouped_tc(GroupedMode mode, const GmmArgs& g, cudaStream_t s);
 
 // Scales of `rows` rows by `cols` columns in `groups` groups, in bytes:
 // ragged groups (offsets on the device) get the most blocks they can need.

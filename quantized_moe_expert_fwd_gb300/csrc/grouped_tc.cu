@@ -1,0 +1,469 @@
+// grouped_tc.cu -- the grouped products on the tensor cores.
+//
+// A tile is 128 rows by BN columns of the output, accumulated in tensor
+// memory by tcgen05.mma (fp32) over the whole reduction, 64 of it a pipeline
+// stage:
+//   forward  rows: slots of a group     columns: n   reduction: k
+//   dx       rows: slots of a group     columns: k   reduction: n
+//   dw       rows: n of an expert       columns: k   reduction: the group's slots
+// Operands come by TMA with the 128-byte swizzle.  An operand whose rows run
+// along the reduction (W in dx, dy and x in dw) lands as sub-blocks of 64
+// columns by 64 reduction rows and is read MN-major.  Row tiles start at a
+// group's first row, so a box may reach into the next group: in forward and
+// dx those rows only feed accumulator rows that are not stored; in dw they
+// are reduction rows, and the last stage's are overwritten with zeros in both
+// operands before the MMA (a product with zero alone would let an infinity
+// of the next group through).
+//
+// Persistent, one CTA of 10 warps per SM: warps 0..7 epilogue (warp w: lanes
+// 32 (w % 4) .. of column half w / 4), 8 TMA producer, 9 MMA.  Two
+// accumulator buffers, so a tile's epilogue overlaps the next tile's MMAs.
+//
+// fp32 outputs: the tensor cores truncate as they add (relative error 2e-6 at
+// 2048 terms, growing with their number), so the accumulator is drained every
+// 512 terms into fp32 registers of the epilogue, where it is added with
+// rounding (5e-7 at any length).  16-bit outputs round away far more than
+// that and take the whole reduction in one accumulator.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "grouped.cuh"
+#include "grouped.h"
+#include "tc.cuh"
+
+namespace strata {
+
+namespace {
+
+constexpr int kGtThreads = 320;
+constexpr int kGtEpiWarps = 8, kGtTmaWarp = 8, kGtMmaWarp = 9;
+constexpr int kGtRows = 128;                    // tile rows
+constexpr int kGtK = 64;                        // reduction of a stage (128 bytes)
+constexpr int kGtPromote = 8;                   // stages between drains of an fp32 output
+constexpr uint32_t kGtABytes = kGtRows * 128;
+constexpr uint32_t kGtSub = 64 * 128;           // a 64 x 64 MN-major sub-block
+constexpr int kGtBox = 32;                      // row box heights: 32, 64, 96, 128
+
+__host__ __device__ constexpr uint32_t gt_stage_bytes(int BN) { return kGtABytes + uint32_t(BN) * 128u; }
+__host__ __device__ constexpr int gt_stages(int BN) { return int(196608u / gt_stage_bytes(BN)); }
+
+struct GtMaps {
+    CUtensorMap a[kGtRows / kGtBox];            // by box height (dw: a[0] alone)
+    CUtensorMap b;
+};
+
+struct GtArgs {
+    void* out;
+    const int32_t* offsets;
+    uint32_t* err;
+    int M, K, N, E;
+    int bf16;                                   // operands (and a 16-bit output)
+    int vec;                                    // bytes that every output row is aligned to: 32, 16, 0
+};
+
+struct GtTile {
+    int e, arow, rows, c0, stages, slot0, cnt;
+    size_t orow;
+};
+
+__device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                        uint32_t site, uint32_t slot) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 255u) == 255u && *reinterpret_cast<const volatile uint32_t*>(err) == 4u)
+            return false;
+    }
+    latch_timeout(err, site, slot, parity, 0);
+    return false;
+}
+
+template <int MODE, int BN>
+__device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a, long long tile) {
+    const int cols = MODE == kGmmFwd ? a.N : a.K;
+    const int nt = (cols + BN - 1) / BN;
+    GtTile i;
+    const int rb = int(tile / nt);
+    i.c0 = int(tile - (long long)rb * nt) * BN;
+    if (MODE == kGmmDw) {
+        const int mt = (a.N + kGtRows - 1) / kGtRows;
+        i.e = rb / mt;
+        i.arow = (rb - i.e * mt) * kGtRows;
+        i.rows = min(kGtRows, a.N - i.arow);
+        i.slot0 = t.row[i.e];
+        i.cnt = t.cnt[i.e];
+        i.stages = (i.cnt + kGtK - 1) / kGtK;
+        i.orow = size_t(i.e) * a.N + i.arow;
+    } else {
+        i.e = group_of_block(t, a.E, rb);
+        const int in = (rb - t.pre[i.e]) * kGtRows;
+        i.arow = t.row[i.e] + in;
+        i.rows = min(kGtRows, t.cnt[i.e] - in);
+        i.slot0 = i.cnt = 0;
+        i.stages = ((MODE == kGmmFwd ? a.K : a.N) + kGtK - 1) / kGtK;
+        i.orow = size_t(i.arow);
+    }
+    return i;
+}
+
+// 32 consecutive columns of one output row from fp32 values; nv of them
+// exist.  A lane writes whole 32-byte sectors where the row allows it.
+__device__ __forceinline__ void gt_st8(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void gt_store_words(uint8_t* p, const uint32_t (&w)[WORDS], int vec) {
+    if (vec == 32) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 8) gt_st8(p + i * 4, w + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4)
+            *reinterpret_cast<uint4*>(p + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+}
+__device__ __forceinline__ uint32_t gt_pack(float lo, float hi, int bf16) {
+    uint32_t r;
+    if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool F32>
+__device__ __forceinline__ void gt_store32(void* out, size_t at, const float* v, int nv, int vec,
+                                           int bf16) {
+    if (F32) {
+        float* p = static_cast<float*>(out) + at;
+        if (nv >= 32 && vec) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
+            gt_store_words(reinterpret_cast<uint8_t*>(p), w, vec);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < nv) p[j] = v[j];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(out) + at;
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = gt_pack(v[2 * j], v[2 * j + 1], bf16);
+        if (nv >= 32 && vec) {
+            gt_store_words(reinterpret_cast<uint8_t*>(p), w, vec);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < nv) p[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+}
+
+template <int MODE, int BN, bool F32>
+__global__ void __launch_bounds__(kGtThreads, 1)
+    k_gmm_tc(const __grid_constant__ GtMaps maps, GtArgs a) {
+    constexpr int STAGES = gt_stages(BN);
+    constexpr uint32_t STAGE = gt_stage_bytes(BN);
+    extern __shared__ uint8_t gt_dyn[];
+    __shared__ GroupTable t;
+    __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], done;
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gt_dyn) + 1023) &
+                                               ~uintptr_t(1023));
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kGtEpiWarps);
+        }
+        mbar_init(&done, 1);
+        mbar_fence_init();
+        tma_prefetch_map(&maps.b);
+        tma_prefetch_map(&maps.a[0]);
+    }
+    if (wid == kGtMmaWarp) {
+        tmem_alloc(&tmem_base, 2 * BN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    build_groups(t, a.offsets, a.E, a.M, kGtRows, a.err);
+    const uint32_t tmem = tmem_base;
+    const int cols = MODE == kGmmFwd ? a.N : a.K;
+    const long long nt = (cols + BN - 1) / BN;
+    const long long tiles =
+        nt * (MODE == kGmmDw ? (long long)a.E * ((a.N + kGtRows - 1) / kGtRows) : t.pre[a.E]);
+
+    if (wid == kGtTmaWarp) {
+        if (lane == 0) {
+            uint32_t st = 0;
+            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+                const GtTile i = gt_tile<MODE, BN>(t, a, tile);
+                const int nbox = (i.rows + kGtBox - 1) / kGtBox;
+                const CUtensorMap* ma = &maps.a[MODE == kGmmDw ? 0 : nbox - 1];
+                const uint32_t bytes =
+                    (MODE == kGmmDw ? kGtABytes : uint32_t(nbox) * kGtBox * 128u) + BN * 128u;
+                for (int ks = 0; ks < i.stages; ++ks, ++st) {
+                    const uint32_t s = st % STAGES, round = st / STAGES;
+                    if (round > 0) gt_wait(&empty[s], (round - 1) & 1, a.err, 50, s);
+                    uint8_t* sa = base + s * STAGE;
+                    uint8_t* sb = sa + kGtABytes;
+                    const int r0 = ks * kGtK;
+                    mbar_expect_tx(&full[s], bytes);
+                    if (MODE == kGmmDw) {
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_2d(sa + j * kGtSub, ma, i.arow + 64 * j, i.slot0 + r0, &full[s]);
+                        for (int j = 0; j < BN / 64; ++j)
+                            tma_load_2d(sb + j * kGtSub, &maps.b, i.c0 + 64 * j, i.slot0 + r0,
+                                        &full[s]);
+                    } else {
+                        tma_load_2d(sa, ma, r0, i.arow, &full[s]);
+                        if (MODE == kGmmFwd) {
+                            tma_load_3d(sb, &maps.b, r0, i.c0, i.e, &full[s]);
+                        } else {
+                            for (int j = 0; j < BN / 64; ++j)
+                                tma_load_3d(sb + j * kGtSub, &maps.b, i.c0 + 64 * j, r0, i.e,
+                                            &full[s]);
+                        }
+                    }
+                }
+            }
+            // every copy has landed before the CTA exits
+            for (uint32_t k = st > STAGES ? st - STAGES : 0; k < st; ++k)
+                gt_wait(&full[k % STAGES], (k / STAGES) & 1, a.err, 51, k % STAGES);
+        }
+    } else if (wid == kGtMmaWarp) {
+        const uint32_t idesc = idesc_f16(kGtRows, BN, a.bf16) |
+                               (MODE == kGmmDw ? kIdescMnA : 0u) |
+                               (MODE != kGmmFwd ? kIdescMnB : 0u);
+        constexpr uint32_t a_step = MODE == kGmmDw ? 2048 / 16 : 2;
+        constexpr uint32_t b_step = MODE != kGmmFwd ? 2048 / 16 : 2;
+        uint32_t st = 0, acc = 0;
+        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            const GtTile i = gt_tile<MODE, BN>(t, a, tile);
+            for (int ks = 0; ks < i.stages; ++ks, ++st) {
+                const uint32_t s = st % STAGES;
+                const bool first = F32 ? ks % kGtPromote == 0 : ks == 0;
+                const bool last = ks == i.stages - 1 || (F32 && ks % kGtPromote == kGtPromote - 1);
+                const uint32_t buf = acc & 1u;
+                if (first && acc >= 2)
+                    gt_wait(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 52, buf);
+                gt_wait(&full[s], (st / STAGES) & 1, a.err, 53, s);
+                uint8_t* sa = base + s * STAGE;
+                uint8_t* sb = sa + kGtABytes;
+                int steps = kGtK / 16;
+                if (MODE == kGmmDw) {
+                    const int valid = min(kGtK, i.cnt - ks * kGtK);
+                    steps = (valid + 15) / 16;
+                    const int dead = steps * 16 - valid;       // rows of the next group
+                    if (dead > 0) {
+                        for (int j = lane; j < dead * 8 * (2 + BN / 64); j += 32) {
+                            const int sub = j / (dead * 8), r = j % (dead * 8);
+                            *reinterpret_cast<uint4*>(sa + sub * kGtSub + valid * 128 + r * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t da = MODE == kGmmDw ? sdesc_mn_sw128(smem_u32(sa), kGtSub)
+                                                       : sdesc_k_sw128(smem_u32(sa));
+                    const uint64_t db = MODE != kGmmFwd ? sdesc_mn_sw128(smem_u32(sb), kGtSub)
+                                                        : sdesc_k_sw128(smem_u32(sb));
+#pragma unroll
+                    for (int j = 0; j < kGtK / 16; ++j)
+                        if (MODE != kGmmDw || j < steps)
+                            umma_f16(tmem + buf * BN, da + j * a_step, db + j * b_step, idesc,
+                                     (first && j == 0) ? 0u : 1u);
+                    umma_commit(&empty[s]);
+                    if (last) umma_commit(&acc_full[buf]);
+                }
+                __syncwarp();
+                if (last) ++acc;
+            }
+        }
+        // no product may still be writing the TMEM when it is freed
+        if (lane == 0) umma_commit(&done);
+        __syncwarp();
+        gt_wait(&done, 0, a.err, 54, 0);
+    } else {
+        constexpr int CH = BN / 64;              // 32-column pieces of a warp's half
+        const int half = wid >> 2, r = (wid & 3) * 32 + lane;
+        const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (BN / 2));
+        uint32_t acc = 0;
+        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            const GtTile i = gt_tile<MODE, BN>(t, a, tile);
+            const int c0 = i.c0 + half * (BN / 2);
+            const size_t at = (i.orow + r) * size_t(cols) + c0;
+            const bool live = r < i.rows;
+            if (F32) {
+                float sum[CH][32];
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
+                for (int ks = 0; ks < i.stages; ks += kGtPromote, ++acc) {
+                    const uint32_t buf = acc & 1u;
+                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(tl + buf * BN + c * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c][j] += __uint_as_float(v[j]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                }
+                if (live) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        gt_store32<true>(a.out, at + c * 32, sum[c], cols - c0 - c * 32, a.vec, 0);
+                }
+            } else {
+                const uint32_t buf = acc & 1u;
+                if (i.stages > 0) {
+                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t v[32];
+                    if (i.stages > 0) {
+                        tmem_ld32(tl + buf * BN + c * 32, v);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+                    if (live)
+                        gt_store32<false>(a.out, at + c * 32, reinterpret_cast<const float*>(v),
+                                          cols - c0 - c * 32, a.vec, a.bf16);
+                }
+                if (i.stages > 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                    ++acc;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (wid == kGtMmaWarp) tmem_dealloc(tmem, 2 * BN);
+}
+
+// ------------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 gt_encode_fn() {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (fn == nullptr) {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+// A row-major array [z][rows][inner] of 16-bit elements with the 128-byte
+// swizzle; boxes of 64 elements by box_rows rows.  z = 0: two dimensions.
+bool gt_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t z,
+            uint32_t box_rows) {
+    auto fn = gt_encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dim[3] = {inner, rows, z};
+    const cuuint64_t stride[2] = {inner * 2, inner * rows * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1}, one[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, z ? 3 : 2, const_cast<void*>(base), dim, stride,
+              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int BN, bool F32>
+cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
+    GtMaps m;
+    bool ok = true;
+    const uint64_t rows = uint64_t(g.M > 0 ? g.M : 1);
+    if (MODE == kGmmDw) {
+        // with no rows nothing is loaded; the maps still need an address
+        const void* a = g.M > 0 ? g.a : g.out;
+        const void* b = g.M > 0 ? g.b : g.out;
+        ok = gt_map(&m.a[0], a, g.N, rows, 0, 64) && gt_map(&m.b, b, g.K, rows, 0, 64);
+        for (int i = 1; i < kGtRows / kGtBox; ++i) m.a[i] = m.a[0];
+    } else {
+        const int red = MODE == kGmmFwd ? g.K : g.N;
+        for (int i = 0; i < kGtRows / kGtBox; ++i)
+            ok = ok && gt_map(&m.a[i], g.a, red, rows, 0, kGtBox * (i + 1));
+        ok = ok && gt_map(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? BN : 64);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    GtArgs a{};
+    a.out = g.out;
+    a.offsets = g.offsets;
+    a.err = g.err;
+    a.M = g.M;
+    a.K = g.K;
+    a.N = g.N;
+    a.E = g.E;
+    a.bf16 = g.dtype == STRATA_BF16;
+    const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
+    const size_t mis = pitch | reinterpret_cast<uintptr_t>(g.out);
+    a.vec = mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
+    const size_t dyn = size_t(gt_stages(BN)) * gt_stage_bytes(BN) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_gmm_tc<MODE, BN, F32>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(device_info().sms);
+    cfg.blockDim = dim3(kGtThreads);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_gmm_tc<MODE, BN, F32>, m, a);
+}
+
+template <int MODE>
+cudaError_t gt_pick(const GmmArgs& g, cudaStream_t s) {
+    const bool f32 = g.out_dtype == STRATA_F32;
+    return f32 ? gt_run<MODE, 256, true>(g, s) : gt_run<MODE, 256, false>(g, s);
+}
+
+}  // namespace
+
+// The tensor maps need rows of a multiple of 16 bytes.
+bool grouped_tc_takes(GroupedMode mode, const GmmArgs& g) {
+    return g.K % 8 == 0 && (mode == kGmmFwd || g.N % 8 == 0);
+}
+
+cudaError_t launch_grouped_tc(GroupedMode mode, const GmmArgs& g, cudaStream_t s) {
+    switch (mode) {
+        case kGmmFwd: return gt_pick<kGmmFwd>(g, s);
+        case kGmmDx: return gt_pick<kGmmDx>(g, s);
+        default: return gt_pick<kGmmDw>(g, s);
+    }
+}
+
+}  // namespace strata

@@ -58,14 +58,30 @@ __device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t smem_addr) {
     return d;
 }
 
+// The same for an MN-major operand tile: sub-blocks of 64 M (or N) elements
+// (128 bytes) by K rows, 8 K rows an atom of 1024 bytes, the next 64
+// elements `sub_bytes` on.  A K step of 16 advances the start address by
+// 2048 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr, uint32_t sub_bytes) {
+    uint64_t d = 0;
+    d |= uint64_t((smem_addr & 0x3FFFFu) >> 4);
+    d |= uint64_t(sub_bytes >> 4) << 16;     // stride between 64-element sub-blocks
+    d |= uint64_t(1024 >> 4) << 32;          // stride between 8-row atoms along K
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16 with an fp32 accumulator,
-// both operands K-major.  ab_bf16: 0 = fp16 operands, 1 = bf16 operands.
+// both operands K-major (kIdescMnA / kIdescMnB or-ed in: that one MN-major).  ab_bf16: 0 = fp16 operands, 1 = bf16 operands.
 //   [4,6) D format (1 = f32)  [7,10) A format  [10,13) B format
 //   [15] A major  [16] B major (0 = K)  [17,23) N >> 3  [24,29) M >> 4
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int ab_bf16) {
     return (1u << 4) | (uint32_t(ab_bf16) << 7) | (uint32_t(ab_bf16) << 10) |
            (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
+
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
 
 // ------------------------------------------------------------------- MMA
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
