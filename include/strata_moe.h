@@ -389,9 +389,9 @@ STRATA_API strata_status moe_layer_bucketing(const strata_moe_dims* dims, int32_
  * (e in [0, E)) holds rows offsets[e] .. offsets[e + 1].  Groups may be empty;
  * rows before offsets[0] and behind offsets[E] belong to no group: they are
  * not read, and outputs keep what they held there.  offsets_dev stays on the
- * device (int32 [E + 1], non-decreasing, within [0, M]); a group whose
- * offsets run backwards or leave [0, M] is treated as empty and latches
- * STRATA_EBADROUTE (rows that two such groups name are then undefined).
+ * device (int32 [E + 1], non-decreasing, within [0, M]); offsets that run
+ * backwards anywhere or leave [0, M] latch STRATA_EBADROUTE, and every group
+ * of that call counts as empty.
  *   - E in [1, 1024], M >= 0, K and N in [1, 2^20] unless a call says less.
  *     M == 0 launches nothing, except that moe_grouped_mm_dw still writes
  *     its zeros.

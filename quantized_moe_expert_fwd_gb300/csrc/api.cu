@@ -1190,7 +1190,6 @@ strata_status moe_grouped_mm_fp4(int32_t format, const uint8_t* xq_dev, const ui
     g.E = E;
     g.fmt = format;
     g.swiglu = swiglu != 0;
-    g.xs_bytes = xs_bytes;
     return cuda_status(launch_grouped_mm_fp4(g, static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,6 +1,5 @@
 // fp4.cu -- the 4-bit block formats: rows quantised to e2m1 blocks with a
-// scale byte each, back to values, and the product grouped by expert of two
-// such operands.
+// scale byte each, and back to values.
 #include <type_traits>
 
 #include "fp4.cuh"
@@ -203,50 +202,6 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_dequantize(Fp4DequantArgs a) 
     }
 }
 
-// One output a thread.
-template <int FMT, typename TO>
-__global__ void __launch_bounds__(256) k_gmm_fp4_simt(Fp4GmmArgs g) {
-    __shared__ GroupTable t;
-    build_groups(t, g.offsets, g.E, g.M, 128, g.err);
-    const int cols = g.swiglu ? g.N / 2 : g.N, words = fp4_words(g.K, FMT);
-    const int wblocks = (g.N + 127) / 128;
-    TO* out = static_cast<TO*>(g.out);
-    const long long total = (long long)g.M * cols;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
-         i += (long long)gridDim.x * 256) {
-        const int row = int(i / cols), c = int(i % cols);
-        const int e = group_of_row(t, g.E, row);
-        if (e < 0) continue;
-        const int r = row - t.row[e];
-        const size_t xb = size_t(t.pre[e]) + (r >> 7);
-        const float al = g.alpha != nullptr ? g.alpha[e] : 1.0f;
-        float y[2];
-        for (int h = 0; h < (g.swiglu ? 2 : 1); ++h) {
-            const int n = g.swiglu ? 2 * c + h : c;
-            const uint8_t* xq = g.xq + size_t(row) * (g.K / 2);
-            const uint8_t* wq = g.wq + (size_t(e) * g.N + n) * (g.K / 2);
-            float sum = 0.0f;
-            for (int b = 0; b < g.K / Fp4<FMT>::kVec; ++b) {
-                const float sx = fp4_scale_f32<FMT>(g.xs[fp4_scale_at(xb, words, r, b >> 2) + (b & 3)]);
-                const float sw = fp4_scale_f32<FMT>(
-                    g.wsc[fp4_scale_at(size_t(e) * wblocks + (n >> 7), words, n, b >> 2) + (b & 3)]);
-                float d = 0.0f;
-                for (int j = 0; j < Fp4<FMT>::kVec / 2; ++j) {
-                    const uint32_t hx = e2m1x2_to_f16x2(xq[b * (Fp4<FMT>::kVec / 2) + j]);
-                    const uint32_t hw = e2m1x2_to_f16x2(wq[b * (Fp4<FMT>::kVec / 2) + j]);
-                    const float2 fx = __half22float2(*reinterpret_cast<const __half2*>(&hx));
-                    const float2 fw = __half22float2(*reinterpret_cast<const __half2*>(&hw));
-                    d = fmaf(fx.x, fw.x, fmaf(fx.y, fw.y, d));
-                }
-                sum = fmaf(d, sx * sw, sum);
-            }
-            y[h] = al * sum;
-        }
-        out[size_t(row) * cols + c] = from_f32<TO>(g.swiglu ? silu_mul(y[0], y[1]) : y[0]);
-    }
-}
-
-
 int flat_grid(long long items, int threads) {
     const long long want = (items + threads - 1) / threads, most = (long long)device_info().sms * 8;
     return int(want < most ? want : most);
@@ -277,19 +232,6 @@ cudaError_t launch_fp4_dequantize(const Fp4DequantArgs& a, cudaStream_t s) {
         else k_fp4_dequantize<F, float><<<grid, kQThreads, 0, s>>>(a);
     };
     if (a.fmt == STRATA_FP4_MX) go(std::integral_constant<int, 0>{});
-    else go(std::integral_constant<int, 1>{});
-    return cudaGetLastError();
-}
-
-cudaError_t launch_grouped_mm_fp4(const Fp4GmmArgs& g, cudaStream_t s) {
-    const int grid = flat_grid((long long)g.M * (g.swiglu ? g.N / 2 : g.N), 256);
-    auto go = [&](auto fmt) {
-        constexpr int F = decltype(fmt)::value;
-        if (g.out_dtype == STRATA_BF16) k_gmm_fp4_simt<F, __nv_bfloat16><<<grid, 256, 0, s>>>(g);
-        else if (g.out_dtype == STRATA_F16) k_gmm_fp4_simt<F, __half><<<grid, 256, 0, s>>>(g);
-        else k_gmm_fp4_simt<F, float><<<grid, 256, 0, s>>>(g);
-    };
-    if (g.fmt == STRATA_FP4_MX) go(std::integral_constant<int, 0>{});
     else go(std::integral_constant<int, 1>{});
     return cudaGetLastError();
 }

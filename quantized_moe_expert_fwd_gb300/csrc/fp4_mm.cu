@@ -1,0 +1,265 @@
+// fp4_mm.cu -- the grouped product of two 4-bit operands on the tensor cores.
+//
+// A tile is 128 slots of a group by 128 rows of W, accumulated in tensor
+// memory by the block-scaled tcgen05.mma (e2m1 operands, K = 64 an
+// instruction, the scales applied by the tensor core), K = 256 a stage: 128
+// packed bytes a row with the 128-byte swizzle.  The scales of both operands
+// lie in memory as 128-row by 4-scale tiles in the order that the tensor
+// memory wants, so a stage's scales are one contiguous bulk copy per operand
+// and one tcgen05.cp per tile (32 lanes by 4 words, to all four lane
+// quarters).  An NV scale word covers one K step (scale_vec::4X), an MX word
+// two (scale_vec::2X, the step's half of the word picked by the descriptor).
+//
+// Roles, buffers and waits as in grouped_tc.cu.  The epilogue multiplies by
+// alpha[e] and, for SwiGLU, joins the gate and up columns 2i and 2i + 1, which
+// one lane holds side by side.
+#include "fp4.cuh"
+#include "grouped_tc.cuh"
+
+namespace strata {
+
+namespace {
+
+constexpr int kF4N = 128;                       // tile columns
+constexpr int kF4K = 256;                       // K of a stage
+constexpr uint32_t kF4Data = 128 * 128;         // one operand's packed rows of a stage
+
+template <int FMT>
+struct F4 {
+    static constexpr int kWords = FMT == 0 ? 2 : 4;            // scale words a stage
+    static constexpr uint32_t kSf = kWords * 512;              // one operand's scales of a stage
+    static constexpr uint32_t kStage = 2 * kF4Data + 2 * kSf;
+    static constexpr int kStages = 5;
+    static constexpr size_t kDyn = size_t(kStages) * kStage + 1024;
+    // tensor memory: two accumulators, two buffers of both operands' scales
+    static constexpr uint32_t kSfCol = 2 * kF4N;
+    static constexpr uint32_t kSfCols = kWords * 4;            // one operand's
+};
+
+struct F4Maps {
+    CUtensorMap a[kGtRows / kGtBox];
+    CUtensorMap b;
+};
+
+// Instruction descriptor of the block-scaled kinds with e2m1 operands:
+//   [4,6) B scale id  [7,10) A format (1 = e2m1)  [10,12) B format
+//   [17,23) N >> 3  [23] scale type (0 = ue4m3, 1 = ue8m0)  [27,29) M >> 7
+//   [29,31) A scale id
+__device__ __forceinline__ uint32_t idesc_f4(int M, int N, int ue8m0, int sf_id) {
+    return (uint32_t(sf_id) << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) |
+           (uint32_t(ue8m0) << 23) | (uint32_t(M >> 7) << 27) | (uint32_t(sf_id) << 29);
+}
+
+template <int FMT>
+__device__ __forceinline__ void umma_f4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if (FMT == 0)
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+            "[%5], p; }" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+            "[%4], [%5], p; }" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// One scale tile (512 bytes of shared memory, no swizzle, 8-row groups of
+// 128 bytes) to 4 columns of tensor memory, all four lane quarters.
+__device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t smem) {
+    const uint64_t d = uint64_t((smem & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 16) |
+                       (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+template <int FMT, bool F32, bool SWIGLU>
+__global__ void __launch_bounds__(kGtThreads, 1)
+    k_gmm_f4(const __grid_constant__ F4Maps maps, Fp4GmmArgs a, int vec) {
+    using C = F4<FMT>;
+    extern __shared__ uint8_t f4_dyn[];
+    __shared__ GroupTable t;
+    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2],
+        done;
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(f4_dyn) + 1023) &
+                                               ~uintptr_t(1023));
+    // a stage: A rows, B rows (1024-byte aligned); the scales of all stages behind
+    uint8_t* sf_base = base + size_t(C::kStages) * 2 * kF4Data;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kGtEpiWarps);
+        }
+        mbar_init(&done, 1);
+        mbar_fence_init();
+        tma_prefetch_map(&maps.b);
+        tma_prefetch_map(&maps.a[0]);
+    }
+    if (wid == kGtMmaWarp) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    build_groups(t, a.offsets, a.E, a.M, kGtRows, a.err);
+    const uint32_t tmem = tmem_base;
+    const int nt = (a.N + kF4N - 1) / kF4N, words = fp4_words(a.K, FMT);
+    const int stages = (a.K + kF4K - 1) / kF4K;
+    const long long tiles = (long long)t.pre[a.E] * nt;
+
+    if (wid == kGtTmaWarp) {
+        if (lane == 0) {
+            uint32_t st = 0;
+            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+                const int rb = int(tile / nt), ct = int(tile - (long long)rb * nt);
+                const int e = group_of_block(t, a.E, rb);
+                const int in = (rb - t.pre[e]) * kGtRows, arow = t.row[e] + in;
+                const int nbox = (min(kGtRows, t.cnt[e] - in) + kGtBox - 1) / kGtBox;
+                const CUtensorMap* ma = &maps.a[nbox - 1];
+                const uint8_t* sa_g = a.xs + size_t(rb) * words * 512;
+                const uint8_t* sb_g = a.wsc + (size_t(e) * nt + ct) * words * 512;
+                for (int ks = 0; ks < stages; ++ks, ++st) {
+                    const uint32_t s = st % C::kStages, round = st / C::kStages;
+                    if (round > 0) gt_wait(&empty[s], (round - 1) & 1, a.err, 60, s);
+                    uint8_t* sa = base + s * (2 * kF4Data);
+                    uint8_t* sf = sf_base + s * (2 * C::kSf);
+                    const int w0 = ks * C::kWords;
+                    const uint32_t sf_bytes = uint32_t(min(C::kWords, words - w0)) * 512u;
+                    mbar_expect_tx(&full[s],
+                                   uint32_t(nbox) * kGtBox * 128u + kF4Data + 2 * sf_bytes);
+                    tma_load_2d(sa, ma, ks * (kF4K / 2), arow, &full[s]);
+                    tma_load_3d(sa + kF4Data, &maps.b, ks * (kF4K / 2), ct * kF4N, e, &full[s]);
+                    bulk_g2s(sf, sa_g + size_t(w0) * 512, sf_bytes, &full[s]);
+                    bulk_g2s(sf + C::kSf, sb_g + size_t(w0) * 512, sf_bytes, &full[s]);
+                }
+            }
+            // every copy has landed before the CTA exits
+            for (uint32_t k = st > C::kStages ? st - C::kStages : 0; k < st; ++k)
+                gt_wait(&full[k % C::kStages], (k / C::kStages) & 1, a.err, 61, k % C::kStages);
+        }
+    } else if (wid == kGtMmaWarp) {
+        uint32_t st = 0, acc = 0;
+        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++acc) {
+            const uint32_t buf = acc & 1u;
+            if (acc >= 2) gt_wait(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 62, buf);
+            for (int ks = 0; ks < stages; ++ks, ++st) {
+                const uint32_t s = st % C::kStages;
+                gt_wait(&full[s], (st / C::kStages) & 1, a.err, 63, s);
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t sa = smem_u32(base + s * (2 * kF4Data));
+                    const uint32_t sf = smem_u32(sf_base + s * (2 * C::kSf));
+                    const uint32_t ca = tmem + C::kSfCol + (st & 1u) * (2 * C::kSfCols);
+                    const uint32_t cb = ca + C::kSfCols;
+                    // K steps that exist: past K the scales are not loaded
+                    const int steps = min(4, (a.K - ks * kF4K + 63) / 64);
+                    const int nw = FMT == 0 ? (steps + 1) / 2 : steps;
+#pragma unroll
+                    for (int w = 0; w < C::kWords; ++w)
+                        if (w < nw) {
+                            sf_copy(ca + 4 * w, sf + w * 512);
+                            sf_copy(cb + 4 * w, sf + C::kSf + w * 512);
+                        }
+                    const uint64_t da = sdesc_k_sw128(sa), db = sdesc_k_sw128(sa + kF4Data);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < steps) {
+                            const int w = FMT == 0 ? j / 2 : j;
+                            umma_f4<FMT>(tmem + buf * kF4N, da + 2 * j, db + 2 * j,
+                                         idesc_f4(kGtRows, kF4N, FMT == 0, FMT == 0 ? 2 * (j & 1) : 0),
+                                         ca + 4 * w, cb + 4 * w, (ks | j) != 0 ? 1u : 0u);
+                        }
+                    umma_commit(&empty[s]);
+                    if (ks == stages - 1) umma_commit(&acc_full[buf]);
+                }
+                __syncwarp();
+            }
+        }
+        // no product may still be writing the TMEM when it is freed
+        if (lane == 0) umma_commit(&done);
+        __syncwarp();
+        gt_wait(&done, 0, a.err, 64, 0);
+    } else {
+        const int half = wid >> 2, r = (wid & 3) * 32 + lane;
+        const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (kF4N / 2));
+        const int cols = SWIGLU ? a.N / 2 : a.N;
+        uint32_t acc = 0;
+        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++acc) {
+            const int rb = int(tile / nt), ct = int(tile - (long long)rb * nt);
+            const int e = group_of_block(t, a.E, rb);
+            const int in = (rb - t.pre[e]) * kGtRows;
+            const bool live = r < t.cnt[e] - in;
+            const float al = a.alpha != nullptr ? __ldg(a.alpha + e) : 1.0f;
+            const size_t row = size_t(t.row[e] + in + r) * cols;
+            const uint32_t buf = acc & 1u;
+            gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kF4N / 64; ++c) {
+                uint32_t u[32];
+                tmem_ld32(tl + buf * kF4N + c * 32, u);
+                tmem_ld_wait();
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = al * __uint_as_float(u[j]);
+                const int c0 = ct * kF4N + half * (kF4N / 2) + c * 32;
+                if (SWIGLU) {
+                    float h[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) h[j] = silu_mul(v[2 * j], v[2 * j + 1]);
+                    if (live)
+                        gt_store<F32, 16>(a.out, row + c0 / 2, h, cols - c0 / 2, vec,
+                                          a.out_dtype == STRATA_BF16);
+                } else if (live) {
+                    gt_store<F32, 32>(a.out, row + c0, v, cols - c0, vec,
+                                      a.out_dtype == STRATA_BF16);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (wid == kGtMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int FMT, bool F32, bool SWIGLU>
+cudaError_t f4_run(const Fp4GmmArgs& g, cudaStream_t s) {
+    F4Maps m;
+    bool ok = gt_map(&m.b, 1, g.wq, g.K / 2, g.N, g.E, kF4N);
+    for (int i = 0; i < kGtRows / kGtBox; ++i)
+        ok = ok && gt_map(&m.a[i], 1, g.xq, g.K / 2, g.M, 0, kGtBox * (i + 1));
+    if (!ok) return cudaErrorInvalidValue;
+    const int vec = gt_vec(g.out, size_t(SWIGLU ? g.N / 2 : g.N) * (F32 ? 4 : 2));
+    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, F4<FMT>::kDyn, s, m, g, vec);
+}
+
+template <int FMT>
+cudaError_t f4_pick(const Fp4GmmArgs& g, cudaStream_t s) {
+    if (g.out_dtype == STRATA_F32)
+        return g.swiglu ? f4_run<FMT, true, true>(g, s) : f4_run<FMT, true, false>(g, s);
+    return g.swiglu ? f4_run<FMT, false, true>(g, s) : f4_run<FMT, false, false>(g, s);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_mm_fp4(const Fp4GmmArgs& g, cudaStream_t s) {
+    return g.fmt == STRATA_FP4_MX ? f4_pick<0>(g, s) : f4_pick<1>(g, s);
+}
+
+}  // namespace strata

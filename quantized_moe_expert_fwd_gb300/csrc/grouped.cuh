@@ -11,8 +11,10 @@
 namespace strata {
 
 // The groups as a CTA sees them: first row, rows, and the exclusive prefix
-// sum of their row blocks (pre[E] = all blocks).  A group whose offsets leave
-// [0, M] or run backwards has no rows (STRATA_EBADROUTE is latched).
+// sum of their row blocks (pre[E] = all blocks).  Offsets that run backwards
+// anywhere or leave [0, M] make every group empty (STRATA_EBADROUTE is
+// latched): the groups of a table are then always disjoint and in order, so
+// their blocks fit the scales' buffers.
 struct GroupTable {
     int row[kMaxExperts];
     int cnt[kMaxExperts];
@@ -25,26 +27,25 @@ struct GroupTable {
 __device__ __forceinline__ void build_groups(GroupTable& t, const int32_t* offsets, int E, int M,
                                              int block_rows, uint32_t* err) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bool bad = false;
+    for (int e = tid; e < E; e += int(blockDim.x)) {
+        int row = e * (M / E), cnt = M / E;
+        if (offsets != nullptr) {
+            row = offsets[e];
+            const int end = offsets[e + 1];
+            bad |= row < 0 || end < row || end > M;
+            cnt = end - row;
+        }
+        t.row[e] = row;
+        t.cnt[e] = cnt;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0) latch(err, STRATA_EBADROUTE);
     int carry = 0;
     for (int base = 0; base < E; base += int(blockDim.x)) {
         const int e = base + tid;
-        int row = 0, cnt = 0;
-        if (e < E) {
-            if (offsets != nullptr) {
-                row = offsets[e];
-                const int end = offsets[e + 1];
-                cnt = end - row;
-                if (row < 0 || end > M || cnt < 0) {
-                    latch(err, STRATA_EBADROUTE);
-                    row = min(max(row, 0), M);
-                    cnt = 0;
-                }
-            } else {
-                cnt = M / E;
-                row = e * cnt;
-            }
-        }
-        const int n = (cnt + block_rows - 1) / block_rows;
+        if (bad && e < E) t.row[e] = t.cnt[e] = 0;
+        const int n = e < E ? (t.cnt[e] + block_rows - 1) / block_rows : 0;
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -58,11 +59,7 @@ __device__ __forceinline__ void build_groups(GroupTable& t, const int32_t* offse
             if (w < warp) before += t.part[w];
             all += t.part[w];
         }
-        if (e < E) {
-            t.row[e] = row;
-            t.cnt[e] = cnt;
-            t.pre[e] = before + incl - n;
-        }
+        if (e < E) t.pre[e] = before + incl - n;
         carry = all;
         __syncthreads();
     }

@@ -61,7 +61,6 @@ struct Fp4GmmArgs {
     const int32_t* offsets;
     uint32_t* err;
     int M, K, N, E, fmt, swiglu;
-    size_t xs_bytes;
 };
 cudaError_t launch_grouped_mm_fp4(const Fp4GmmArgs& g, cudaStream_t s);
 

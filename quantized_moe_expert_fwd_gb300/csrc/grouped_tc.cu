@@ -24,27 +24,16 @@
 // 512 terms into fp32 registers of the epilogue, where it is added with
 // rounding (5e-7 at any length).  16-bit outputs round away far more than
 // that and take the whole reduction in one accumulator.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
-#include "grouped.cuh"
-#include "grouped.h"
-#include "tc.cuh"
+#include "grouped_tc.cuh"
 
 namespace strata {
 
 namespace {
 
-constexpr int kGtThreads = 320;
-constexpr int kGtEpiWarps = 8, kGtTmaWarp = 8, kGtMmaWarp = 9;
-constexpr int kGtRows = 128;                    // tile rows
 constexpr int kGtK = 64;                        // reduction of a stage (128 bytes)
 constexpr int kGtPromote = 8;                   // stages between drains of an fp32 output
 constexpr uint32_t kGtABytes = kGtRows * 128;
 constexpr uint32_t kGtSub = 64 * 128;           // a 64 x 64 MN-major sub-block
-constexpr int kGtBox = 32;                      // row box heights: 32, 64, 96, 128
 
 __host__ __device__ constexpr uint32_t gt_stage_bytes(int BN) { return kGtABytes + uint32_t(BN) * 128u; }
 __host__ __device__ constexpr int gt_stages(int BN) { return int(196608u / gt_stage_bytes(BN)); }
@@ -67,17 +56,6 @@ struct GtTile {
     int e, arow, rows, c0, stages, slot0, cnt;
     size_t orow;
 };
-
-__device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                        uint32_t site, uint32_t slot) {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 255u) == 255u && *reinterpret_cast<const volatile uint32_t*>(err) == 4u)
-            return false;
-    }
-    latch_timeout(err, site, slot, parity, 0);
-    return false;
-}
 
 template <int MODE, int BN>
 __device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a, long long tile) {
@@ -105,60 +83,6 @@ __device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a, 
         i.orow = size_t(i.arow);
     }
     return i;
-}
-
-// 32 consecutive columns of one output row from fp32 values; nv of them
-// exist.  A lane writes whole 32-byte sectors where the row allows it.
-__device__ __forceinline__ void gt_st8(void* p, const uint32_t* w) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-template <int WORDS>
-__device__ __forceinline__ void gt_store_words(uint8_t* p, const uint32_t (&w)[WORDS], int vec) {
-    if (vec == 32) {
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 8) gt_st8(p + i * 4, w + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 4)
-            *reinterpret_cast<uint4*>(p + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-    }
-}
-__device__ __forceinline__ uint32_t gt_pack(float lo, float hi, int bf16) {
-    uint32_t r;
-    if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-template <bool F32>
-__device__ __forceinline__ void gt_store32(void* out, size_t at, const float* v, int nv, int vec,
-                                           int bf16) {
-    if (F32) {
-        float* p = static_cast<float*>(out) + at;
-        if (nv >= 32 && vec) {
-            uint32_t w[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
-            gt_store_words(reinterpret_cast<uint8_t*>(p), w, vec);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < nv) p[j] = v[j];
-        }
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(out) + at;
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = gt_pack(v[2 * j], v[2 * j + 1], bf16);
-        if (nv >= 32 && vec) {
-            gt_store_words(reinterpret_cast<uint8_t*>(p), w, vec);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < nv) p[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
-        }
-    }
 }
 
 template <int MODE, int BN, bool F32>
@@ -331,7 +255,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 if (live) {
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
-                        gt_store32<true>(a.out, at + c * 32, sum[c], cols - c0 - c * 32, a.vec, 0);
+                        gt_store<true, 32>(a.out, at + c * 32, sum[c], cols - c0 - c * 32, a.vec, 0);
                 }
             } else {
                 const uint32_t buf = acc & 1u;
@@ -350,8 +274,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                         for (int j = 0; j < 32; ++j) v[j] = 0u;
                     }
                     if (live)
-                        gt_store32<false>(a.out, at + c * 32, reinterpret_cast<const float*>(v),
-                                          cols - c0 - c * 32, a.vec, a.bf16);
+                        gt_store<false, 32>(a.out, at + c * 32, reinterpret_cast<const float*>(v),
+                                            cols - c0 - c * 32, a.vec, a.bf16);
                 }
                 if (i.stages > 0) {
                     tc_fence_before();
@@ -369,35 +293,6 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 }
 
 // ------------------------------------------------------------------- host
-PFN_cuTensorMapEncodeTiled_v12000 gt_encode_fn() {
-    static std::mutex mu;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (fn == nullptr) {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
-// A row-major array [z][rows][inner] of 16-bit elements with the 128-byte
-// swizzle; boxes of 64 elements by box_rows rows.  z = 0: two dimensions.
-bool gt_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t z,
-            uint32_t box_rows) {
-    auto fn = gt_encode_fn();
-    if (fn == nullptr) return false;
-    const cuuint64_t dim[3] = {inner, rows, z};
-    const cuuint64_t stride[2] = {inner * 2, inner * rows * 2};
-    const cuuint32_t box[3] = {64, box_rows, 1}, one[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, z ? 3 : 2, const_cast<void*>(base), dim, stride,
-              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MODE, int BN, bool F32>
 cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
     GtMaps m;
@@ -407,13 +302,13 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
         // with no rows nothing is loaded; the maps still need an address
         const void* a = g.M > 0 ? g.a : g.out;
         const void* b = g.M > 0 ? g.b : g.out;
-        ok = gt_map(&m.a[0], a, g.N, rows, 0, 64) && gt_map(&m.b, b, g.K, rows, 0, 64);
+        ok = gt_map16(&m.a[0], a, g.N, rows, 0, 64) && gt_map16(&m.b, b, g.K, rows, 0, 64);
         for (int i = 1; i < kGtRows / kGtBox; ++i) m.a[i] = m.a[0];
     } else {
         const int red = MODE == kGmmFwd ? g.K : g.N;
         for (int i = 0; i < kGtRows / kGtBox; ++i)
-            ok = ok && gt_map(&m.a[i], g.a, red, rows, 0, kGtBox * (i + 1));
-        ok = ok && gt_map(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? BN : 64);
+            ok = ok && gt_map16(&m.a[i], g.a, red, rows, 0, kGtBox * (i + 1));
+        ok = ok && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? BN : 64);
     }
     if (!ok) return cudaErrorInvalidValue;
     GtArgs a{};
@@ -426,23 +321,9 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
     a.E = g.E;
     a.bf16 = g.dtype == STRATA_BF16;
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
-    const size_t mis = pitch | reinterpret_cast<uintptr_t>(g.out);
-    a.vec = mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
+    a.vec = gt_vec(g.out, pitch);
     const size_t dyn = size_t(gt_stages(BN)) * gt_stage_bytes(BN) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(k_gmm_tc<MODE, BN, F32>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(device_info().sms);
-    cfg.blockDim = dim3(kGtThreads);
-    cfg.dynamicSmemBytes = dyn;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_gmm_tc<MODE, BN, F32>, m, a);
+    return gt_launch(k_gmm_tc<MODE, BN, F32>, dyn, s, m, a);
 }
 
 template <int MODE>

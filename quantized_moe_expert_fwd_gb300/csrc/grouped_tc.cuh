@@ -1,0 +1,151 @@
+// grouped_tc.cuh -- what the tensor-core kernels of the grouped products
+// share: the CTA's roles, bounded waits, output stores, tensor maps, launch.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "grouped.cuh"
+#include "grouped.h"
+#include "tc.cuh"
+
+namespace strata {
+
+constexpr int kGtThreads = 320;
+constexpr int kGtEpiWarps = 8, kGtTmaWarp = 8, kGtMmaWarp = 9;
+constexpr int kGtRows = 128;                    // tile rows
+constexpr int kGtBox = 32;                      // row box heights: 32, 64, 96, 128
+
+// Bounded wait that gives up early once a timed-out wait has been latched.
+__device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                        uint32_t site, uint32_t slot) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 255u) == 255u && *reinterpret_cast<const volatile uint32_t*>(err) == 4u)
+            return false;
+    }
+    latch_timeout(err, site, slot, parity, 0);
+    return false;
+}
+
+
+// N consecutive columns of one output row from fp32 values; nv of them
+// exist.  A lane writes whole 32-byte sectors where the rows are aligned
+// for it (vec: the bytes that every row is aligned to: 32, 16 or 0).
+__device__ __forceinline__ void gt_st8(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void gt_store_words(uint8_t* p, const uint32_t (&w)[WORDS], int vec) {
+    if (vec == 32) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 8) gt_st8(p + i * 4, w + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4)
+            *reinterpret_cast<uint4*>(p + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+}
+__device__ __forceinline__ uint32_t gt_pack(float lo, float hi, int bf16) {
+    uint32_t r;
+    if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool F32, int N>
+__device__ __forceinline__ void gt_store(void* out, size_t at, const float* v, int nv, int vec,
+                                         int bf16) {
+    if (F32) {
+        float* p = static_cast<float*>(out) + at;
+        if (nv >= N && vec) {
+            uint32_t w[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) w[j] = __float_as_uint(v[j]);
+            gt_store_words(reinterpret_cast<uint8_t*>(p), w, vec);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < nv) p[j] = v[j];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(out) + at;
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) w[j] = gt_pack(v[2 * j], v[2 * j + 1], bf16);
+        if (nv >= N && vec) {
+            gt_store_words(reinterpret_cast<uint8_t*>(p), w, vec);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < nv) p[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+}
+
+// ------------------------------------------------------------------- host
+inline PFN_cuTensorMapEncodeTiled_v12000 gt_encode_fn() {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (fn == nullptr) {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+
+// A row-major array [z][rows][inner bytes] with the 128-byte swizzle; boxes
+// of 128 bytes by box_rows rows.  z = 0: two dimensions.  esize: bytes of an
+// element (1 or 2), the unit of the inner coordinate.
+inline bool gt_map(CUtensorMap* m, int esize, const void* base, uint64_t inner, uint64_t rows,
+                   uint64_t z, uint32_t box_rows) {
+    auto fn = gt_encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dim[3] = {inner / esize, rows, z};
+    const cuuint64_t stride[2] = {inner, inner * rows};
+    const cuuint32_t box[3] = {cuuint32_t(128 / esize), box_rows, 1}, one[3] = {1, 1, 1};
+    return fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+              z ? 3 : 2, const_cast<void*>(base), dim, stride, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool gt_map16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t z,
+                     uint32_t box_rows) {
+    return gt_map(m, 2, base, inner * 2, rows, z, box_rows);
+}
+
+inline int gt_vec(const void* out, size_t pitch) {
+    const size_t mis = pitch | reinterpret_cast<uintptr_t>(out);
+    return mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
+}
+
+// One CTA per SM, after the grids before it (programmatic dependent launch:
+// the kernel's prologue overlaps their tail).
+template <typename... P, typename... A>
+cudaError_t gt_launch(void (*kernel)(P...), size_t dyn, cudaStream_t s, const A&... args) {
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(device_info().sms);
+    cfg.blockDim = dim3(kGtThreads);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace strata

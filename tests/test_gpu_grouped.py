@@ -169,27 +169,23 @@ def test_gradients_against_differences(name):
     _done(ws)
 
 
-@pytest.mark.parametrize("bad", [[0, 5, 3, 9], [-1, 4, 6, 9], [0, 4, 9, 10], [9, 6, 4, 0]], ids=str)
+@pytest.mark.parametrize("bad", [[0, 5, 3, 9], [-1, 4, 6, 9], [0, 4, 9, 10], [9, 6, 4, 0],
+                                 [0, 9, 0, 9]], ids=str)
 def test_bad_offsets_are_reported_and_harmless(bad):
-    """Backward or outside offsets: their groups are skipped, the others computed."""
+    """Backward or outside offsets: the call is reported and treats every group as empty."""
     x = torch.randn(9, 64, device="cuda").bfloat16()
     w = torch.randn(3, 32, 64, device="cuda").bfloat16()
     off, ws = torch.tensor(bad, dtype=torch.int32, device="cuda"), q.make_grouped_workspace()
     y = torch.full((9, 32), 7.0, device="cuda")
+    dx = torch.full((9, 64), 7.0, device="cuda")
     dw = torch.full((3, 32, 64), 7.0, device="cuda")
     for call in (lambda: q.moe_grouped_mm(x, w, off, y, ws),
-                 lambda: q.moe_grouped_mm_dx(y.bfloat16(), w, off, torch.zeros(9, 64, device="cuda"), ws),
+                 lambda: q.moe_grouped_mm_dx(y.bfloat16(), w, off, dx, ws),
                  lambda: q.moe_grouped_mm_dw(y.bfloat16(), x, off, dw, ws)):
         call()
         assert q.moe_get_device_status(ws) == q.STRATA_EBADROUTE
         assert q.moe_get_device_status(ws) == q.STRATA_OK
-    good = [e for e in range(3) if 0 <= bad[e] <= bad[e + 1] <= 9]
-    for e in range(3):
-        if e not in good:
-            assert (dw[e] == 0).all()
-    if bad == [0, 4, 9, 10]:
-        want, mags = ref.mm(x, w[:2], torch.tensor(bad[:3]))
-        ref.check(y, want, mags, 64)
+    assert (y == 7).all() and (dx == 7).all() and (dw == 0).all()
 
 
 def test_graph_replays_follow_the_offsets():
