@@ -429,9 +429,10 @@ def _grouped(ws, stream, *tensors):
             raise ValueError("tensors passed to strata_moe must be contiguous")
     if not ws.is_contiguous() or ws.dtype != torch.uint8:
         raise ValueError("the workspace must be a contiguous uint8 tensor")
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream, ws.numel()
+    # the raw handle: a decode call's host time is a good part of its whole,
+    # and building torch's Stream object alone takes 5 us
+    st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    return st, ws.numel()
 
 
 def _dtype(t, what, *allowed):
