@@ -20,6 +20,8 @@ namespace strata {
 
 namespace {
 
+constexpr int kF4Threads = kGtThreads + 32;     // a warp more: the scales' copies
+constexpr int kF4SfWarp = 10;
 constexpr int kF4N = 128;                       // tile columns
 constexpr int kF4K = 256;                       // K of a stage
 constexpr uint32_t kF4Data = 128 * 128;         // one operand's packed rows of a stage
@@ -31,9 +33,10 @@ struct F4 {
     static constexpr uint32_t kStage = 2 * kF4Data + 2 * kSf;
     static constexpr int kStages = 5;
     static constexpr size_t kDyn = size_t(kStages) * kStage + 1024;
-    // tensor memory: two accumulators, two buffers of both operands' scales
+    // tensor memory: two accumulators, both operands' scales of every stage
     static constexpr uint32_t kSfCol = 2 * kF4N;
-    static constexpr uint32_t kSfCols = kWords * 4;            // one operand's
+    static constexpr uint32_t kSfCols = kWords * 4;            // one operand's, a stage
+    static_assert(kSfCol + kStages * 2 * kSfCols <= 512, "TMEM columns");
 };
 
 struct F4Maps {
@@ -77,14 +80,23 @@ __device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t smem) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
+// 16-bit outputs take the fast exponential and quotient (relative error near
+// 1e-6, next to a rounding of 2^-9 or 2^-12).
+template <bool F32>
+__device__ __forceinline__ float f4_swiglu(float g, float u) {
+    return F32 ? silu_mul(g, u) : __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
 template <int FMT, bool F32, bool SWIGLU>
-__global__ void __launch_bounds__(kGtThreads, 1)
+__global__ void __launch_bounds__(kF4Threads, 1)
     k_gmm_f4(const __grid_constant__ F4Maps maps, Fp4GmmArgs a, int vec) {
     using C = F4<FMT>;
     extern __shared__ uint8_t f4_dyn[];
     __shared__ GroupTable t;
-    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2],
-        done;
+    // full: a stage's copies landed; sf_full: its scales are in tensor memory
+    // too; empty: its products are done (shared memory and scales free again)
+    __shared__ __align__(8) uint64_t full[C::kStages], sf_full[C::kStages], empty[C::kStages];
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done;
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(f4_dyn) + 1023) &
@@ -94,6 +106,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&full[i], 1);
+            mbar_init(&sf_full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -117,13 +130,14 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     const uint32_t tmem = tmem_base;
     const int nt = (a.N + kF4N - 1) / kF4N, words = fp4_words(a.K, FMT);
     const int stages = (a.K + kF4K - 1) / kF4K;
-    const long long tiles = (long long)t.pre[a.E] * nt;
+    const int blocks = t.pre[a.E];
+    const GtIter<false> first_tile(nt, 0);
 
     if (wid == kGtTmaWarp) {
         if (lane == 0) {
             uint32_t st = 0;
-            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-                const int rb = int(tile / nt), ct = int(tile - (long long)rb * nt);
+            for (auto it = first_tile; it.m < blocks; it.next()) {
+                const int rb = it.m, ct = it.c;
                 const int e = group_of_block(t, a.E, rb);
                 const int in = (rb - t.pre[e]) * kGtRows, arow = t.row[e] + in;
                 const int nbox = (min(kGtRows, t.cnt[e] - in) + kGtBox - 1) / kGtBox;
@@ -149,29 +163,44 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             for (uint32_t k = st > C::kStages ? st - C::kStages : 0; k < st; ++k)
                 gt_wait(&full[k % C::kStages], (k / C::kStages) & 1, a.err, 61, k % C::kStages);
         }
-    } else if (wid == kGtMmaWarp) {
-        uint32_t st = 0, acc = 0;
-        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++acc) {
-            const uint32_t buf = acc & 1u;
-            if (acc >= 2) gt_wait(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 62, buf);
-            for (int ks = 0; ks < stages; ++ks, ++st) {
-                const uint32_t s = st % C::kStages;
-                gt_wait(&full[s], (st / C::kStages) & 1, a.err, 63, s);
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t sa = smem_u32(base + s * (2 * kF4Data));
+    } else if (wid == kF4SfWarp) {
+        // the scales of each stage to tensor memory, on a thread of their own:
+        // a copy takes about as long to issue as a product
+        if (lane == 0) {
+            uint32_t st = 0;
+            for (auto it = first_tile; it.m < blocks; it.next()) {
+                for (int ks = 0; ks < stages; ++ks, ++st) {
+                    const uint32_t s = st % C::kStages;
+                    gt_wait(&full[s], (st / C::kStages) & 1, a.err, 66, s);
+                    tc_fence_after();
                     const uint32_t sf = smem_u32(sf_base + s * (2 * C::kSf));
-                    const uint32_t ca = tmem + C::kSfCol + (st & 1u) * (2 * C::kSfCols);
-                    const uint32_t cb = ca + C::kSfCols;
-                    // K steps that exist: past K the scales are not loaded
-                    const int steps = min(4, (a.K - ks * kF4K + 63) / 64);
-                    const int nw = FMT == 0 ? (steps + 1) / 2 : steps;
+                    const uint32_t ca = tmem + C::kSfCol + s * (2 * C::kSfCols);
+                    const int nw = min(C::kWords, words - ks * C::kWords);
 #pragma unroll
                     for (int w = 0; w < C::kWords; ++w)
                         if (w < nw) {
                             sf_copy(ca + 4 * w, sf + w * 512);
-                            sf_copy(cb + 4 * w, sf + C::kSf + w * 512);
+                            sf_copy(ca + C::kSfCols + 4 * w, sf + C::kSf + w * 512);
                         }
+                    umma_commit(&sf_full[s]);
+                }
+            }
+        }
+    } else if (wid == kGtMmaWarp) {
+        uint32_t st = 0, acc = 0;
+        for (auto it = first_tile; it.m < blocks; it.next(), ++acc) {
+            const uint32_t buf = acc & 1u;
+            if (acc >= 2) gt_wait(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 62, buf);
+            for (int ks = 0; ks < stages; ++ks, ++st) {
+                const uint32_t s = st % C::kStages;
+                gt_wait(&sf_full[s], (st / C::kStages) & 1, a.err, 63, s);
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t sa = smem_u32(base + s * (2 * kF4Data));
+                    const uint32_t ca = tmem + C::kSfCol + s * (2 * C::kSfCols);
+                    const uint32_t cb = ca + C::kSfCols;
+                    // K steps that exist: past K the scales are not loaded
+                    const int steps = min(4, (a.K - ks * kF4K + 63) / 64);
                     const uint64_t da = sdesc_k_sw128(sa), db = sdesc_k_sw128(sa + kF4Data);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -191,13 +220,13 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         if (lane == 0) umma_commit(&done);
         __syncwarp();
         gt_wait(&done, 0, a.err, 64, 0);
-    } else {
+    } else if (wid < kGtEpiWarps) {
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (kF4N / 2));
         const int cols = SWIGLU ? a.N / 2 : a.N;
         uint32_t acc = 0;
-        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++acc) {
-            const int rb = int(tile / nt), ct = int(tile - (long long)rb * nt);
+        for (auto it = first_tile; it.m < blocks; it.next(), ++acc) {
+            const int rb = it.m, ct = it.c;
             const int e = group_of_block(t, a.E, rb);
             const int in = (rb - t.pre[e]) * kGtRows;
             const bool live = r < t.cnt[e] - in;
@@ -206,6 +235,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             const uint32_t buf = acc & 1u;
             gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
             tc_fence_after();
+            // warps whose rows all lie behind the group's end have nothing to do
+            if (r - lane < t.cnt[e] - in)
 #pragma unroll
             for (int c = 0; c < kF4N / 64; ++c) {
                 uint32_t u[32];
@@ -213,12 +244,12 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 tmem_ld_wait();
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = al * __uint_as_float(u[j]);
+                for (int j = 0; j < 32; ++j) v[j] = live ? al * __uint_as_float(u[j]) : 0.0f;
                 const int c0 = ct * kF4N + half * (kF4N / 2) + c * 32;
                 if (SWIGLU) {
                     float h[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) h[j] = silu_mul(v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) h[j] = f4_swiglu<F32>(v[2 * j], v[2 * j + 1]);
                     if (live)
                         gt_store<F32, 16>(a.out, row + c0 / 2, h, cols - c0 / 2, vec,
                                           a.out_dtype == STRATA_BF16);
@@ -246,7 +277,7 @@ cudaError_t f4_run(const Fp4GmmArgs& g, cudaStream_t s) {
         ok = ok && gt_map(&m.a[i], 1, g.xq, g.K / 2, g.M, 0, kGtBox * (i + 1));
     if (!ok) return cudaErrorInvalidValue;
     const int vec = gt_vec(g.out, size_t(SWIGLU ? g.N / 2 : g.N) * (F32 ? 4 : 2));
-    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, F4<FMT>::kDyn, s, m, g, vec);
+    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, kF4Threads, F4<FMT>::kDyn, s, m, g, vec);
 }
 
 template <int FMT>

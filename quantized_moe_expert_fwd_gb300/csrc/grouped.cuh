@@ -15,11 +15,14 @@ namespace strata {
 // anywhere or leave [0, M] make every group empty (STRATA_EBADROUTE is
 // latched): the groups of a table are then always disjoint and in order, so
 // their blocks fit the scales' buffers.
+// of[b]: the group of row block b, for the first kBlockMap blocks.
+constexpr int kBlockMap = 2048;
 struct GroupTable {
     int row[kMaxExperts];
     int cnt[kMaxExperts];
     int pre[kMaxExperts + 1];
     int part[32];
+    uint16_t of[kBlockMap];
 };
 
 // Built by all threads of the CTA (a multiple of 32, at most 1024); ends
@@ -59,7 +62,9 @@ __device__ __forceinline__ void build_groups(GroupTable& t, const int32_t* offse
             if (w < warp) before += t.part[w];
             all += t.part[w];
         }
-        if (e < E) t.pre[e] = before + incl - n;
+        const int first = before + incl - n;
+        if (e < E) t.pre[e] = first;
+        for (int b = first; b < min(first + n, kBlockMap); ++b) t.of[b] = uint16_t(e);
         carry = all;
         __syncthreads();
     }
@@ -67,26 +72,16 @@ __device__ __forceinline__ void build_groups(GroupTable& t, const int32_t* offse
     __syncthreads();
 }
 
-// The group that holds row block b (b < pre[E]): the last e with pre[e] <= b
-// that is not empty.
+// The group that holds row block b (b < pre[E]): from the map, or past it the
+// last e with pre[e] <= b, which is not empty.
 __device__ __forceinline__ int group_of_block(const GroupTable& t, int E, int b) {
+    if (b < kBlockMap) return t.of[b];
     int lo = 0, hi = E;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (t.pre[mid] <= b) lo = mid; else hi = mid;
     }
     return lo;
-}
-
-// The group that holds row r, or -1: the last one whose first row is not
-// behind r (empty groups share their first row with the group after them).
-__device__ __forceinline__ int group_of_row(const GroupTable& t, int E, int r) {
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.row[mid] <= r) lo = mid; else hi = mid;
-    }
-    return (r >= t.row[lo] && r < t.row[lo] + t.cnt[lo]) ? lo : -1;
 }
 
 template <typename T>

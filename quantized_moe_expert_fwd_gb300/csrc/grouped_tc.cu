@@ -58,24 +58,21 @@ struct GtTile {
 };
 
 template <int MODE, int BN>
-__device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a, long long tile) {
-    const int cols = MODE == kGmmFwd ? a.N : a.K;
-    const int nt = (cols + BN - 1) / BN;
+__device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a,
+                                          const GtIter<MODE == kGmmDw>& it) {
     GtTile i;
-    const int rb = int(tile / nt);
-    i.c0 = int(tile - (long long)rb * nt) * BN;
+    i.c0 = it.c * BN;
     if (MODE == kGmmDw) {
-        const int mt = (a.N + kGtRows - 1) / kGtRows;
-        i.e = rb / mt;
-        i.arow = (rb - i.e * mt) * kGtRows;
+        i.e = it.e;
+        i.arow = it.m * kGtRows;
         i.rows = min(kGtRows, a.N - i.arow);
         i.slot0 = t.row[i.e];
         i.cnt = t.cnt[i.e];
         i.stages = (i.cnt + kGtK - 1) / kGtK;
         i.orow = size_t(i.e) * a.N + i.arow;
     } else {
-        i.e = group_of_block(t, a.E, rb);
-        const int in = (rb - t.pre[i.e]) * kGtRows;
+        i.e = group_of_block(t, a.E, it.m);
+        const int in = (it.m - t.pre[i.e]) * kGtRows;
         i.arow = t.row[i.e] + in;
         i.rows = min(kGtRows, t.cnt[i.e] - in);
         i.slot0 = i.cnt = 0;
@@ -122,15 +119,17 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     build_groups(t, a.offsets, a.E, a.M, kGtRows, a.err);
     const uint32_t tmem = tmem_base;
     const int cols = MODE == kGmmFwd ? a.N : a.K;
-    const long long nt = (cols + BN - 1) / BN;
-    const long long tiles =
-        nt * (MODE == kGmmDw ? (long long)a.E * ((a.N + kGtRows - 1) / kGtRows) : t.pre[a.E]);
+    const GtIter<MODE == kGmmDw> first_tile((cols + BN - 1) / BN, (a.N + kGtRows - 1) / kGtRows);
+    const int blocks = t.pre[a.E];
+    auto more = [&](const GtIter<MODE == kGmmDw>& it) {
+        return MODE == kGmmDw ? it.e < a.E : it.m < blocks;
+    };
 
     if (wid == kGtTmaWarp) {
         if (lane == 0) {
             uint32_t st = 0;
-            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-                const GtTile i = gt_tile<MODE, BN>(t, a, tile);
+            for (auto it = first_tile; more(it); it.next()) {
+                const GtTile i = gt_tile<MODE, BN>(t, a, it);
                 const int nbox = (i.rows + kGtBox - 1) / kGtBox;
                 const CUtensorMap* ma = &maps.a[MODE == kGmmDw ? 0 : nbox - 1];
                 const uint32_t bytes =
@@ -171,8 +170,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         constexpr uint32_t a_step = MODE == kGmmDw ? 2048 / 16 : 2;
         constexpr uint32_t b_step = MODE != kGmmFwd ? 2048 / 16 : 2;
         uint32_t st = 0, acc = 0;
-        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const GtTile i = gt_tile<MODE, BN>(t, a, tile);
+        for (auto it = first_tile; more(it); it.next()) {
+            const GtTile i = gt_tile<MODE, BN>(t, a, it);
             for (int ks = 0; ks < i.stages; ++ks, ++st) {
                 const uint32_t s = st % STAGES;
                 const bool first = F32 ? ks % kGtPromote == 0 : ks == 0;
@@ -225,8 +224,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (BN / 2));
         uint32_t acc = 0;
-        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const GtTile i = gt_tile<MODE, BN>(t, a, tile);
+        for (auto it = first_tile; more(it); it.next()) {
+            const GtTile i = gt_tile<MODE, BN>(t, a, it);
             const int c0 = i.c0 + half * (BN / 2);
             const size_t at = (i.orow + r) * size_t(cols) + c0;
             const bool live = r < i.rows;
@@ -323,7 +322,7 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
     a.vec = gt_vec(g.out, pitch);
     const size_t dyn = size_t(gt_stages(BN)) * gt_stage_bytes(BN) + 1024;
-    return gt_launch(k_gmm_tc<MODE, BN, F32>, dyn, s, m, a);
+    return gt_launch(k_gmm_tc<MODE, BN, F32>, kGtThreads, dyn, s, m, a);
 }
 
 template <int MODE>

@@ -31,6 +31,42 @@ __device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t
 }
 
 
+// A CTA's tiles in order: column tile c (of nt) fastest, then row block m, and
+// with MT row blocks an expert (dw) the expert e.  Steps of gridDim.x tiles
+// are added digit by digit: a 64-bit division a tile took longer than the
+// tile's first copies.
+template <bool EXPERTS>
+struct GtIter {
+    int c, m, e, nt, mt, dc, dm, de;
+    __device__ __forceinline__ GtIter(int nt_, int mt_) : e(0), nt(nt_), mt(mt_), de(0) {
+        c = int(blockIdx.x) % nt;
+        m = int(blockIdx.x) / nt;
+        dc = int(gridDim.x) % nt;
+        dm = int(gridDim.x) / nt;
+        if (EXPERTS) {
+            e = m / mt;
+            m %= mt;
+            de = dm / mt;
+            dm %= mt;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        c += dc;
+        m += dm;
+        if (c >= nt) {
+            c -= nt;
+            ++m;
+        }
+        if (EXPERTS) {
+            e += de;
+            if (m >= mt) {
+                m -= mt;
+                ++e;
+            }
+        }
+    }
+};
+
 // N consecutive columns of one output row from fp32 values; nv of them
 // exist.  A lane writes whole 32-byte sectors where the rows are aligned
 // for it (vec: the bytes that every row is aligned to: 32, 16 or 0).
@@ -131,13 +167,14 @@ inline int gt_vec(const void* out, size_t pitch) {
 // One CTA per SM, after the grids before it (programmatic dependent launch:
 // the kernel's prologue overlaps their tail).
 template <typename... P, typename... A>
-cudaError_t gt_launch(void (*kernel)(P...), size_t dyn, cudaStream_t s, const A&... args) {
+cudaError_t gt_launch(void (*kernel)(P...), int threads, size_t dyn, cudaStream_t s,
+                      const A&... args) {
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(device_info().sms);
-    cfg.blockDim = dim3(kGtThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = dyn;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
