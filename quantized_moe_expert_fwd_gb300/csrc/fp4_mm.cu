@@ -20,8 +20,8 @@ namespace strata {
 
 namespace {
 
-constexpr int kF4Threads = kGtThreads + 32;     // a warp more: the scales' copies
-constexpr int kF4SfWarp = 10;
+constexpr int kF4Threads = kGtThreads + 64;     // two warps more: the scales' copies
+constexpr int kF4SfWarp = 10;                   // warp 10: A's, 11: B's
 constexpr int kF4N = 128;                       // tile columns
 constexpr int kF4K = 256;                       // K of a stage
 constexpr uint32_t kF4Data = 128 * 128;         // one operand's packed rows of a stage
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&sf_full[i], 1);
+            mbar_init(&sf_full[i], 2);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -163,25 +163,23 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             for (uint32_t k = st > C::kStages ? st - C::kStages : 0; k < st; ++k)
                 gt_wait(&full[k % C::kStages], (k / C::kStages) & 1, a.err, 61, k % C::kStages);
         }
-    } else if (wid == kF4SfWarp) {
-        // the scales of each stage to tensor memory, on a thread of their own:
-        // a copy takes about as long to issue as a product
+    } else if (wid >= kF4SfWarp) {
+        // one operand's scales of each stage to tensor memory, on a thread of
+        // their own: a copy takes about as long to issue as a product
         if (lane == 0) {
+            const int op = wid - kF4SfWarp;
             uint32_t st = 0;
             for (auto it = first_tile; it.m < blocks; it.next()) {
                 for (int ks = 0; ks < stages; ++ks, ++st) {
                     const uint32_t s = st % C::kStages;
-                    gt_wait(&full[s], (st / C::kStages) & 1, a.err, 66, s);
+                    gt_wait(&full[s], (st / C::kStages) & 1, a.err, 66 + op, s);
                     tc_fence_after();
-                    const uint32_t sf = smem_u32(sf_base + s * (2 * C::kSf));
-                    const uint32_t ca = tmem + C::kSfCol + s * (2 * C::kSfCols);
+                    const uint32_t sf = smem_u32(sf_base + s * (2 * C::kSf) + op * C::kSf);
+                    const uint32_t col = tmem + C::kSfCol + (2 * s + op) * C::kSfCols;
                     const int nw = min(C::kWords, words - ks * C::kWords);
 #pragma unroll
                     for (int w = 0; w < C::kWords; ++w)
-                        if (w < nw) {
-                            sf_copy(ca + 4 * w, sf + w * 512);
-                            sf_copy(ca + C::kSfCols + 4 * w, sf + C::kSf + w * 512);
-                        }
+                        if (w < nw) sf_copy(col + 4 * w, sf + w * 512);
                     umma_commit(&sf_full[s]);
                 }
             }
