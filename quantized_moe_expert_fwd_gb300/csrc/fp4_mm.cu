@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     __shared__ __align__(8) uint64_t full[C::kStages], sf_full[C::kStages], empty[C::kStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done;
     __shared__ uint32_t tmem_base;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(f4_dyn) + 1023) &
                                                ~uintptr_t(1023));
     // a stage: A rows, B rows (1024-byte aligned); the scales of all stages behind
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     const GtIter<false> first_tile(nt, 0);
 
     if (wid == kGtTmaWarp) {
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t st = 0;
             for (auto it = first_tile; it.m < blocks; it.next()) {
                 const int rb = it.m, ct = it.c;
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     } else if (wid >= kF4SfWarp) {
         // one operand's scales of each stage to tensor memory, on a thread of
         // their own: a copy takes about as long to issue as a product
-        if (lane == 0) {
+        if (elect_one()) {
             const int op = wid - kF4SfWarp;
             uint32_t st = 0;
             for (auto it = first_tile; it.m < blocks; it.next()) {
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                 const uint32_t s = st % C::kStages;
                 gt_wait(&sf_full[s], (st / C::kStages) & 1, a.err, 63, s);
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t sa = smem_u32(base + s * (2 * kF4Data));
                     const uint32_t ca = tmem + C::kSfCol + s * (2 * C::kSfCols);
                     const uint32_t cb = ca + C::kSfCols;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             }
         }
         // no product may still be writing the TMEM when it is freed
-        if (lane == 0) umma_commit(&done);
+        if (elect_one()) umma_commit(&done);
         __syncwarp();
         gt_wait(&done, 0, a.err, 64, 0);
     } else if (wid < kGtEpiWarps) {

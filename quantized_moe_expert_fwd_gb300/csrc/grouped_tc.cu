@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     __shared__ GroupTable t;
     __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], done;
     __shared__ uint32_t tmem_base;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gt_dyn) + 1023) &
                                                ~uintptr_t(1023));
     if (tid == 0) {
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     };
 
     if (wid == kGtTmaWarp) {
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t st = 0;
             for (auto it = first_tile; more(it); it.next()) {
                 const GtTile i = gt_tile<MODE, BN>(t, a, it);
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     }
                 }
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint64_t da = MODE == kGmmDw ? sdesc_mn_sw128(smem_u32(sa), kGtSub)
                                                        : sdesc_k_sw128(smem_u32(sa));
                     const uint64_t db = MODE != kGmmFwd ? sdesc_mn_sw128(smem_u32(sb), kGtSub)
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             }
         }
         // no product may still be writing the TMEM when it is freed
-        if (lane == 0) umma_commit(&done);
+        if (elect_one()) umma_commit(&done);
         __syncwarp();
         gt_wait(&done, 0, a.err, 54, 0);
     } else {
