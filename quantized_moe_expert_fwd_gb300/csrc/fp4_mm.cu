@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch();
     pdl_wait();
     build_groups(t, a.offsets, a.E, a.M, kGtRows, a.err);
     const uint32_t tmem = tmem_base;

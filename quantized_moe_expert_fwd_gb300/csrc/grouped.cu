@@ -115,6 +115,7 @@ cudaError_t pick_simt(const GmmArgs& g, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_grouped_mm(GroupedMode mode, const GmmArgs& g, cudaStream_t s) {
+    if (mode == kGmmFwd && g.K % 8 == 0 && g.M <= kFewRowsMax) return launch_grouped_few(g, s);
     if (grouped_tc_takes(mode, g)) return launch_grouped_tc(mode, g, s);
     switch (mode) {
         case kGmmFwd: return pick_simt<kGmmFwd>(g, s);

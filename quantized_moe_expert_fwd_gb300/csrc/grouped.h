@@ -28,6 +28,9 @@ struct GmmArgs {
 cudaError_t launch_grouped_mm(GroupedMode mode, const GmmArgs& g, cudaStream_t s);
 // The tensor-core kernels, and whether they take this shape.
 bool grouped_tc_takes(GroupedMode mode, const GmmArgs& g);
+// The forward product of at most kFewRowsMax rows on the CUDA cores.
+constexpr int kFewRowsMax = 8;
+cudaError_t launch_grouped_few(const GmmArgs& g, cudaStream_t s);
 cudaError_t launch_grouped_tc(GroupedMode mode, const GmmArgs& g, cudaStream_t s);
 
 // Scales of `rows` rows by `cols` columns in `groups` groups, in bytes:
