@@ -401,6 +401,7 @@ def moe_layer_bucketing(dims, T: int, ws, counts, offsets, perm, inv, stream=Non
 
 # ------------------------------------- products grouped by expert, 4-bit blocks
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_DTYPES16 = {torch.bfloat16: 0, torch.float16: 1}
 FP4_MX, FP4_NV = 0, 1
 
 
@@ -413,81 +414,88 @@ def moe_grouped_workspace_bytes() -> int:
     return int(load().moe_grouped_workspace_bytes())
 
 
+# A decode call's host time is a good part of its whole, so the checks below
+# compare integers and sizes directly and format nothing unless they refuse.
 def _grouped(ws, stream, *tensors):
     """Checks that the tensors are the binding's to pass on (the library sees
     pointers only): contiguous, on one CUDA device, the current one.  Returns
     the stream handle and the workspace's size."""
-    dev = ws.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+    dev = ws.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("the workspace must be on the current CUDA device")
     for t in tensors:
-        if t is None:
-            continue
-        if t.device != dev:
-            raise ValueError("tensors must be on the workspace's device")
-        if not t.is_contiguous():
-            raise ValueError("tensors passed to strata_moe must be contiguous")
-    if not ws.is_contiguous() or ws.dtype != torch.uint8:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("tensors must be on the workspace's device" if t.get_device() != dev
+                             else "tensors passed to strata_moe must be contiguous")
+    if ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("the workspace must be a contiguous uint8 tensor")
-    # the raw handle: a decode call's host time is a good part of its whole,
-    # and building torch's Stream object alone takes 5 us
-    st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    # the raw handle: building torch's Stream object alone takes 5 us
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     return st, ws.numel()
 
 
-def _dtype(t, what, *allowed):
-    if t.dtype not in allowed:
+def _dtype(t, what, allowed=_DTYPES):
+    d = allowed.get(t.dtype)
+    if d is None:
         raise TypeError(f"{what} must be one of {', '.join(map(str, allowed))}, not {t.dtype}")
-    return _DTYPES.get(t.dtype)
+    return d
 
 
 def _offsets(offsets, groups=None):
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2:
+    n = offsets.numel() - 1
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or n < 1:
         raise ValueError("offsets must be an int32 vector of groups + 1 entries")
-    if groups is not None and offsets.numel() != groups + 1:
-        raise ValueError(f"offsets must have {groups + 1} entries, not {offsets.numel()}")
-    return offsets.numel() - 1
+    if groups is not None and n != groups:
+        raise ValueError(f"offsets must have {groups + 1} entries, not {n + 1}")
+    return n
 
 
 def _shape(t, shape, what):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _grouped_mm(fn, a, b, offsets, out, ws, stream, M, K, N, E):
     st, n = _grouped(ws, stream, a, b, offsets, out)
-    dt = _dtype(a, "the operands", torch.bfloat16, torch.float16)
-    _dtype(b, "the second operand", a.dtype)
-    od = _dtype(out, "the output", a.dtype, torch.float32)
+    dt = _dtype(a, "the operands", _DTYPES16)
+    if b.dtype != a.dtype:
+        raise TypeError(f"the operands must have one type, not {a.dtype} and {b.dtype}")
+    od = _dtype(out, "the output")
+    if od != dt and od != 2:
+        raise TypeError(f"the output must be {a.dtype} or fp32, not {out.dtype}")
     _offsets(offsets, E)
-    _check(fn, getattr(load(), fn)(dt, a.data_ptr(), b.data_ptr(), M, K, N, E,
-                                   offsets.data_ptr(), od, out.data_ptr(), ws.data_ptr(), n, st))
+    _check(fn, getattr(_lib or load(), fn)(dt, a.data_ptr(), b.data_ptr(), M, K, N, E,
+                                           offsets.data_ptr(), od, out.data_ptr(), ws.data_ptr(),
+                                           n, st))
 
 
 def moe_grouped_mm(x, w, offsets, y, ws, stream=None):
     """y[s] = w[e] x[s] for the rows s of each group e (x [M][K], w [E][N][K],
     offsets int32 [E + 1], y [M][N] in x's type or fp32)."""
     E, N, K = w.shape
-    _shape(x, (x.shape[0], K), "x")
-    _shape(y, (x.shape[0], N), "y")
-    _grouped_mm("moe_grouped_mm", x, w, offsets, y, ws, stream, x.shape[0], K, N, E)
+    M = x.shape[0]
+    _shape(x, (M, K), "x")
+    _shape(y, (M, N), "y")
+    _grouped_mm("moe_grouped_mm", x, w, offsets, y, ws, stream, M, K, N, E)
 
 
 def moe_grouped_mm_dx(dy, w, offsets, dx, ws, stream=None):
     """dx[s] = w[e]^T dy[s]: moe_grouped_mm's gradient by x."""
     E, N, K = w.shape
-    _shape(dy, (dy.shape[0], N), "dy")
-    _shape(dx, (dy.shape[0], K), "dx")
-    _grouped_mm("moe_grouped_mm_dx", dy, w, offsets, dx, ws, stream, dy.shape[0], K, N, E)
+    M = dy.shape[0]
+    _shape(dy, (M, N), "dy")
+    _shape(dx, (M, K), "dx")
+    _grouped_mm("moe_grouped_mm_dx", dy, w, offsets, dx, ws, stream, M, K, N, E)
 
 
 def moe_grouped_mm_dw(dy, x, offsets, dw, ws, stream=None):
     """dw[e] = sum over e's rows s of dy[s] x[s]^T: moe_grouped_mm's gradient
     by w (every expert written, zeros for an empty group)."""
     E, N, K = dw.shape
-    _shape(dy, (dy.shape[0], N), "dy")
-    _shape(x, (dy.shape[0], K), "x")
-    _grouped_mm("moe_grouped_mm_dw", dy, x, offsets, dw, ws, stream, dy.shape[0], K, N, E)
+    M = dy.shape[0]
+    _shape(dy, (M, N), "dy")
+    _shape(x, (M, K), "x")
+    _grouped_mm("moe_grouped_mm_dw", dy, x, offsets, dw, ws, stream, M, K, N, E)
 
 
 def moe_fp4_scale_bytes(fmt: int, rows: int, cols: int, n_groups: int = 1,
@@ -496,11 +504,9 @@ def moe_fp4_scale_bytes(fmt: int, rows: int, cols: int, n_groups: int = 1,
                                           1 if ragged else 0))
 
 
-def _fp4_rows(q, scales, offsets, n_groups, cols):
+def _fp4_codes(q, scales):
     if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError("codes and scales must be uint8")
-    _shape(q, (q.shape[0], cols // 2), "the codes")
-    return int(n_groups) if offsets is None else _offsets(offsets)
 
 
 def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1,
@@ -510,31 +516,39 @@ def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1
     perm[s] / top_k where perm (int32) is given, which may be shorter than q
     when offsets end with it."""
     st, n = _grouped(ws, stream, x, q, scales, offsets, perm)
-    dt = _dtype(x, "x", torch.bfloat16, torch.float16, torch.float32)
-    groups = _fp4_rows(q, scales, offsets, n_groups, x.shape[1])
-    rows = q.shape[0]
+    dt = _dtype(x, "x")
+    _fp4_codes(q, scales)
+    R, C = x.shape
+    rows, half = q.shape
+    if 2 * half != C:
+        raise ValueError(f"q must have shape {(rows, C // 2)}, not {tuple(q.shape)}")
+    if offsets is not None:
+        n_groups = _offsets(offsets)
+        offsets = offsets.data_ptr()
     if perm is not None:
         if perm.dtype != torch.int32 or perm.dim() != 1 or perm.numel() > rows:
             raise ValueError("perm must be an int32 vector of at most q's rows")
         rows = perm.numel()
-    _check("moe_fp4_quantize", load().moe_fp4_quantize(
-        int(fmt), dt, x.data_ptr(), x.shape[0], x.shape[1],
-        None if perm is None else perm.data_ptr(), int(top_k), rows,
-        None if offsets is None else offsets.data_ptr(), groups, int(scale_exp), q.data_ptr(),
-        scales.data_ptr(), scales.numel(), ws.data_ptr(), n, st))
+        perm = perm.data_ptr()
+    _check("moe_fp4_quantize", (_lib or load()).moe_fp4_quantize(
+        fmt, dt, x.data_ptr(), R, C, perm, top_k, rows, offsets, n_groups, scale_exp,
+        q.data_ptr(), scales.data_ptr(), scales.numel(), ws.data_ptr(), n, st))
 
 
 def moe_fp4_dequantize(q, scales, out, fmt: int, ws, offsets=None, n_groups: int = 1,
                        scale_exp: int = 0, stream=None):
     """The values of quantised rows into out [rows][C] (bf16, fp16 or fp32)."""
     st, n = _grouped(ws, stream, q, scales, out, offsets)
-    od = _dtype(out, "out", torch.bfloat16, torch.float16, torch.float32)
-    groups = _fp4_rows(q, scales, offsets, n_groups, out.shape[1])
-    _shape(out, (q.shape[0], out.shape[1]), "out")
-    _check("moe_fp4_dequantize", load().moe_fp4_dequantize(
-        int(fmt), q.data_ptr(), scales.data_ptr(), scales.numel(), q.shape[0], out.shape[1],
-        None if offsets is None else offsets.data_ptr(), groups, int(scale_exp), od,
-        out.data_ptr(), ws.data_ptr(), n, st))
+    od = _dtype(out, "out")
+    _fp4_codes(q, scales)
+    rows, C = out.shape
+    _shape(q, (rows, C // 2), "q")
+    if offsets is not None:
+        n_groups = _offsets(offsets)
+        offsets = offsets.data_ptr()
+    _check("moe_fp4_dequantize", (_lib or load()).moe_fp4_dequantize(
+        fmt, q.data_ptr(), scales.data_ptr(), scales.numel(), rows, C, offsets, n_groups,
+        scale_exp, od, out.data_ptr(), ws.data_ptr(), n, st))
 
 
 def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
@@ -544,20 +558,21 @@ def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
     its interleaved gate/up rows (y [M][N / 2])."""
     st, n = _grouped(ws, stream, xq, xs, wq, wsc, offsets, y, alpha)
     E, N, half = wq.shape
-    _fp4_rows(xq, xs, offsets, E, 2 * half)
-    if wq.dtype != torch.uint8 or wsc.dtype != torch.uint8:
-        raise TypeError("codes and scales must be uint8")
+    M = xq.shape[0]
+    _fp4_codes(xq, xs)
+    _fp4_codes(wq, wsc)
+    _shape(xq, (M, half), "xq")
     _offsets(offsets, E)
-    od = _dtype(y, "y", torch.bfloat16, torch.float16, torch.float32)
-    _shape(y, (xq.shape[0], N // 2 if swiglu else N), "y")
+    od = _dtype(y, "y")
+    _shape(y, (M, N // 2 if swiglu else N), "y")
     if alpha is not None:
-        _dtype(alpha, "alpha", torch.float32)
-        _shape(alpha, (E,), "alpha")
-    _check("moe_grouped_mm_fp4", load().moe_grouped_mm_fp4(
-        int(fmt), xq.data_ptr(), xs.data_ptr(), xs.numel(), wq.data_ptr(), wsc.data_ptr(),
-        wsc.numel(), xq.shape[0], 2 * half, N, E, offsets.data_ptr(),
-        None if alpha is None else alpha.data_ptr(), 1 if swiglu else 0, od, y.data_ptr(),
-        ws.data_ptr(), n, st))
+        if alpha.dtype != torch.float32 or alpha.shape != (E,):
+            raise ValueError(f"alpha must be an fp32 vector of {E} entries")
+        alpha = alpha.data_ptr()
+    _check("moe_grouped_mm_fp4", (_lib or load()).moe_grouped_mm_fp4(
+        fmt, xq.data_ptr(), xs.data_ptr(), xs.numel(), wq.data_ptr(), wsc.data_ptr(),
+        wsc.numel(), M, 2 * half, N, E, offsets.data_ptr(), alpha, 1 if swiglu else 0, od,
+        y.data_ptr(), ws.data_ptr(), n, st))
 
 
 def strata_px_trace_read(nbytes: int = 1024 * 4 * 16 * 8):
