@@ -36,11 +36,22 @@ constexpr uint32_t kGtABytes = kGtRows * 128;
 constexpr uint32_t kGtSub = 64 * 128;           // a 64 x 64 MN-major sub-block
 
 __host__ __device__ constexpr uint32_t gt_stage_bytes(int BN) { return kGtABytes + uint32_t(BN) * 128u; }
-__host__ __device__ constexpr int gt_stages(int BN) { return int(196608u / gt_stage_bytes(BN)); }
+// dw writes a whole tile for every stage or two that it reads: it gives up a
+// stage for the output's staging (per epilogue warp two pieces of 32 rows by
+// 128 bytes).
+constexpr uint32_t kGtPiece = 32 * 128;
+constexpr uint32_t kGtStaging = kGtEpiWarps * 2 * kGtPiece;
+__host__ __device__ constexpr uint32_t gt_staging(int mode) {
+    return mode == kGmmDw ? kGtStaging : 0u;
+}
+__host__ __device__ constexpr int gt_stages(int mode, int BN) {
+    return int((212992u - gt_staging(mode)) / gt_stage_bytes(BN));
+}
 
 struct GtMaps {
     CUtensorMap a[kGtRows / kGtBox];            // by box height (dw: a[0] alone)
     CUtensorMap b;
+    CUtensorMap out;                            // dw alone
 };
 
 struct GtArgs {
@@ -85,7 +96,7 @@ __device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a,
 template <int MODE, int BN, bool F32>
 __global__ void __launch_bounds__(kGtThreads, 1)
     k_gmm_tc(const __grid_constant__ GtMaps maps, GtArgs a) {
-    constexpr int STAGES = gt_stages(BN);
+    constexpr int STAGES = gt_stages(MODE, BN);
     constexpr uint32_t STAGE = gt_stage_bytes(BN);
     extern __shared__ uint8_t gt_dyn[];
     __shared__ GroupTable t;
@@ -225,7 +236,28 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         constexpr int CH = BN / 64;              // 32-column pieces of a warp's half
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (BN / 2));
-        uint32_t acc = 0;
+        uint8_t* stage = base + STAGES * STAGE + wid * (2 * kGtPiece);      // dw
+        uint32_t acc = 0, pieces = 0;
+        // dw: 128 bytes of each of the warp's 32 rows to memory by TMA, which
+        // writes whole lines (32-byte stores of a lane a row took 1.7 times
+        // as long); the lanes' 16-byte pieces are spread by the swizzle
+        auto put = [&](const GtTile& i, int col, const uint32_t (&w)[32]) {
+            uint8_t* s = stage + (pieces & 1u) * kGtPiece;
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(s + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            const int y = i.arow + (wid & 3) * 32;
+            if (lane == 0) {
+                if (col < a.K && y < a.N) tma_store_3d(&maps.out, s, col, y, i.e);
+                bulk_commit();
+            }
+            ++pieces;
+        };
         for (auto it = first_tile; more(it); it.next()) {
             const GtTile i = gt_tile<MODE, BN>(t, a, it);
             const int c0 = i.c0 + half * (BN / 2);
@@ -253,7 +285,11 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_empty[buf]);
                 }
-                if (live) {
+                if (MODE == kGmmDw) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        put(i, c0 + c * 32, reinterpret_cast<const uint32_t(&)[32]>(sum[c]));
+                } else if (live) {
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
                         gt_store<true, 32>(a.out, at + c * 32, sum[c], cols - c0 - c * 32, a.vec, 0);
@@ -264,6 +300,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
                     tc_fence_after();
                 }
+                uint32_t w[32];                  // dw: 64 columns, packed
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     uint32_t v[32];
@@ -274,9 +311,16 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0u;
                     }
-                    if (live)
+                    if (MODE == kGmmDw) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            w[16 * (c & 1) + j] = gt_pack(__uint_as_float(v[2 * j]),
+                                                          __uint_as_float(v[2 * j + 1]), a.bf16);
+                        if (c & 1) put(i, c0 + (c - 1) * 32, w);
+                    } else if (live) {
                         gt_store<false, 32>(a.out, at + c * 32, reinterpret_cast<const float*>(v),
                                             cols - c0 - c * 32, a.vec, a.bf16);
+                    }
                 }
                 if (i.stages > 0) {
                     tc_fence_before();
@@ -286,6 +330,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 }
             }
         }
+        if (MODE == kGmmDw && lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -305,11 +350,13 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
         const void* b = g.M > 0 ? g.b : g.out;
         ok = gt_map16(&m.a[0], a, g.N, rows, 0, 64) && gt_map16(&m.b, b, g.K, rows, 0, 64);
         for (int i = 1; i < kGtRows / kGtBox; ++i) m.a[i] = m.a[0];
+        ok = ok && gt_map(&m.out, F32 ? 4 : 2, g.out, uint64_t(g.K) * (F32 ? 4 : 2), g.N, g.E, 32);
     } else {
         const int red = MODE == kGmmFwd ? g.K : g.N;
         for (int i = 0; i < kGtRows / kGtBox; ++i)
             ok = ok && gt_map16(&m.a[i], g.a, red, rows, 0, kGtBox * (i + 1));
         ok = ok && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? BN : 64);
+        m.out = m.b;
     }
     if (!ok) return cudaErrorInvalidValue;
     GtArgs a{};
@@ -323,7 +370,8 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
     a.bf16 = g.dtype == STRATA_BF16;
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
     a.vec = gt_vec(g.out, pitch);
-    const size_t dyn = size_t(gt_stages(BN)) * gt_stage_bytes(BN) + 1024;
+    const size_t dyn =
+        size_t(gt_stages(MODE, BN)) * gt_stage_bytes(BN) + gt_staging(MODE) + 1024;
     return gt_launch(k_gmm_tc<MODE, BN, F32>, kGtThreads, dyn, s, m, a);
 }
 

@@ -141,7 +141,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 gt_encode_fn() {
 
 // A row-major array [z][rows][inner bytes] with the 128-byte swizzle; boxes
 // of 128 bytes by box_rows rows.  z = 0: two dimensions.  esize: bytes of an
-// element (1 or 2), the unit of the inner coordinate.
+// element (1, 2 or 4), the unit of the inner coordinate.
 inline bool gt_map(CUtensorMap* m, int esize, const void* base, uint64_t inner, uint64_t rows,
                    uint64_t z, uint32_t box_rows) {
     auto fn = gt_encode_fn();
@@ -149,8 +149,10 @@ inline bool gt_map(CUtensorMap* m, int esize, const void* base, uint64_t inner, 
     const cuuint64_t dim[3] = {inner / esize, rows, z};
     const cuuint64_t stride[2] = {inner, inner * rows};
     const cuuint32_t box[3] = {cuuint32_t(128 / esize), box_rows, 1}, one[3] = {1, 1, 1};
-    return fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-              z ? 3 : 2, const_cast<void*>(base), dim, stride, box, one,
+    const CUtensorMapDataType type = esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    return fn(m, type, z ? 3 : 2, const_cast<void*>(base), dim, stride, box, one,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
