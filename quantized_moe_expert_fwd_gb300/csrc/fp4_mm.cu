@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     const int nt = (a.N + kF4N - 1) / kF4N, words = fp4_words(a.K, FMT);
     const int stages = (a.K + kF4K - 1) / kF4K;
     const int blocks = t.pre[a.E];
-    const GtIter<false> first_tile(nt, 0);
+    const GtIter<false> first_tile(nt, 0, int(blockIdx.x), int(gridDim.x));
 
     if (wid == kGtTmaWarp) {
         if (elect_one()) {
@@ -277,7 +277,7 @@ cudaError_t f4_run(const Fp4GmmArgs& g, cudaStream_t s) {
         ok = ok && gt_map(&m.a[i], 1, g.xq, g.K / 2, g.M, 0, kGtBox * (i + 1));
     if (!ok) return cudaErrorInvalidValue;
     const int vec = gt_vec(g.out, size_t(SWIGLU ? g.N / 2 : g.N) * (F32 ? 4 : 2));
-    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, kF4Threads, F4<FMT>::kDyn, s, m, g, vec);
+    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, kF4Threads, 1, F4<FMT>::kDyn, s, m, g, vec);
 }
 
 template <int FMT>

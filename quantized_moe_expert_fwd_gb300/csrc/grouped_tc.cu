@@ -35,18 +35,24 @@ constexpr int kGtPromote = 8;                   // stages between drains of an f
 constexpr uint32_t kGtABytes = kGtRows * 128;
 constexpr uint32_t kGtSub = 64 * 128;           // a 64 x 64 MN-major sub-block
 
-__host__ __device__ constexpr uint32_t gt_stage_bytes(int BN) { return kGtABytes + uint32_t(BN) * 128u; }
-// dw writes a whole tile for every stage or two that it reads: it gives up a
-// stage for the output's staging (per epilogue warp two pieces of 32 rows by
+// dw writes a whole tile for every stage or two that it reads: it gives up
+// stages for the output's staging (per epilogue warp two pieces of 32 rows by
 // 128 bytes).
 constexpr uint32_t kGtPiece = 32 * 128;
 constexpr uint32_t kGtStaging = kGtEpiWarps * 2 * kGtPiece;
-__host__ __device__ constexpr uint32_t gt_staging(int mode) {
-    return mode == kGmmDw ? kGtStaging : 0u;
-}
-__host__ __device__ constexpr int gt_stages(int mode, int BN) {
-    return int((212992u - gt_staging(mode)) / gt_stage_bytes(BN));
-}
+
+// A kernel's geometry.  PAIR: two CTAs make one tile of 256 rows by BN
+// columns; each loads its 128 rows and half of the columns.
+template <int MODE, int BN, bool PAIR>
+struct Gt {
+    static constexpr int kCols = PAIR ? BN / 2 : BN;             // B columns a CTA loads
+    static constexpr uint32_t kBBytes = uint32_t(kCols) * 128u;
+    static constexpr uint32_t kStage = kGtABytes + kBBytes;
+    static constexpr uint32_t kStagingBytes = MODE == kGmmDw ? kGtStaging : 0u;
+    static constexpr int kStages = int((212992u - kStagingBytes) / kStage);
+    static constexpr size_t kDyn = size_t(kStages) * kStage + kStagingBytes + 1024;
+    static constexpr int kBlock = PAIR ? 2 * kGtRows : kGtRows;  // rows of a tile
+};
 
 struct GtMaps {
     CUtensorMap a[kGtRows / kGtBox];            // by box height (dw: a[0] alone)
@@ -68,14 +74,16 @@ struct GtTile {
     size_t orow;
 };
 
-template <int MODE, int BN>
+// rank: the CTA's half of a pair's rows.
+template <int MODE, int BN, bool PAIR>
 __device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a,
-                                          const GtIter<MODE == kGmmDw>& it) {
+                                          const GtIter<MODE == kGmmDw>& it, int rank) {
+    constexpr int BLOCK = Gt<MODE, BN, PAIR>::kBlock;
     GtTile i;
     i.c0 = it.c * BN;
     if (MODE == kGmmDw) {
         i.e = it.e;
-        i.arow = it.m * kGtRows;
+        i.arow = it.m * BLOCK + rank * kGtRows;
         i.rows = min(kGtRows, a.N - i.arow);
         i.slot0 = t.row[i.e];
         i.cnt = t.cnt[i.e];
@@ -83,7 +91,7 @@ __device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a,
         i.orow = size_t(i.e) * a.N + i.arow;
     } else {
         i.e = group_of_block(t, a.E, it.m);
-        const int in = (it.m - t.pre[i.e]) * kGtRows;
+        const int in = (it.m - t.pre[i.e]) * BLOCK + rank * kGtRows;
         i.arow = t.row[i.e] + in;
         i.rows = min(kGtRows, t.cnt[i.e] - in);
         i.slot0 = i.cnt = 0;
@@ -93,27 +101,44 @@ __device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a,
     return i;
 }
 
-template <int MODE, int BN, bool F32>
+// dw: the rows of stage ks that the last 16-row step takes from behind the
+// group's end.
+template <int MODE>
+__device__ __forceinline__ int gt_dead(const GtTile& i, int ks) {
+    return MODE == kGmmDw ? -min(kGtK, i.cnt - ks * kGtK) & 15 : 0;
+}
+
+template <int MODE, int BN, bool F32, bool PAIR>
 __global__ void __launch_bounds__(kGtThreads, 1)
     k_gmm_tc(const __grid_constant__ GtMaps maps, GtArgs a) {
-    constexpr int STAGES = gt_stages(MODE, BN);
-    constexpr uint32_t STAGE = gt_stage_bytes(BN);
+    using G = Gt<MODE, BN, PAIR>;
+    constexpr int STAGES = G::kStages;
+    constexpr uint32_t STAGE = G::kStage;
     extern __shared__ uint8_t gt_dyn[];
     __shared__ GroupTable t;
-    __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], done;
+    // full: a stage's copies landed.  Pairs: both CTAs' copies complete on rank
+    // 0's `both`; a stage that needs rows overwritten instead completes on each
+    // CTA's own `full`, and rank 1 reports at rank 0's `fixed` (a report from
+    // thread to thread takes a microsecond, so only those stages pay it).
+    // empty, acc_full and done signal in both CTAs, acc_empty at rank 0.
+    __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], both[STAGES], fixed[STAGES];
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done;
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31;
     const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
+    const int rank = PAIR ? int(cluster_rank()) : 0;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gt_dyn) + 1023) &
                                                ~uintptr_t(1023));
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+            mbar_init(&both[i], 1);
+            mbar_init(&fixed[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], kGtEpiWarps);
+            mbar_init(&acc_empty[i], PAIR ? 2 * kGtEpiWarps : kGtEpiWarps);
         }
         mbar_init(&done, 1);
         mbar_fence_init();
@@ -121,18 +146,26 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         tma_prefetch_map(&maps.a[0]);
     }
     if (wid == kGtMmaWarp) {
-        tmem_alloc(&tmem_base, 2 * BN);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc2(&tmem_base, 2 * BN);
+            tmem_relinquish2();
+        } else {
+            tmem_alloc(&tmem_base, 2 * BN);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();            // both CTAs' barriers exist
     tc_fence_after();
     pdl_launch();
     pdl_wait();
-    build_groups(t, a.offsets, a.E, a.M, kGtRows, a.err);
+    build_groups(t, a.offsets, a.E, a.M, G::kBlock, a.err);
     const uint32_t tmem = tmem_base;
     const int cols = MODE == kGmmFwd ? a.N : a.K;
-    const GtIter<MODE == kGmmDw> first_tile((cols + BN - 1) / BN, (a.N + kGtRows - 1) / kGtRows);
+    const GtIter<MODE == kGmmDw> first_tile(
+        (cols + BN - 1) / BN, (a.N + G::kBlock - 1) / G::kBlock,
+        int(blockIdx.x) / (PAIR ? 2 : 1), int(gridDim.x) / (PAIR ? 2 : 1));
     const int blocks = t.pre[a.E];
     auto more = [&](const GtIter<MODE == kGmmDw>& it) {
         return MODE == kGmmDw ? it.e < a.E : it.m < blocks;
@@ -142,73 +175,105 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         if (elect_one()) {
             uint32_t st = 0;
             for (auto it = first_tile; more(it); it.next()) {
-                const GtTile i = gt_tile<MODE, BN>(t, a, it);
-                const int nbox = (i.rows + kGtBox - 1) / kGtBox;
-                const CUtensorMap* ma = &maps.a[MODE == kGmmDw ? 0 : nbox - 1];
+                const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
+                // rows of a pair's tile may all be the other CTA's
+                const int nbox = i.rows > 0 ? (i.rows + kGtBox - 1) / kGtBox : 0;
+                const CUtensorMap* ma = &maps.a[MODE == kGmmDw || nbox == 0 ? 0 : nbox - 1];
+                const int b0 = i.c0 + rank * G::kCols;
                 const uint32_t bytes =
-                    (MODE == kGmmDw ? kGtABytes : uint32_t(nbox) * kGtBox * 128u) + BN * 128u;
+                    (MODE == kGmmDw ? kGtABytes : uint32_t(nbox) * kGtBox * 128u) + G::kBBytes;
                 for (int ks = 0; ks < i.stages; ++ks, ++st) {
                     const uint32_t s = st % STAGES, round = st / STAGES;
                     if (round > 0) gt_wait(&empty[s], (round - 1) & 1, a.err, 50, s);
                     uint8_t* sa = base + s * STAGE;
                     uint8_t* sb = sa + kGtABytes;
                     const int r0 = ks * kGtK;
+                    if (PAIR && !gt_dead<MODE>(i, ks)) {
+                        const uint32_t bar = rank0_addr(&both[s]);
+                        if (rank == 0) mbar_expect_tx(&both[s], 2 * bytes);
+                        for (int j = 0; j < 2; ++j)
+                            tma2_load_2d(sa + j * kGtSub, ma, i.arow + 64 * j, i.slot0 + r0, bar);
+                        for (int j = 0; j < G::kCols / 64; ++j)
+                            tma2_load_2d(sb + j * kGtSub, &maps.b, b0 + 64 * j, i.slot0 + r0, bar);
+                        continue;
+                    }
                     mbar_expect_tx(&full[s], bytes);
                     if (MODE == kGmmDw) {
                         for (int j = 0; j < 2; ++j)
                             tma_load_2d(sa + j * kGtSub, ma, i.arow + 64 * j, i.slot0 + r0, &full[s]);
-                        for (int j = 0; j < BN / 64; ++j)
-                            tma_load_2d(sb + j * kGtSub, &maps.b, i.c0 + 64 * j, i.slot0 + r0,
+                        for (int j = 0; j < G::kCols / 64; ++j)
+                            tma_load_2d(sb + j * kGtSub, &maps.b, b0 + 64 * j, i.slot0 + r0,
                                         &full[s]);
                     } else {
-                        tma_load_2d(sa, ma, r0, i.arow, &full[s]);
+                        if (nbox > 0) tma_load_2d(sa, ma, r0, i.arow, &full[s]);
                         if (MODE == kGmmFwd) {
-                            tma_load_3d(sb, &maps.b, r0, i.c0, i.e, &full[s]);
+                            tma_load_3d(sb, &maps.b, r0, b0, i.e, &full[s]);
                         } else {
-                            for (int j = 0; j < BN / 64; ++j)
-                                tma_load_3d(sb + j * kGtSub, &maps.b, i.c0 + 64 * j, r0, i.e,
+                            for (int j = 0; j < G::kCols / 64; ++j)
+                                tma_load_3d(sb + j * kGtSub, &maps.b, b0 + 64 * j, r0, i.e,
                                             &full[s]);
                         }
                     }
                 }
             }
-            // every copy has landed before the CTA exits
+            // every copy has landed (a pair's: has been consumed) before the CTA exits
             for (uint32_t k = st > STAGES ? st - STAGES : 0; k < st; ++k)
-                gt_wait(&full[k % STAGES], (k / STAGES) & 1, a.err, 51, k % STAGES);
+                gt_wait(PAIR ? &empty[k % STAGES] : &full[k % STAGES], (k / STAGES) & 1, a.err, 51,
+                        k % STAGES);
         }
     } else if (wid == kGtMmaWarp) {
-        const uint32_t idesc = idesc_f16(kGtRows, BN, a.bf16) |
+        const uint32_t idesc = idesc_f16(G::kBlock, BN, a.bf16) |
                                (MODE == kGmmDw ? kIdescMnA : 0u) |
                                (MODE != kGmmFwd ? kIdescMnB : 0u);
         constexpr uint32_t a_step = MODE == kGmmDw ? 2048 / 16 : 2;
         constexpr uint32_t b_step = MODE != kGmmFwd ? 2048 / 16 : 2;
         uint32_t st = 0, acc = 0;
+        uint32_t both_phase = 0, own_phase = 0;      // a bit a stage: the phase waited for next
         for (auto it = first_tile; more(it); it.next()) {
-            const GtTile i = gt_tile<MODE, BN>(t, a, it);
+            const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
             for (int ks = 0; ks < i.stages; ++ks, ++st) {
                 const uint32_t s = st % STAGES;
                 const bool first = F32 ? ks % kGtPromote == 0 : ks == 0;
                 const bool last = ks == i.stages - 1 || (F32 && ks % kGtPromote == kGtPromote - 1);
                 const uint32_t buf = acc & 1u;
-                if (first && acc >= 2)
-                    gt_wait(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 52, buf);
-                gt_wait(&full[s], (st / STAGES) & 1, a.err, 53, s);
+                if (rank == 0 && first && acc >= 2)
+                    gt_wait<PAIR>(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 52, buf);
                 uint8_t* sa = base + s * STAGE;
                 uint8_t* sb = sa + kGtABytes;
+                const int dead = gt_dead<MODE>(i, ks);         // rows of the next group
                 int steps = kGtK / 16;
-                if (MODE == kGmmDw) {
-                    const int valid = min(kGtK, i.cnt - ks * kGtK);
-                    steps = (valid + 15) / 16;
-                    const int dead = steps * 16 - valid;       // rows of the next group
-                    if (dead > 0) {
-                        for (int j = lane; j < dead * 8 * (2 + BN / 64); j += 32) {
-                            const int sub = j / (dead * 8), r = j % (dead * 8);
-                            *reinterpret_cast<uint4*>(sa + sub * kGtSub + valid * 128 + r * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                if (MODE == kGmmDw) steps = (min(kGtK, i.cnt - ks * kGtK) + 15) / 16;
+                if (!PAIR) {
+                    gt_wait(&full[s], (st / STAGES) & 1, a.err, 53, s);
+                } else if (dead == 0) {
+                    if (rank == 0) {
+                        gt_wait(&both[s], (both_phase >> s) & 1u, a.err, 56, s);
+                        both_phase ^= 1u << s;
                     }
+                } else {
+                    gt_wait(&full[s], (own_phase >> s) & 1u, a.err, 53, s);
+                }
+                if (dead > 0) {
+                    const int valid = steps * 16 - dead;
+                    for (int j = lane; j < dead * 8 * (2 + G::kCols / 64); j += 32) {
+                        const int sub = j / (dead * 8), r = j % (dead * 8);
+                        *reinterpret_cast<uint4*>(sa + sub * kGtSub + valid * 128 + r * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    if (PAIR) {
+                        fence_proxy_async_all();
+                        __syncwarp();
+                        if (rank == 0) gt_wait<true>(&fixed[s], (own_phase >> s) & 1u, a.err, 57, s);
+                        else if (elect_one()) mbar_arrive_rank0(&fixed[s]);
+                        own_phase ^= 1u << s;
+                    } else {
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                }
+                if (rank != 0) {
+                    if (last) ++acc;
+                    continue;
                 }
                 tc_fence_after();
                 if (elect_one()) {
@@ -218,18 +283,30 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                                                         : sdesc_k_sw128(smem_u32(sb));
 #pragma unroll
                     for (int j = 0; j < kGtK / 16; ++j)
-                        if (MODE != kGmmDw || j < steps)
-                            umma_f16(tmem + buf * BN, da + j * a_step, db + j * b_step, idesc,
-                                     (first && j == 0) ? 0u : 1u);
-                    umma_commit(&empty[s]);
-                    if (last) umma_commit(&acc_full[buf]);
+                        if (MODE != kGmmDw || j < steps) {
+                            const uint32_t add = (first && j == 0) ? 0u : 1u;
+                            if (PAIR)
+                                umma2_f16(tmem + buf * BN, da + j * a_step, db + j * b_step, idesc, add);
+                            else
+                                umma_f16(tmem + buf * BN, da + j * a_step, db + j * b_step, idesc, add);
+                        }
+                    if (PAIR) {
+                        umma2_commit(&empty[s]);
+                        if (last) umma2_commit(&acc_full[buf]);
+                    } else {
+                        umma_commit(&empty[s]);
+                        if (last) umma_commit(&acc_full[buf]);
+                    }
                 }
                 __syncwarp();
                 if (last) ++acc;
             }
         }
         // no product may still be writing the TMEM when it is freed
-        if (elect_one()) umma_commit(&done);
+        if (rank == 0 && elect_one()) {
+            if (PAIR) umma2_commit(&done);
+            else umma_commit(&done);
+        }
         __syncwarp();
         gt_wait(&done, 0, a.err, 54, 0);
     } else {
@@ -259,7 +336,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             ++pieces;
         };
         for (auto it = first_tile; more(it); it.next()) {
-            const GtTile i = gt_tile<MODE, BN>(t, a, it);
+            const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
             const int c0 = i.c0 + half * (BN / 2);
             const size_t at = (i.orow + r) * size_t(cols) + c0;
             const bool live = r < i.rows;
@@ -283,7 +360,10 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_rank0(&acc_empty[buf]);
+                        else mbar_arrive(&acc_empty[buf]);
+                    }
                 }
                 if (MODE == kGmmDw) {
 #pragma unroll
@@ -325,7 +405,10 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 if (i.stages > 0) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_rank0(&acc_empty[buf]);
+                        else mbar_arrive(&acc_empty[buf]);
+                    }
                     ++acc;
                 }
             }
@@ -334,12 +417,16 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();            // the other CTA reads and signals no more
     tc_fence_after();
-    if (wid == kGtMmaWarp) tmem_dealloc(tmem, 2 * BN);
+    if (wid == kGtMmaWarp) {
+        if (PAIR) tmem_dealloc2(tmem, 2 * BN);
+        else tmem_dealloc(tmem, 2 * BN);
+    }
 }
 
 // ------------------------------------------------------------------- host
-template <int MODE, int BN, bool F32>
+template <int MODE, int BN, bool F32, bool PAIR>
 cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
     GtMaps m;
     bool ok = true;
@@ -355,7 +442,7 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
         const int red = MODE == kGmmFwd ? g.K : g.N;
         for (int i = 0; i < kGtRows / kGtBox; ++i)
             ok = ok && gt_map16(&m.a[i], g.a, red, rows, 0, kGtBox * (i + 1));
-        ok = ok && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? BN : 64);
+        ok = ok && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? Gt<MODE, BN, PAIR>::kCols : 64);
         m.out = m.b;
     }
     if (!ok) return cudaErrorInvalidValue;
@@ -370,14 +457,14 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
     a.bf16 = g.dtype == STRATA_BF16;
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
     a.vec = gt_vec(g.out, pitch);
-    const size_t dyn =
-        size_t(gt_stages(MODE, BN)) * gt_stage_bytes(BN) + gt_staging(MODE) + 1024;
-    return gt_launch(k_gmm_tc<MODE, BN, F32>, kGtThreads, dyn, s, m, a);
+    return gt_launch(k_gmm_tc<MODE, BN, F32, PAIR>, kGtThreads, PAIR ? 2 : 1,
+                     Gt<MODE, BN, PAIR>::kDyn, s, m, a);
 }
 
-template <int MODE, int BN>
+template <int MODE, int BN, bool PAIR>
 cudaError_t gt_typed(const GmmArgs& g, cudaStream_t s) {
-    return g.out_dtype == STRATA_F32 ? gt_run<MODE, BN, true>(g, s) : gt_run<MODE, BN, false>(g, s);
+    return g.out_dtype == STRATA_F32 ? gt_run<MODE, BN, true, PAIR>(g, s)
+                                     : gt_run<MODE, BN, false, PAIR>(g, s);
 }
 
 template <int MODE>
@@ -387,9 +474,11 @@ cudaError_t gt_pick(const GmmArgs& g, cudaStream_t s) {
     // 1024 x 2048: 14.0 us against 16.5; 32 rows: 24.9 against 24.1)
     const int cols = MODE == kGmmFwd ? g.N : g.K;
     const long long blocks = (g.M < g.E ? g.M : g.E) + g.M / kGtRows;
-    if (MODE != kGmmDw && 2 * blocks * ((cols + 255) / 256) <= device_info().sms)
-        return gt_typed<MODE, 128>(g, s);
-    return gt_typed<MODE, 256>(g, s);
+    if (MODE == kGmmDw)
+        return g.M / g.E >= 512 ? gt_typed<kGmmDw, 256, true>(g, s) : gt_typed<kGmmDw, 256, false>(g, s);
+    if (2 * blocks * ((cols + 255) / 256) <= device_info().sms)
+        return gt_typed<MODE, 128, false>(g, s);
+    return gt_typed<MODE, 256, false>(g, s);
 }
 
 }  // namespace

@@ -19,10 +19,11 @@ constexpr int kGtRows = 128;                    // tile rows
 constexpr int kGtBox = 32;                      // row box heights: 32, 64, 96, 128
 
 // Bounded wait that gives up early once a timed-out wait has been latched.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                         uint32_t site, uint32_t slot) {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((i & 255u) == 255u && *reinterpret_cast<const volatile uint32_t*>(err) == 4u)
             return false;
     }
@@ -30,19 +31,19 @@ __device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t
     return false;
 }
 
-
-// A CTA's tiles in order: column tile c (of nt) fastest, then row block m, and
-// with MT row blocks an expert (dw) the expert e.  Steps of gridDim.x tiles
-// are added digit by digit: a 64-bit division a tile took longer than the
+// A CTA's (or CTA pair's) tiles in order: column tile c (of nt) fastest, then row block m, and
+// with MT row blocks an expert (dw) the expert e.  Steps of one tile a
+// worker are added digit by digit: a 64-bit division a tile took longer than the
 // tile's first copies.
 template <bool EXPERTS>
 struct GtIter {
     int c, m, e, nt, mt, dc, dm, de;
-    __device__ __forceinline__ GtIter(int nt_, int mt_) : e(0), nt(nt_), mt(mt_), de(0) {
-        c = int(blockIdx.x) % nt;
-        m = int(blockIdx.x) / nt;
-        dc = int(gridDim.x) % nt;
-        dm = int(gridDim.x) / nt;
+    __device__ __forceinline__ GtIter(int nt_, int mt_, int worker, int workers)
+        : e(0), nt(nt_), mt(mt_), de(0) {
+        c = worker % nt;
+        m = worker / nt;
+        dc = workers % nt;
+        dm = workers / nt;
         if (EXPERTS) {
             e = m / mt;
             m %= mt;
@@ -166,24 +167,29 @@ inline int gt_vec(const void* out, size_t pitch) {
     return mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
 }
 
-// One CTA per SM, after the grids before it (programmatic dependent launch:
-// the kernel's prologue overlaps their tail).
+// One CTA per SM (in clusters of `cluster`), after the grids before it
+// (programmatic dependent launch: the kernel's prologue overlaps their tail).
 template <typename... P, typename... A>
-cudaError_t gt_launch(void (*kernel)(P...), int threads, size_t dyn, cudaStream_t s,
+cudaError_t gt_launch(void (*kernel)(P...), int threads, int cluster, size_t dyn, cudaStream_t s,
                       const A&... args) {
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(device_info().sms);
+    const int sms = device_info().sms;
+    cfg.gridDim = dim3(sms >= cluster ? sms / cluster * cluster : cluster);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = dyn;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

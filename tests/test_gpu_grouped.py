@@ -26,6 +26,10 @@ SHAPES = {
     "one_by_one": ([2, 3], 1, 1),
     "long": ([40, 300, 7], 2560, 264),
     "many": ([(7 * e) % 11 for e in range(300)], 128, 72),
+    # long groups (512 rows on average and more), some of them ragged, empty or a single row
+    "long_groups": ([1500, 0, 777, 2048, 1], 320, 264),
+    "long_even": ([1024, 512], 512, 1024),
+    "long_many": ([640 + 37 * (e % 5) for e in range(40)], 256, 392),
 }
 SEED = 11
 
