@@ -35,11 +35,12 @@ constexpr int kGtPromote = 8;                   // stages between drains of an f
 constexpr uint32_t kGtABytes = kGtRows * 128;
 constexpr uint32_t kGtSub = 64 * 128;           // a 64 x 64 MN-major sub-block
 
-// dw writes a whole tile for every stage or two that it reads: it gives up
-// stages for the output's staging (per epilogue warp two pieces of 32 rows by
-// 128 bytes).
+// dw writes a whole tile for every stage or two that it reads: it gives up a
+// stage for the output's staging, a piece of 32 rows by 128 bytes an epilogue
+// warp (two pieces a warp and a stage less: 16384 rows 196 us instead of 192,
+// 65536 rows 215 instead of 202).
 constexpr uint32_t kGtPiece = 32 * 128;
-constexpr uint32_t kGtStaging = kGtEpiWarps * 2 * kGtPiece;
+constexpr uint32_t kGtStaging = kGtEpiWarps * kGtPiece;
 
 // A kernel's geometry.  PAIR: two CTAs make one tile of 256 rows by BN
 // columns; each loads its 128 rows and half of the columns.
@@ -176,12 +177,12 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             uint32_t st = 0;
             for (auto it = first_tile; more(it); it.next()) {
                 const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
-                // rows of a pair's tile may all be the other CTA's
-                const int nbox = i.rows > 0 ? (i.rows + kGtBox - 1) / kGtBox : 0;
-                const CUtensorMap* ma = &maps.a[MODE == kGmmDw || nbox == 0 ? 0 : nbox - 1];
+                // a pair always loads whole boxes, so that rank 0 knows the bytes of both
+                const int nbox = PAIR || MODE == kGmmDw ? kGtRows / kGtBox
+                                                        : (i.rows + kGtBox - 1) / kGtBox;
+                const CUtensorMap* ma = &maps.a[MODE == kGmmDw ? 0 : nbox - 1];
                 const int b0 = i.c0 + rank * G::kCols;
-                const uint32_t bytes =
-                    (MODE == kGmmDw ? kGtABytes : uint32_t(nbox) * kGtBox * 128u) + G::kBBytes;
+                const uint32_t bytes = uint32_t(nbox) * kGtBox * 128u + G::kBBytes;
                 for (int ks = 0; ks < i.stages; ++ks, ++st) {
                     const uint32_t s = st % STAGES, round = st / STAGES;
                     if (round > 0) gt_wait(&empty[s], (round - 1) & 1, a.err, 50, s);
@@ -191,10 +192,20 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     if (PAIR && !gt_dead<MODE>(i, ks)) {
                         const uint32_t bar = rank0_addr(&both[s]);
                         if (rank == 0) mbar_expect_tx(&both[s], 2 * bytes);
-                        for (int j = 0; j < 2; ++j)
-                            tma2_load_2d(sa + j * kGtSub, ma, i.arow + 64 * j, i.slot0 + r0, bar);
-                        for (int j = 0; j < G::kCols / 64; ++j)
-                            tma2_load_2d(sb + j * kGtSub, &maps.b, b0 + 64 * j, i.slot0 + r0, bar);
+                        if (MODE == kGmmDw) {
+                            for (int j = 0; j < 2; ++j)
+                                tma2_load_2d(sa + j * kGtSub, ma, i.arow + 64 * j, i.slot0 + r0, bar);
+                            for (int j = 0; j < G::kCols / 64; ++j)
+                                tma2_load_2d(sb + j * kGtSub, &maps.b, b0 + 64 * j, i.slot0 + r0, bar);
+                        } else {
+                            tma2_load_2d(sa, ma, r0, i.arow, bar);
+                            if (MODE == kGmmFwd) {
+                                tma2_load_3d(sb, &maps.b, r0, b0, i.e, bar);
+                            } else {
+                                for (int j = 0; j < G::kCols / 64; ++j)
+                                    tma2_load_3d(sb + j * kGtSub, &maps.b, b0 + 64 * j, r0, i.e, bar);
+                            }
+                        }
                         continue;
                     }
                     mbar_expect_tx(&full[s], bytes);
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                             tma_load_2d(sb + j * kGtSub, &maps.b, b0 + 64 * j, i.slot0 + r0,
                                         &full[s]);
                     } else {
-                        if (nbox > 0) tma_load_2d(sa, ma, r0, i.arow, &full[s]);
+                        tma_load_2d(sa, ma, r0, i.arow, &full[s]);
                         if (MODE == kGmmFwd) {
                             tma_load_3d(sb, &maps.b, r0, b0, i.e, &full[s]);
                         } else {
@@ -313,27 +324,25 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         constexpr int CH = BN / 64;              // 32-column pieces of a warp's half
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (BN / 2));
-        uint8_t* stage = base + STAGES * STAGE + wid * (2 * kGtPiece);      // dw
-        uint32_t acc = 0, pieces = 0;
+        uint8_t* stage = base + STAGES * STAGE + wid * kGtPiece;            // dw
+        uint32_t acc = 0;
         // dw: 128 bytes of each of the warp's 32 rows to memory by TMA, which
         // writes whole lines (32-byte stores of a lane a row took 1.7 times
         // as long); the lanes' 16-byte pieces are spread by the swizzle
         auto put = [&](const GtTile& i, int col, const uint32_t (&w)[32]) {
-            uint8_t* s = stage + (pieces & 1u) * kGtPiece;
-            if (lane == 0) bulk_wait_read<1>();
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(s + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) * 16)) =
                     make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
             fence_proxy_async_smem();
             __syncwarp();
             const int y = i.arow + (wid & 3) * 32;
             if (lane == 0) {
-                if (col < a.K && y < a.N) tma_store_3d(&maps.out, s, col, y, i.e);
+                if (col < a.K && y < a.N) tma_store_3d(&maps.out, stage, col, y, i.e);
                 bulk_commit();
             }
-            ++pieces;
         };
         for (auto it = first_tile; more(it); it.next()) {
             const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
@@ -467,6 +476,18 @@ cudaError_t gt_typed(const GmmArgs& g, cudaStream_t s) {
                                      : gt_run<MODE, BN, false, PAIR>(g, s);
 }
 
+// Rows a group, on average, from which a CTA pair makes the tiles: half of the
+// column operand's traffic, but tiles of 256 rows.  Single against pair, us,
+// 32 experts of 1024 x 2048 in bf16:
+//   rows a group    128        256        512        1024
+//   forward     37.3 31.9  46.1 40.7  57.3 58.0  100.7  90.5
+//   dx          31.4 31.3  39.5 36.5  58.2 56.0  101.0  94.6
+//   dw          36.8 46.0  51.4 55.8  77.2 74.1  124.7 107.2
+// (16384 x 4096 x 4096 in one group: 306 and 281, the library's product 270).
+constexpr int gt_pair_rows(int mode) {
+    return mode == kGmmFwd ? 128 : mode == kGmmDx ? 256 : 512;
+}
+
 template <int MODE>
 cudaError_t gt_pick(const GmmArgs& g, cudaStream_t s) {
     // 256 columns a tile halve the row operand's traffic and the stages; 128
@@ -474,8 +495,8 @@ cudaError_t gt_pick(const GmmArgs& g, cudaStream_t s) {
     // 1024 x 2048: 14.0 us against 16.5; 32 rows: 24.9 against 24.1)
     const int cols = MODE == kGmmFwd ? g.N : g.K;
     const long long blocks = (g.M < g.E ? g.M : g.E) + g.M / kGtRows;
-    if (MODE == kGmmDw)
-        return g.M / g.E >= 512 ? gt_typed<kGmmDw, 256, true>(g, s) : gt_typed<kGmmDw, 256, false>(g, s);
+    if (g.M / g.E >= gt_pair_rows(MODE)) return gt_typed<MODE, 256, true>(g, s);
+    if (MODE == kGmmDw) return gt_typed<MODE, 256, false>(g, s);
     if (2 * blocks * ((cols + 255) / 256) <= device_info().sms)
         return gt_typed<MODE, 128, false>(g, s);
     return gt_typed<MODE, 256, false>(g, s);

@@ -29,6 +29,7 @@ SHAPES = {
     # long groups (512 rows on average and more), some of them ragged, empty or a single row
     "long_groups": ([1500, 0, 777, 2048, 1], 320, 264),
     "long_even": ([1024, 512], 512, 1024),
+    "mid_groups": ([300, 129, 0, 1, 256, 255, 400, 350], 200, 144),
     "long_many": ([640 + 37 * (e % 5) for e in range(40)], 256, 392),
 }
 SEED = 11
