@@ -73,22 +73,42 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* y) {
     return r;
 }
 
+// Eight words at once where the address is a multiple of 32 bytes (`wide`): a
+// lane then takes a whole sector, and a warp's 32 lanes one request.
+__device__ __forceinline__ void load8(const void* p, bool wide, uint32_t* w) {
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                       "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store8(void* p, bool wide, const uint32_t* w) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // The sixteen elements at p as raw words (8 of a 16-bit type, 16 of fp32).
 template <typename T>
 struct Raw16 {
     uint32_t w[sizeof(T) * 4];
 };
 template <typename T>
-__device__ __forceinline__ Raw16<T> load_raw(const T* p) {
+__device__ __forceinline__ Raw16<T> load_raw(const T* p, bool wide) {
     Raw16<T> r;
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T)); ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        r.w[4 * i] = v.x;
-        r.w[4 * i + 1] = v.y;
-        r.w[4 * i + 2] = v.z;
-        r.w[4 * i + 3] = v.w;
-    }
+    for (int i = 0; i < int(sizeof(T)); i += 2)
+        load8(reinterpret_cast<const uint8_t*>(p) + 16 * i, wide, r.w + 4 * i);
     return r;
 }
 // Their largest magnitude as an fp32 bit pattern: magnitudes order like
@@ -126,19 +146,23 @@ __device__ __forceinline__ void raw_f32(const Raw16<T>& r, float (&v)[16]) {
 //
 // Every rounding decision is that of exact arithmetic:
 //  - MX: dividing by a power of two is exact.
-//  - NV scale: amax / 6 in fp32 lands on a border between two e4m3 values
-//    only when it is one (a border times 6 has at most 7 bits, and floats
-//    next to it stay apart after the division).
-//  - NV elements of 16-bit inputs: the quotient x / s is either a border t
-//    between two e2m1 values or at least 2^-11 of it away, and x times the
-//    reciprocal of s rounded up, rounded toward zero, is exactly t in the
-//    first case (all 8 mantissas of s by all 7 borders) and within 2^-22 of
-//    the quotient in the second.
-//  - NV elements of fp32 inputs can be closer: they are compared with the
-//    seven borders times s, which have at most 7 bits.
+//  - NV, 16-bit inputs: a quotient amax / 6 (x / s) either is a border between
+//    two e4m3 (e2m1) values, or is at least 2^-11 of it away.  The product with
+//    the reciprocal rounded up, rounded toward zero, is exactly the border in
+//    the first case -- for all 126 borders of e4m3, and for all 8 mantissas of
+//    s by all 7 borders of e2m1 -- and within 2^-22 of the quotient in the
+//    second.  (Two IEEE divisions a unit were a third of its instructions.)
+//  - NV, fp32 inputs can be closer: amax / 6 rounded to fp32 is a border only
+//    when it is one (6 times a border has at most 7 bits, and floats next to
+//    it stay apart after the division); elements are compared with the seven
+//    borders times s, which have at most 7 bits.
+// recip[m]: 8 / (8 + m) rounded up, for the mantissa m of s.
+constexpr float kSixthUp = 0x1.555556p-3f;
+__device__ __forceinline__ float recip_up(int m) { return __fdiv_ru(8.0f, float(8 + m)); }
+
 template <int FMT, typename T>
 __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t amax, float down,
-                                               uint2& q) {
+                                               int scale_exp, const float* recip, uint2& q) {
     const bool finite = amax < 0x7f800000u;
     q = make_uint2(0u, 0u);
     float v[16];
@@ -155,7 +179,8 @@ __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t ama
         q = make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(v + 8));
         return uint32_t(ex + 127);
     }
-    const float want = __uint_as_float(amax) * down / 6.0f;
+    const float top = __uint_as_float(amax) * down;
+    const float want = sizeof(T) == 4 ? top / 6.0f : __fmul_rz(top, kSixthUp);
     uint16_t s2;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.0f), "f"(want));
     const uint32_t sbyte = uint32_t(s2 & 0xffu);
@@ -177,7 +202,10 @@ __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t ama
         }
         q = make_uint2(w[0], w[1]);
     } else {
-        const float inv = __fdiv_ru(down, s);
+        // the exponent of s and the tensor's power of two come off as integers
+        const int e = int(__float_as_uint(s) >> 23) - 127 + scale_exp;
+        const float inv = __uint_as_float(
+            __float_as_uint(recip[__float_as_uint(s) >> 20 & 7u]) - (uint32_t(e) << 23));
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = __fmul_rz(v[j], inv);
         q = make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(v + 8));
@@ -185,28 +213,48 @@ __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t ama
     return sbyte;
 }
 
-// A warp works through consecutive rows, a lane 16 elements (a unit) at a
-// time: 512 columns of a row a step, gridDim.y steps side by side.  The 4
-// (NV) or 8 (MX) lanes of a scale word write it as one; units past the row's
-// end contribute the zeros of its last word.
+// The rows cut into steps of 512 columns (a lane 16 of them, a unit), a run of
+// consecutive steps a warp: all warps the GPU holds get the same number to
+// within one, and a row's group is looked up about once a run.
+struct Steps {
+    int row, step, left;                 // the next step and the number that remain
+};
+__device__ __forceinline__ Steps warp_steps(int rows, int steps) {
+    const long long total = (long long)rows * steps;
+    const int warps = int(gridDim.x) * (kQThreads / 32);
+    const int w = int(blockIdx.x) * (kQThreads / 32) + int(threadIdx.x >> 5);
+    const long long lo = total * w / warps, hi = total * (w + 1) / warps;
+    return Steps{int(lo / steps), int(lo % steps), int(hi - lo)};
+}
+
+// The 4 (NV) or 8 (MX) lanes of a scale word write it as one; units past the
+// row's end contribute the zeros of its last word.
 //
-// Bound by instructions: about 100 a unit, near 4 for each two elements;
-// memory moves 2.6 bytes an element.
+// 16384 rows of 2048 (bf16, NV) gathered from 2048: 18 us before the steps
+// were dealt out evenly and the loads widened to 32 bytes.  Bound by
+// instructions (about 110 a unit) and, read from memory, by the 2.6 bytes an
+// element.
 template <int FMT, typename T>
-__global__ void __launch_bounds__(kQThreads) k_fp4_quantize(Fp4QuantArgs a, int rows_per_warp) {
+__global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, int wide) {
+    __shared__ float recip[8];
+    if (threadIdx.x < 8) recip[threadIdx.x] = recip_up(threadIdx.x);
+    __syncthreads();
     pdl_launch();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int units = a.cols / 16, words = fp4_words(a.cols, FMT);
+    const int units = a.cols / 16, words = fp4_words(a.cols, FMT), steps = (units + 31) / 32;
     const float down = ldexpf(1.0f, -a.scale_exp);
     const T* x = static_cast<const T*>(a.x);
-    int row = int(blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5)) * rows_per_warp;
-    const int last = min(row + rows_per_warp, a.rows);
+    Steps s = warp_steps(a.rows, steps);
     RowGroup g{-1, -1, 0};
-    while (row < last) {
+    while (s.left > 0) {
+        const int row = s.row;
         if (row >= g.end) g = row_group(a.offsets, a.n_groups, a.rows, row, a.err);
         if (g.first < 0) {
-            row = g.end;
+            // on to the next row that may have a group
+            s.left -= (g.end - row) * steps - s.step;
+            s.row = g.end;
+            s.step = 0;
             continue;
         }
         int src = row;
@@ -218,15 +266,19 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quantize(Fp4QuantArgs a, int 
         const bool bad = src < 0 || src >= a.x_rows;
         if (bad && lane == 0) latch(a.err, STRATA_EBADROUTE);
         const int r = row - g.first;
-        const size_t block = size_t(g.block) + (r >> 7);
-        for (int u = int(blockIdx.y) * 32 + lane; u - lane < units; u += 32 * int(gridDim.y)) {
+        const T* xr = x + size_t(bad ? 0 : src) * a.cols;
+        uint8_t* qr = a.q + size_t(row) * (a.cols / 2);
+        uint8_t* sr = a.scales + fp4_scale_at(size_t(g.block) + (r >> 7), words, r, 0);
+        const int end = min(steps, s.step + s.left);
+        s.left -= end - s.step;
+        for (int u = s.step * 32 + lane; u < end * 32; u += 32) {
             const bool live = u < units;
             Raw16<T> raw = {};
-            if (live && !bad) raw = load_raw(x + size_t(src) * a.cols + u * 16);
+            if (live && !bad) raw = load_raw(xr + u * 16, wide != 0);
             uint32_t amax = raw_amax(raw);
             if (FMT == 0) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             uint2 q;
-            uint32_t word = quantize16<FMT>(raw, amax, down, q);
+            uint32_t word = quantize16<FMT>(raw, amax, down, a.scale_exp, recip, q);
             // gather the word's 4 bytes: two exchanges among its lanes
             if (FMT == 0) {
                 word |= __shfl_down_sync(0xffffffffu, word, 2) << 8;
@@ -237,39 +289,42 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quantize(Fp4QuantArgs a, int 
             }
             const int w = u >> (FMT == 0 ? 3 : 2);
             if ((lane & (FMT == 0 ? 7 : 3)) == 0 && w < words)
-                *reinterpret_cast<uint32_t*>(a.scales + fp4_scale_at(block, words, r, w)) = word;
-            if (live)
-                *reinterpret_cast<uint2*>(a.q + size_t(row) * (a.cols / 2) + u * 8) = q;
+                *reinterpret_cast<uint32_t*>(sr + size_t(w) * 512) = word;
+            if (live) *reinterpret_cast<uint2*>(qr + u * 8) = q;
         }
-        ++row;
+        s.step = 0;
+        ++s.row;
     }
 }
 
 template <int FMT, typename T>
-__global__ void __launch_bounds__(kQThreads) k_fp4_dequantize(Fp4DequantArgs a, int rows_per_warp) {
+__global__ void __launch_bounds__(kQThreads, 6) k_fp4_dequantize(Fp4DequantArgs a, int wide) {
     pdl_launch();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int units = a.cols / 16, words = fp4_words(a.cols, FMT);
+    const int units = a.cols / 16, words = fp4_words(a.cols, FMT), steps = (units + 31) / 32;
     const float up = ldexpf(1.0f, a.scale_exp);
     T* out = static_cast<T*>(a.out);
-    int row = int(blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5)) * rows_per_warp;
-    const int last = min(row + rows_per_warp, a.rows);
+    Steps s = warp_steps(a.rows, steps);
     RowGroup g{-1, -1, 0};
-    while (row < last) {
+    while (s.left > 0) {
+        const int row = s.row;
         if (row >= g.end) g = row_group(a.offsets, a.n_groups, a.rows, row, a.err);
         if (g.first < 0) {
-            row = g.end;
+            s.left -= (g.end - row) * steps - s.step;
+            s.row = g.end;
+            s.step = 0;
             continue;
         }
         const int r = row - g.first;
-        const size_t block = size_t(g.block) + (r >> 7);
-        for (int u = int(blockIdx.y) * 32 + lane; u < units; u += 32 * int(gridDim.y)) {
+        const uint8_t* qr = a.q + size_t(row) * (a.cols / 2);
+        const uint8_t* sr = a.scales + fp4_scale_at(size_t(g.block) + (r >> 7), words, r, 0);
+        const int end = min(steps, s.step + s.left);
+        s.left -= end - s.step;
+        for (int u = s.step * 32 + lane; u < min(end * 32, units); u += 32) {
             const int sc = FMT == 0 ? u >> 1 : u;
-            const float s = fp4_scale_f32<FMT>(
-                __ldg(a.scales + fp4_scale_at(block, words, r, sc >> 2) + (sc & 3)));
-            const uint2 q =
-                __ldg(reinterpret_cast<const uint2*>(a.q + size_t(row) * (a.cols / 2) + u * 8));
+            const float f32s = fp4_scale_f32<FMT>(__ldg(sr + size_t(sc >> 2) * 512 + (sc & 3)));
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(qr + u * 8));
             uint32_t w[sizeof(T) * 4];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -277,7 +332,7 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_dequantize(Fp4DequantArgs a, 
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
                 // value times scale is exact (6 bits); the power of two is
                 // applied last, so it rounds only outside fp32's normal range
-                const float v0 = f.x * s * up, v1 = f.y * s * up;
+                const float v0 = f.x * f32s * up, v1 = f.y * f32s * up;
                 if constexpr (sizeof(T) == 4) {
                     w[2 * j] = __float_as_uint(v0);
                     w[2 * j + 1] = __float_as_uint(v1);
@@ -287,35 +342,24 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_dequantize(Fp4DequantArgs a, 
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v1), "f"(v0));
                 }
             }
-            uint4* o = reinterpret_cast<uint4*>(out + size_t(row) * a.cols + u * 16);
+            uint8_t* o = reinterpret_cast<uint8_t*>(out + size_t(row) * a.cols + u * 16);
 #pragma unroll
-            for (int j = 0; j < int(sizeof(T)); ++j)
-                o[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            for (int j = 0; j < int(sizeof(T)); j += 2) store8(o + 16 * j, wide != 0, w + 4 * j);
         }
-        ++row;
+        s.step = 0;
+        ++s.row;
     }
 }
 
-// Rows in runs over all the warps the GPU holds; with fewer rows than that, a
-// row's 512-column steps go to warps of their own.
-struct RowGrid {
-    dim3 grid;
-    int rows_per_warp;
-};
-RowGrid row_grid(int rows, int units) {
-    const int warps = device_info().sms * 64, per_cta = kQThreads / 32;
-    RowGrid g;
-    g.rows_per_warp = (rows + warps - 1) / warps;
-    const int runs = (rows + g.rows_per_warp - 1) / g.rows_per_warp;
-    const int steps = (units + 31) / 32, room = warps / runs;
-    g.grid = dim3((runs + per_cta - 1) / per_cta, steps < room ? steps : (room > 0 ? room : 1));
-    return g;
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_rows(void (*kernel)(P...), dim3 grid, cudaStream_t s, const A&... args) {
+// per_sm: the CTAs of the kernel that a SM holds.
+template <typename... P, typename A>
+cudaError_t launch_steps(void (*kernel)(P...), int per_sm, cudaStream_t s, const A& args,
+                         const void* wide_base) {
+    const long long steps = (long long)args.rows * ((args.cols / 16 + 31) / 32);
+    const long long want = (steps + kQThreads / 32 - 1) / (kQThreads / 32);
+    const int most = device_info().sms * per_sm;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(want < most ? int(want) : most);
     cfg.blockDim = dim3(kQThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -323,27 +367,26 @@ cudaError_t launch_rows(void (*kernel)(P...), dim3 grid, cudaStream_t s, const A
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    // rows are multiples of 64 bytes, so the base decides for all of them
+    return cudaLaunchKernelEx(&cfg, kernel, args,
+                              int((reinterpret_cast<uintptr_t>(wide_base) & 31u) == 0));
 }
 
 template <int FMT>
 cudaError_t quantize(const Fp4QuantArgs& a, cudaStream_t s) {
-    const RowGrid g = row_grid(a.rows, a.cols / 16);
     if (a.dtype == STRATA_BF16)
-        return launch_rows(k_fp4_quantize<FMT, __nv_bfloat16>, g.grid, s, a, g.rows_per_warp);
-    if (a.dtype == STRATA_F16)
-        return launch_rows(k_fp4_quantize<FMT, __half>, g.grid, s, a, g.rows_per_warp);
-    return launch_rows(k_fp4_quantize<FMT, float>, g.grid, s, a, g.rows_per_warp);
+        return launch_steps(k_fp4_quantize<FMT, __nv_bfloat16>, 4, s, a, a.x);
+    if (a.dtype == STRATA_F16) return launch_steps(k_fp4_quantize<FMT, __half>, 4, s, a, a.x);
+    return launch_steps(k_fp4_quantize<FMT, float>, 4, s, a, a.x);
 }
 
 template <int FMT>
 cudaError_t dequantize(const Fp4DequantArgs& a, cudaStream_t s) {
-    const RowGrid g = row_grid(a.rows, a.cols / 16);
     if (a.out_dtype == STRATA_BF16)
-        return launch_rows(k_fp4_dequantize<FMT, __nv_bfloat16>, g.grid, s, a, g.rows_per_warp);
+        return launch_steps(k_fp4_dequantize<FMT, __nv_bfloat16>, 6, s, a, a.out);
     if (a.out_dtype == STRATA_F16)
-        return launch_rows(k_fp4_dequantize<FMT, __half>, g.grid, s, a, g.rows_per_warp);
-    return launch_rows(k_fp4_dequantize<FMT, float>, g.grid, s, a, g.rows_per_warp);
+        return launch_steps(k_fp4_dequantize<FMT, __half>, 6, s, a, a.out);
+    return launch_steps(k_fp4_dequantize<FMT, float>, 6, s, a, a.out);
 }
 
 }  // namespace

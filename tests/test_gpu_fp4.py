@@ -174,6 +174,43 @@ def test_nv_scale_exp(ex):
         assert torch.equal(v.cpu().double(), torch.from_numpy(ref.values(codes, sb, 1, ex)))
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("ex", [0, -5, 17])
+def test_nv_every_scale_and_border(dtype, ex):
+    """A block for each e4m3 scale whose elements are that scale's seven borders, the values beside
+    them in the type, and the values themselves; and blocks whose largest magnitude is a border
+    between two scales, or beside one."""
+    if dtype == "fp16" and ex == 17:
+        pytest.skip("outside fp16's range")
+    dt = DT[dtype]
+    s = np.array([m * 2.0 ** -9 for m in range(1, 8)]
+                 + [(8 + m) * 2.0 ** (e - 10) for e in range(1, 16) for m in range(8) if e < 15 or m < 7])
+    s = s[(s * 6 * 2.0 ** ex < float(torch.finfo(dt).max)) & (s * 2.0 ** ex > 2.0 ** -12)]
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    rows = []
+    for off in (0, -1, 1):
+        v = torch.from_numpy(s[:, None] * borders * 2.0 ** ex).to(dt)
+        bits = v.view(torch.int32 if dt == torch.float32 else torch.int16)
+        v = (bits + off).view(dt).double().numpy()
+        rows.append(np.concatenate([6 * s[:, None] * 2.0 ** ex, v, -v, s[:, None] * 2.0 ** ex], axis=1))
+    mids = (s[1:] + s[:-1]) / 2
+    top = torch.from_numpy(6 * mids * 2.0 ** ex).to(dt)
+    bits = top.view(torch.int32 if dt == torch.float32 else torch.int16)
+    for off in (0, -1, 1):
+        t = (bits + off).view(dt).double().numpy()
+        rows.append(np.concatenate([t[:, None], np.outer(mids * 2.0 ** ex, np.linspace(-5, 5, 15))], axis=1))
+    x = torch.from_numpy(np.concatenate(rows)).to(dt)
+    x = torch.cat([x, x.flip(1)], dim=1)                # 32 columns: two blocks a row
+    R = x.shape[0]
+    codes, sb = ref.quantize(x.double().numpy(), 1, ex)
+    qd, sc = _bufs(R, 32, 1, 1, ragged=False)
+    ws = q.make_grouped_workspace()
+    q.moe_fp4_quantize(x.cuda(), qd, sc, 1, ws, scale_exp=ex)
+    place, _ = ref.tile_places([R], 32, 1)
+    assert np.array_equal(sc.cpu().numpy()[place], sb)
+    assert np.array_equal(ref.unpack(qd.cpu().numpy()), codes)
+
+
 # -------------------------------------------------------------- the product
 def _operand(counts, K, fmt, seed, ragged, fill=0xFF):
     """Random codes and scales of groups of rows: (packed, tiled on the GPU, float64 values).
