@@ -17,6 +17,7 @@ size_t fp4_scale_bytes(int fmt, int64_t rows, int64_t cols, int64_t groups, bool
 namespace {
 
 constexpr int kQThreads = 256;
+constexpr int kQAhead = 2;               // steps whose loads a warp has in flight
 
 // Where row `r` lies: its group's rows [first, end) and first row block, or
 // first = -1 for a row of no group (end = the next row that may have one).
@@ -271,26 +272,36 @@ __global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, i
         uint8_t* sr = a.scales + fp4_scale_at(size_t(g.block) + (r >> 7), words, r, 0);
         const int end = min(steps, s.step + s.left);
         s.left -= end - s.step;
-        for (int u = s.step * 32 + lane; u < end * 32; u += 32) {
-            const bool live = u < units;
-            Raw16<T> raw = {};
-            if (live && !bad) raw = load_raw(xr + u * 16, wide != 0);
-            uint32_t amax = raw_amax(raw);
-            if (FMT == 0) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            uint2 q;
-            uint32_t word = quantize16<FMT>(raw, amax, down, a.scale_exp, recip, q);
-            // gather the word's 4 bytes: two exchanges among its lanes
-            if (FMT == 0) {
-                word |= __shfl_down_sync(0xffffffffu, word, 2) << 8;
-                word |= __shfl_down_sync(0xffffffffu, word, 4) << 16;
-            } else {
-                word |= __shfl_down_sync(0xffffffffu, word, 1) << 8;
-                word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
+        for (int u0 = s.step * 32 + lane; u0 < end * 32; u0 += 32 * kQAhead) {
+            Raw16<T> raws[kQAhead];
+#pragma unroll
+            for (int k = 0; k < kQAhead; ++k) {
+                const int u = u0 + 32 * k;
+                raws[k] = Raw16<T>{};
+                if (u < min(units, end * 32) && !bad) raws[k] = load_raw(xr + u * 16, wide != 0);
             }
-            const int w = u >> (FMT == 0 ? 3 : 2);
-            if ((lane & (FMT == 0 ? 7 : 3)) == 0 && w < words)
-                *reinterpret_cast<uint32_t*>(sr + size_t(w) * 512) = word;
-            if (live) *reinterpret_cast<uint2*>(qr + u * 8) = q;
+#pragma unroll
+            for (int k = 0; k < kQAhead; ++k) {
+                const int u = u0 + 32 * k;
+                if (u - lane >= end * 32) break;
+                const Raw16<T>& raw = raws[k];
+                uint32_t amax = raw_amax(raw);
+                if (FMT == 0) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                uint2 q;
+                uint32_t word = quantize16<FMT>(raw, amax, down, a.scale_exp, recip, q);
+                // gather the word's 4 bytes: two exchanges among its lanes
+                if (FMT == 0) {
+                    word |= __shfl_down_sync(0xffffffffu, word, 2) << 8;
+                    word |= __shfl_down_sync(0xffffffffu, word, 4) << 16;
+                } else {
+                    word |= __shfl_down_sync(0xffffffffu, word, 1) << 8;
+                    word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
+                }
+                const int w = u >> (FMT == 0 ? 3 : 2);
+                if ((lane & (FMT == 0 ? 7 : 3)) == 0 && w < words)
+                    *reinterpret_cast<uint32_t*>(sr + size_t(w) * 512) = word;
+                if (u < units) *reinterpret_cast<uint2*>(qr + u * 8) = q;
+            }
         }
         s.step = 0;
         ++s.row;
