@@ -32,7 +32,7 @@ struct F4 {
     static constexpr uint32_t kSf = kWords * 512;              // one operand's scales of a stage
     static constexpr uint32_t kStage = 2 * kF4Data + 2 * kSf;
     static constexpr int kStages = 5;
-    static constexpr size_t kDyn = size_t(kStages) * kStage + 1024;
+    static constexpr size_t kDyn = size_t(kStages) * kStage + kGtStoreBytes + 1024;
     // tensor memory: two accumulators, both operands' scales of every stage
     static constexpr uint32_t kSfCol = 2 * kF4N;
     static constexpr uint32_t kSfCols = kWords * 4;            // one operand's, a stage
@@ -224,6 +224,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (kF4N / 2));
         const int cols = SWIGLU ? a.N / 2 : a.N;
+        uint32_t* stage =
+            reinterpret_cast<uint32_t*>(sf_base + C::kStages * 2 * C::kSf) + wid * kGtStoreWords;
         uint32_t acc = 0;
         for (auto it = first_tile; it.m < blocks; it.next(), ++acc) {
             const int rb = it.m, ct = it.c;
@@ -231,12 +233,14 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             const int in = (rb - t.pre[e]) * kGtRows;
             const bool live = r < t.cnt[e] - in;
             const float al = a.alpha != nullptr ? __ldg(a.alpha + e) : 1.0f;
-            const size_t row = size_t(t.row[e] + in + r) * cols;
+            // the warp's rows, and the first one's place
+            const int rows = t.cnt[e] - in - (r - lane);
+            const size_t row = size_t(t.row[e] + in + r - lane) * cols;
             const uint32_t buf = acc & 1u;
             gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
             tc_fence_after();
             // warps whose rows all lie behind the group's end have nothing to do
-            if (r - lane < t.cnt[e] - in)
+            if (rows > 0)
 #pragma unroll
             for (int c = 0; c < kF4N / 64; ++c) {
                 uint32_t u[32];
@@ -250,12 +254,11 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                     float h[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) h[j] = f4_swiglu<F32>(v[2 * j], v[2 * j + 1]);
-                    if (live)
-                        gt_store<F32, 16>(a.out, row + c0 / 2, h, cols - c0 / 2, vec,
-                                          a.out_dtype == STRATA_BF16);
-                } else if (live) {
-                    gt_store<F32, 32>(a.out, row + c0, v, cols - c0, vec,
-                                      a.out_dtype == STRATA_BF16);
+                    gt_store<F32, 16>(a.out, row + c0 / 2, cols, min(rows, 32), h, cols - c0 / 2, vec,
+                                      a.out_dtype == STRATA_BF16, stage);
+                } else {
+                    gt_store<F32, 32>(a.out, row + c0, cols, min(rows, 32), v, cols - c0, vec,
+                                      a.out_dtype == STRATA_BF16, stage);
                 }
             }
             tc_fence_before();
@@ -277,7 +280,7 @@ cudaError_t f4_run(const Fp4GmmArgs& g, cudaStream_t s) {
         ok = ok && gt_map(&m.a[i], 1, g.xq, g.K / 2, g.M, 0, kGtBox * (i + 1));
     if (!ok) return cudaErrorInvalidValue;
     const int vec = gt_vec(g.out, size_t(SWIGLU ? g.N / 2 : g.N) * (F32 ? 4 : 2));
-    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, kF4Threads, 1, F4<FMT>::kDyn, s, m, g, vec);
+    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, kF4Threads, 1, device_info().sms, F4<FMT>::kDyn, s, m, g, vec);
 }
 
 template <int FMT>

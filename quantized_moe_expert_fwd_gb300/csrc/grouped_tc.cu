@@ -37,20 +37,24 @@ constexpr uint32_t kGtSub = 64 * 128;           // a 64 x 64 MN-major sub-block
 
 // dw writes a whole tile for every stage or two that it reads: it gives up a
 // stage for the output's staging, a piece of 32 rows by 128 bytes an epilogue
-// warp (two pieces a warp and a stage less: 16384 rows 196 us instead of 192,
-// 65536 rows 215 instead of 202).
+// warp.  (Two pieces: no faster where they fit, 196 us instead of 193 for
+// 16384 rows into 256 experts; in a pair they cost another stage, 215 instead
+// of 202 for 65536 rows.)
 constexpr uint32_t kGtPiece = 32 * 128;
-constexpr uint32_t kGtStaging = kGtEpiWarps * kGtPiece;
 
-// A kernel's geometry.  PAIR: two CTAs make one tile of 256 rows by BN
-// columns; each loads its 128 rows and half of the columns.
-template <int MODE, int BN, bool PAIR>
+constexpr int kGtPair = 1, kGtSplit = 2;        // what the CTAs of a cluster share
+
+// A kernel's geometry.  CL = kGtPair: two CTAs make one tile of 256 rows by
+// BN columns; each loads its 128 rows and half of the columns.  CL =
+// kGtSplit: the CTAs of a cluster take a part of one tile's reduction each.
+template <int MODE, int BN, int CL>
 struct Gt {
+    static constexpr bool PAIR = CL == kGtPair;
     static constexpr int kCols = PAIR ? BN / 2 : BN;             // B columns a CTA loads
     static constexpr uint32_t kBBytes = uint32_t(kCols) * 128u;
     static constexpr uint32_t kStage = kGtABytes + kBBytes;
-    static constexpr uint32_t kStagingBytes = MODE == kGmmDw ? kGtStaging : 0u;
-    static constexpr int kStages = int((212992u - kStagingBytes) / kStage);
+    static constexpr uint32_t kStagingBytes = MODE == kGmmDw ? kGtEpiWarps * kGtPiece : kGtStoreBytes;
+    static constexpr int kStages = int((214016u - kStagingBytes) / kStage);
     static constexpr size_t kDyn = size_t(kStages) * kStage + kStagingBytes + 1024;
     static constexpr int kBlock = PAIR ? 2 * kGtRows : kGtRows;  // rows of a tile
 };
@@ -70,34 +74,45 @@ struct GtArgs {
     int vec;                                    // bytes that every output row is aligned to: 32, 16, 0
 };
 
+// k0, k1: the stages of the reduction that this CTA takes.
 struct GtTile {
-    int e, arow, rows, c0, stages, slot0, cnt;
+    int e, arow, rows, c0, k0, k1, slot0, cnt;
     size_t orow;
 };
+constexpr int kGtPartPitch = 132;               // split: floats of a row of partial sums
 
-// rank: the CTA's half of a pair's rows.
-template <int MODE, int BN, bool PAIR>
+// rank: the CTA's half of a pair's rows, or its part of the reduction.
+template <int MODE, int BN, int CL>
 __device__ __forceinline__ GtTile gt_tile(const GroupTable& t, const GtArgs& a,
                                           const GtIter<MODE == kGmmDw>& it, int rank) {
-    constexpr int BLOCK = Gt<MODE, BN, PAIR>::kBlock;
+    constexpr int BLOCK = Gt<MODE, BN, CL>::kBlock;
+    const int half = CL == kGtPair ? rank * kGtRows : 0;
     GtTile i;
     i.c0 = it.c * BN;
+    int stages;
     if (MODE == kGmmDw) {
         i.e = it.e;
-        i.arow = it.m * BLOCK + rank * kGtRows;
+        i.arow = it.m * BLOCK + half;
         i.rows = min(kGtRows, a.N - i.arow);
         i.slot0 = t.row[i.e];
         i.cnt = t.cnt[i.e];
-        i.stages = (i.cnt + kGtK - 1) / kGtK;
+        stages = (i.cnt + kGtK - 1) / kGtK;
         i.orow = size_t(i.e) * a.N + i.arow;
     } else {
         i.e = group_of_block(t, a.E, it.m);
-        const int in = (it.m - t.pre[i.e]) * BLOCK + rank * kGtRows;
+        const int in = (it.m - t.pre[i.e]) * BLOCK + half;
         i.arow = t.row[i.e] + in;
         i.rows = min(kGtRows, t.cnt[i.e] - in);
         i.slot0 = i.cnt = 0;
-        i.stages = ((MODE == kGmmFwd ? a.K : a.N) + kGtK - 1) / kGtK;
+        stages = ((MODE == kGmmFwd ? a.K : a.N) + kGtK - 1) / kGtK;
         i.orow = size_t(i.arow);
+    }
+    i.k0 = 0;
+    i.k1 = stages;
+    if (CL == kGtSplit) {
+        const int part = (stages + int(cluster_size()) - 1) / int(cluster_size());
+        i.k0 = min(rank * part, stages);
+        i.k1 = min(i.k0 + part, stages);
     }
     return i;
 }
@@ -109,10 +124,18 @@ __device__ __forceinline__ int gt_dead(const GtTile& i, int ks) {
     return MODE == kGmmDw ? -min(kGtK, i.cnt - ks * kGtK) & 15 : 0;
 }
 
-template <int MODE, int BN, bool F32, bool PAIR>
+// Split: 32 partial sums to shared memory.
+__device__ __forceinline__ void gt_part(float* p, const float* v) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+}
+
+template <int MODE, int BN, bool F32, int CL>
 __global__ void __launch_bounds__(kGtThreads, 1)
     k_gmm_tc(const __grid_constant__ GtMaps maps, GtArgs a) {
-    using G = Gt<MODE, BN, PAIR>;
+    using G = Gt<MODE, BN, CL>;
+    constexpr bool PAIR = CL == kGtPair, SPLIT = CL == kGtSplit;
     constexpr int STAGES = G::kStages;
     constexpr uint32_t STAGE = G::kStage;
     extern __shared__ uint8_t gt_dyn[];
@@ -127,7 +150,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31;
     const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
-    const int rank = PAIR ? int(cluster_rank()) : 0;
+    const int rank = CL != 0 ? int(cluster_rank()) : 0;
+    const int workers = CL != 0 ? int(cluster_size()) : 1;       // CTAs of a tile
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gt_dyn) + 1023) &
                                                ~uintptr_t(1023));
     if (tid == 0) {
@@ -166,7 +190,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     const int cols = MODE == kGmmFwd ? a.N : a.K;
     const GtIter<MODE == kGmmDw> first_tile(
         (cols + BN - 1) / BN, (a.N + G::kBlock - 1) / G::kBlock,
-        int(blockIdx.x) / (PAIR ? 2 : 1), int(gridDim.x) / (PAIR ? 2 : 1));
+        int(blockIdx.x) / workers, int(gridDim.x) / workers);
     const int blocks = t.pre[a.E];
     auto more = [&](const GtIter<MODE == kGmmDw>& it) {
         return MODE == kGmmDw ? it.e < a.E : it.m < blocks;
@@ -176,14 +200,14 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         if (elect_one()) {
             uint32_t st = 0;
             for (auto it = first_tile; more(it); it.next()) {
-                const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
+                const GtTile i = gt_tile<MODE, BN, CL>(t, a, it, rank);
                 // a pair always loads whole boxes, so that rank 0 knows the bytes of both
                 const int nbox = PAIR || MODE == kGmmDw ? kGtRows / kGtBox
                                                         : (i.rows + kGtBox - 1) / kGtBox;
                 const CUtensorMap* ma = &maps.a[MODE == kGmmDw ? 0 : nbox - 1];
-                const int b0 = i.c0 + rank * G::kCols;
+                const int b0 = i.c0 + (PAIR ? rank * G::kCols : 0);
                 const uint32_t bytes = uint32_t(nbox) * kGtBox * 128u + G::kBBytes;
-                for (int ks = 0; ks < i.stages; ++ks, ++st) {
+                for (int ks = i.k0; ks < i.k1; ++ks, ++st) {
                     const uint32_t s = st % STAGES, round = st / STAGES;
                     if (round > 0) gt_wait(&empty[s], (round - 1) & 1, a.err, 50, s);
                     uint8_t* sa = base + s * STAGE;
@@ -241,13 +265,14 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         uint32_t st = 0, acc = 0;
         uint32_t both_phase = 0, own_phase = 0;      // a bit a stage: the phase waited for next
         for (auto it = first_tile; more(it); it.next()) {
-            const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
-            for (int ks = 0; ks < i.stages; ++ks, ++st) {
+            const GtTile i = gt_tile<MODE, BN, CL>(t, a, it, rank);
+            for (int ks = i.k0; ks < i.k1; ++ks, ++st) {
                 const uint32_t s = st % STAGES;
-                const bool first = F32 ? ks % kGtPromote == 0 : ks == 0;
-                const bool last = ks == i.stages - 1 || (F32 && ks % kGtPromote == kGtPromote - 1);
+                const int nth = ks - i.k0;
+                const bool first = F32 ? nth % kGtPromote == 0 : nth == 0;
+                const bool last = ks == i.k1 - 1 || (F32 && nth % kGtPromote == kGtPromote - 1);
                 const uint32_t buf = acc & 1u;
-                if (rank == 0 && first && acc >= 2)
+                if ((!PAIR || rank == 0) && first && acc >= 2)
                     gt_wait<PAIR>(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 52, buf);
                 uint8_t* sa = base + s * STAGE;
                 uint8_t* sb = sa + kGtABytes;
@@ -282,7 +307,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (rank != 0) {
+                if (PAIR && rank != 0) {
                     if (last) ++acc;
                     continue;
                 }
@@ -314,7 +339,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             }
         }
         // no product may still be writing the TMEM when it is freed
-        if (rank == 0 && elect_one()) {
+        if ((!PAIR || rank == 0) && elect_one()) {
             if (PAIR) umma2_commit(&done);
             else umma_commit(&done);
         }
@@ -325,6 +350,10 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (BN / 2));
         uint8_t* stage = base + STAGES * STAGE + wid * kGtPiece;            // dw
+        uint32_t* store =                                                   // forward, dx
+            reinterpret_cast<uint32_t*>(base + STAGES * STAGE) + wid * kGtStoreWords;
+        // split: this CTA's partial sums, in the stages (all consumed by then)
+        float* part = reinterpret_cast<float*>(base) + r * kGtPartPitch + half * (BN / 2);
         uint32_t acc = 0;
         // dw: 128 bytes of each of the warp's 32 rows to memory by TMA, which
         // writes whole lines (32-byte stores of a lane a row took 1.7 times
@@ -345,17 +374,17 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             }
         };
         for (auto it = first_tile; more(it); it.next()) {
-            const GtTile i = gt_tile<MODE, BN, PAIR>(t, a, it, rank);
+            const GtTile i = gt_tile<MODE, BN, CL>(t, a, it, rank);
             const int c0 = i.c0 + half * (BN / 2);
-            const size_t at = (i.orow + r) * size_t(cols) + c0;
-            const bool live = r < i.rows;
+            const size_t at = (i.orow + r - lane) * size_t(cols) + c0;
+            const int live = min(32, i.rows - (r - lane));       // of the warp's rows
             if (F32) {
                 float sum[CH][32];
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
-                for (int ks = 0; ks < i.stages; ks += kGtPromote, ++acc) {
+                for (int ks = i.k0; ks < i.k1; ks += kGtPromote, ++acc) {
                     const uint32_t buf = acc & 1u;
                     gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
                     tc_fence_after();
@@ -378,14 +407,18 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
                         put(i, c0 + c * 32, reinterpret_cast<const uint32_t(&)[32]>(sum[c]));
-                } else if (live) {
+                } else {
 #pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        gt_store<true, 32>(a.out, at + c * 32, sum[c], cols - c0 - c * 32, a.vec, 0);
+                    for (int c = 0; c < CH; ++c) {
+                        if (SPLIT) gt_part(part + c * 32, sum[c]);
+                        else
+                            gt_store<true, 32>(a.out, at + c * 32, cols, live, sum[c],
+                                               cols - c0 - c * 32, a.vec, 0, store);
+                    }
                 }
             } else {
                 const uint32_t buf = acc & 1u;
-                if (i.stages > 0) {
+                if (i.k1 > i.k0) {
                     gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
                     tc_fence_after();
                 }
@@ -393,7 +426,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     uint32_t v[32];
-                    if (i.stages > 0) {
+                    if (i.k1 > i.k0) {
                         tmem_ld32(tl + buf * BN + c * 32, v);
                         tmem_ld_wait();
                     } else {
@@ -406,12 +439,15 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                             w[16 * (c & 1) + j] = gt_pack(__uint_as_float(v[2 * j]),
                                                           __uint_as_float(v[2 * j + 1]), a.bf16);
                         if (c & 1) put(i, c0 + (c - 1) * 32, w);
-                    } else if (live) {
-                        gt_store<false, 32>(a.out, at + c * 32, reinterpret_cast<const float*>(v),
-                                            cols - c0 - c * 32, a.vec, a.bf16);
+                    } else if (SPLIT) {
+                        gt_part(part + c * 32, reinterpret_cast<const float*>(v));
+                    } else {
+                        gt_store<false, 32>(a.out, at + c * 32, cols, live,
+                                            reinterpret_cast<const float*>(v), cols - c0 - c * 32,
+                                            a.vec, a.bf16, store);
                     }
                 }
-                if (i.stages > 0) {
+                if (i.k1 > i.k0) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -426,7 +462,44 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();            // the other CTA reads and signals no more
+    if (SPLIT) {
+        // the partial sums of all parts, added in their order; this CTA
+        // stores its share of the tile's rows, a warp 128 columns of one row
+        cluster_sync();
+        if (more(first_tile)) {
+            const GtTile i = gt_tile<MODE, BN, CL>(t, a, first_tile, rank);
+            const float* part = reinterpret_cast<const float*>(base);
+            const int share = kGtRows / workers, c = i.c0 + lane * 4;
+            for (int r = rank * share + wid; r < min(i.rows, (rank + 1) * share);
+                 r += kGtThreads / 32) {
+                if (c >= cols) continue;
+                float v[4] = {};
+                for (int p = 0; p < workers; ++p) {
+                    const float4 x = ld_cluster_f4(part + r * kGtPartPitch + lane * 4, p);
+                    v[0] += x.x;
+                    v[1] += x.y;
+                    v[2] += x.z;
+                    v[3] += x.w;
+                }
+                const size_t at = (i.orow + r) * size_t(cols) + c;
+                if (F32) {
+                    float* o = static_cast<float*>(a.out) + at;
+                    if (a.vec && c + 4 <= cols)
+                        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+                    else
+                        for (int j = 0; j < min(4, cols - c); ++j) o[j] = v[j];
+                } else {
+                    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+                    const uint2 w = make_uint2(gt_pack(v[0], v[1], a.bf16), gt_pack(v[2], v[3], a.bf16));
+                    if (a.vec && c + 4 <= cols) *reinterpret_cast<uint2*>(o) = w;
+                    else
+                        for (int j = 0; j < min(4, cols - c); ++j)
+                            o[j] = uint16_t((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
+                }
+            }
+        }
+    }
+    if (CL != 0) cluster_sync();         // the other CTAs read and signal no more
     tc_fence_after();
     if (wid == kGtMmaWarp) {
         if (PAIR) tmem_dealloc2(tmem, 2 * BN);
@@ -435,8 +508,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 }
 
 // ------------------------------------------------------------------- host
-template <int MODE, int BN, bool F32, bool PAIR>
-cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
+template <int MODE, int BN, bool F32, int CL>
+cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
     GtMaps m;
     bool ok = true;
     const uint64_t rows = uint64_t(g.M > 0 ? g.M : 1);
@@ -451,7 +524,7 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
         const int red = MODE == kGmmFwd ? g.K : g.N;
         for (int i = 0; i < kGtRows / kGtBox; ++i)
             ok = ok && gt_map16(&m.a[i], g.a, red, rows, 0, kGtBox * (i + 1));
-        ok = ok && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? Gt<MODE, BN, PAIR>::kCols : 64);
+        ok = ok && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? Gt<MODE, BN, CL>::kCols : 64);
         m.out = m.b;
     }
     if (!ok) return cudaErrorInvalidValue;
@@ -466,40 +539,61 @@ cudaError_t gt_run(const GmmArgs& g, cudaStream_t s) {
     a.bf16 = g.dtype == STRATA_BF16;
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
     a.vec = gt_vec(g.out, pitch);
-    return gt_launch(k_gmm_tc<MODE, BN, F32, PAIR>, kGtThreads, PAIR ? 2 : 1,
-                     Gt<MODE, BN, PAIR>::kDyn, s, m, a);
+    return gt_launch(k_gmm_tc<MODE, BN, F32, CL>, kGtThreads, cluster, grid,
+                     Gt<MODE, BN, CL>::kDyn, s, m, a);
 }
 
-template <int MODE, int BN, bool PAIR>
-cudaError_t gt_typed(const GmmArgs& g, cudaStream_t s) {
-    return g.out_dtype == STRATA_F32 ? gt_run<MODE, BN, true, PAIR>(g, s)
-                                     : gt_run<MODE, BN, false, PAIR>(g, s);
+template <int MODE, int BN, int CL>
+cudaError_t gt_typed(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
+    return g.out_dtype == STRATA_F32 ? gt_run<MODE, BN, true, CL>(g, cluster, grid, s)
+                                     : gt_run<MODE, BN, false, CL>(g, cluster, grid, s);
 }
 
-// Rows a group, on average, from which a CTA pair makes the tiles: half of the
-// column operand's traffic, but tiles of 256 rows.  Single against pair, us,
-// 32 experts of 1024 x 2048 in bf16:
-//   rows a group    128        256        512        1024
-//   forward     37.3 31.9  46.1 40.7  57.3 58.0  100.7  90.5
-//   dx          31.4 31.3  39.5 36.5  58.2 56.0  101.0  94.6
-//   dw          36.8 46.0  51.4 55.8  77.2 74.1  124.7 107.2
-// (16384 x 4096 x 4096 in one group: 306 and 281, the library's product 270).
-constexpr int gt_pair_rows(int mode) {
-    return mode == kGmmFwd ? 128 : mode == kGmmDx ? 256 : 512;
-}
-
+// Which tiles.  dw: a CTA pair from 512 rows a group on average (us, 32
+// experts of 1024 x 2048 in bf16, single and pair: 51.4 55.8 at 256 rows,
+// 77.2 74.1 at 512, 124.7 107.2 at 1024).
+//
+// Forward and dx: the shortest by a count of waves and stages.  A stage takes
+// a CTA about 0.25 us with 128 columns, 0.385 with 256, a pair (256 rows, 256
+// columns) 0.35, however few of its rows are live; blocks are what the groups
+// need on average (a half-empty last one each).  Single with 256 columns
+// against pair, forward, same experts: 27.5 30.3 at 64 rows a group, 37.3 31.9
+// at 128, 46.1 40.7 at 256, 57.3 58.0 at 512, 100.7 90.5 at 1024; 16 rows of
+// 16 experts: 16.5, 14.0 with 128 columns.  Where even 128 columns leave most
+// SMs idle, a cluster of up to 8 CTAs splits the reduction (1.5 us to join).
 template <int MODE>
 cudaError_t gt_pick(const GmmArgs& g, cudaStream_t s) {
-    // 256 columns a tile halve the row operand's traffic and the stages; 128
-    // where twice the tiles still run side by side (16 rows of 16 experts of
-    // 1024 x 2048: 14.0 us against 16.5; 32 rows: 24.9 against 24.1)
-    const int cols = MODE == kGmmFwd ? g.N : g.K;
-    const long long blocks = (g.M < g.E ? g.M : g.E) + g.M / kGtRows;
-    if (g.M / g.E >= gt_pair_rows(MODE)) return gt_typed<MODE, 256, true>(g, s);
-    if (MODE == kGmmDw) return gt_typed<MODE, 256, false>(g, s);
-    if (2 * blocks * ((cols + 255) / 256) <= device_info().sms)
-        return gt_typed<MODE, 128, false>(g, s);
-    return gt_typed<MODE, 256, false>(g, s);
+    const int sms = device_info().sms, pairs = sms >= 2 ? sms / 2 * 2 : 2;
+    if (MODE == kGmmDw) {
+        if (g.M / g.E >= 512) return gt_typed<MODE, 256, kGtPair>(g, 2, pairs, s);
+        return gt_typed<MODE, 256, 0>(g, 1, sms, s);
+    }
+    const long long cols = MODE == kGmmFwd ? g.N : g.K;
+    const int stages = ((MODE == kGmmFwd ? g.K : g.N) + kGtK - 1) / kGtK;
+    const long long groups = g.M < g.E ? g.M : g.E;
+    const long long nt128 = (cols + 127) / 128, nt256 = (cols + 255) / 256;
+    auto blocks = [&](int rows) {
+        const long long b = g.M / rows + groups / 2;
+        return b > groups ? b : groups;
+    };
+    auto cost = [&](long long tiles, int workers, double stage) {
+        return double((tiles + workers - 1) / workers) * stages * stage;
+    };
+    const double c128 = cost(blocks(128) * nt128, sms, 0.25);
+    const double c256 = cost(blocks(128) * nt256, sms, 0.385);
+    const double cpair = cost(blocks(256) * nt256, pairs / 2, 0.35);
+    // the most tiles that the offsets can make, so that a cluster takes one
+    const long long most = (groups + g.M / kGtRows) * nt128;
+    for (int parts = 8; parts >= 2; parts /= 2) {
+        // clusters of 8 do not fill every part of the GPU
+        if (most * parts > (parts == 8 ? sms - 24 : sms) || stages < 4 * parts) continue;
+        const double split = (stages + parts - 1) / parts * 0.25 + 1.5;
+        if (split < c128 && split < c256 && split < cpair)
+            return gt_typed<MODE, 128, kGtSplit>(g, parts, int(most) * parts, s);
+    }
+    if (cpair < c128 && cpair < c256) return gt_typed<MODE, 256, kGtPair>(g, 2, pairs, s);
+    if (c128 < c256) return gt_typed<MODE, 128, 0>(g, 1, sms, s);
+    return gt_typed<MODE, 256, 0>(g, 1, sms, s);
 }
 
 }  // namespace

@@ -226,6 +226,23 @@ __device__ __forceinline__ void umma2_commit(uint64_t* bar) {
         "h"(uint16_t(3))
         : "memory");
 }
+// CTAs of the cluster, and 16 bytes of the shared memory of CTA `rank` at the
+// place that `p` has in this one.
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(const void* p, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %4, %5; "
+        "ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a]; }"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
 // The address of rank 0's copy of a barrier, and loads into this CTA's shared
 // memory that complete on it.
 __device__ __forceinline__ uint32_t rank0_addr(const void* p) {

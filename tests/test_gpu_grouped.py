@@ -29,6 +29,11 @@ SHAPES = {
     # long groups (512 rows on average and more), some of them ragged, empty or a single row
     "long_groups": ([1500, 0, 777, 2048, 1], 320, 264),
     "long_even": ([1024, 512], 512, 1024),
+    # few tiles and long reductions, in every direction; the last parts of a split are short
+    "few_tiles": ([40, 1], 4096, 264),
+    "few_tiles_back": ([33, 0, 12], 200, 3016),
+    "one_tile": ([100], 1048, 100),
+    "narrow_out": ([60, 9, 130], 1992, 3),
     "mid_groups": ([300, 129, 0, 1, 256, 255, 400, 350], 200, 144),
     "long_many": ([640 + 37 * (e % 5) for e in range(40)], 256, 392),
 }
