@@ -40,7 +40,7 @@ struct F4 {
 };
 
 struct F4Maps {
-    CUtensorMap a[kGtRows / kGtBox];
+    GtRowMaps a;
     CUtensorMap b;
 };
 
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         mbar_init(&done, 1);
         mbar_fence_init();
         tma_prefetch_map(&maps.b);
-        tma_prefetch_map(&maps.a[0]);
+        tma_prefetch_map(&maps.a.part);
     }
     if (wid == kGtMmaWarp) {
         tmem_alloc(&tmem_base, 512);
@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                 const int e = group_of_block(t, a.E, rb);
                 const int in = (rb - t.pre[e]) * kGtRows, arow = t.row[e] + in;
                 const int nbox = (min(kGtRows, t.cnt[e] - in) + kGtBox - 1) / kGtBox;
-                const CUtensorMap* ma = &maps.a[nbox - 1];
+                const bool whole = nbox == kGtRows / kGtBox;
+                const CUtensorMap* ma = whole ? &maps.a.whole : &maps.a.part;
                 const uint8_t* sa_g = a.xs + size_t(rb) * words * 512;
                 const uint8_t* sb_g = a.wsc + (size_t(e) * nt + ct) * words * 512;
                 for (int ks = 0; ks < stages; ++ks, ++st) {
@@ -155,7 +156,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                     const uint32_t sf_bytes = uint32_t(min(C::kWords, words - w0)) * 512u;
                     mbar_expect_tx(&full[s],
                                    uint32_t(nbox) * kGtBox * 128u + kF4Data + 2 * sf_bytes);
-                    tma_load_2d(sa, ma, ks * (kF4K / 2), arow, &full[s]);
+                    for (int j = 0; j < (whole ? 1 : nbox); ++j)
+                        tma_load_2d(sa + j * (kGtBox * 128), ma, ks * (kF4K / 2), arow + j * kGtBox,
+                                    &full[s]);
                     tma_load_3d(sa + kF4Data, &maps.b, ks * (kF4K / 2), ct * kF4N, e, &full[s]);
                     bulk_g2s(sf, sa_g + size_t(w0) * 512, sf_bytes, &full[s]);
                     bulk_g2s(sf + C::kSf, sb_g + size_t(w0) * 512, sf_bytes, &full[s]);
@@ -275,12 +278,13 @@ __global__ void __launch_bounds__(kF4Threads, 1)
 template <int FMT, bool F32, bool SWIGLU>
 cudaError_t f4_run(const Fp4GmmArgs& g, cudaStream_t s) {
     F4Maps m;
-    bool ok = gt_map(&m.b, 1, g.wq, g.K / 2, g.N, g.E, kF4N);
-    for (int i = 0; i < kGtRows / kGtBox; ++i)
-        ok = ok && gt_map(&m.a[i], 1, g.xq, g.K / 2, g.M, 0, kGtBox * (i + 1));
+    const bool ok = gt_map(&m.b, 1, g.wq, g.K / 2, g.N, g.E, kF4N) &&
+                    gt_map(&m.a.part, 1, g.xq, g.K / 2, g.M, 0, kGtBox) &&
+                    gt_map(&m.a.whole, 1, g.xq, g.K / 2, g.M, 0, kGtRows);
     if (!ok) return cudaErrorInvalidValue;
     const int vec = gt_vec(g.out, size_t(SWIGLU ? g.N / 2 : g.N) * (F32 ? 4 : 2));
-    return gt_launch(k_gmm_f4<FMT, F32, SWIGLU>, kF4Threads, 1, device_info().sms, F4<FMT>::kDyn, s, m, g, vec);
+    return gt_launch<k_gmm_f4<FMT, F32, SWIGLU>>(kF4Threads, 1, device_info().sms, F4<FMT>::kDyn, s,
+                                                 m, g, vec);
 }
 
 template <int FMT>

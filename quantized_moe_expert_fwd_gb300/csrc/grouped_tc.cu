@@ -60,7 +60,7 @@ struct Gt {
 };
 
 struct GtMaps {
-    CUtensorMap a[kGtRows / kGtBox];            // by box height (dw: a[0] alone)
+    GtRowMaps a;                                // dw: 64-row boxes in both
     CUtensorMap b;
     CUtensorMap out;                            // dw alone
 };
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         mbar_init(&done, 1);
         mbar_fence_init();
         tma_prefetch_map(&maps.b);
-        tma_prefetch_map(&maps.a[0]);
+        tma_prefetch_map(&maps.a.part);
     }
     if (wid == kGtMmaWarp) {
         if (PAIR) {
@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 // a pair always loads whole boxes, so that rank 0 knows the bytes of both
                 const int nbox = PAIR || MODE == kGmmDw ? kGtRows / kGtBox
                                                         : (i.rows + kGtBox - 1) / kGtBox;
-                const CUtensorMap* ma = &maps.a[MODE == kGmmDw ? 0 : nbox - 1];
+                const bool whole = nbox == kGtRows / kGtBox;
+                const CUtensorMap* ma = whole ? &maps.a.whole : &maps.a.part;
                 const int b0 = i.c0 + (PAIR ? rank * G::kCols : 0);
                 const uint32_t bytes = uint32_t(nbox) * kGtBox * 128u + G::kBBytes;
                 for (int ks = i.k0; ks < i.k1; ++ks, ++st) {
@@ -240,7 +241,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                             tma_load_2d(sb + j * kGtSub, &maps.b, b0 + 64 * j, i.slot0 + r0,
                                         &full[s]);
                     } else {
-                        tma_load_2d(sa, ma, r0, i.arow, &full[s]);
+                        for (int j = 0; j < (whole ? 1 : nbox); ++j)
+                            tma_load_2d(sa + j * (kGtBox * 128), ma, r0, i.arow + j * kGtBox, &full[s]);
                         if (MODE == kGmmFwd) {
                             tma_load_3d(sb, &maps.b, r0, b0, i.e, &full[s]);
                         } else {
@@ -517,14 +519,13 @@ cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
         // with no rows nothing is loaded; the maps still need an address
         const void* a = g.M > 0 ? g.a : g.out;
         const void* b = g.M > 0 ? g.b : g.out;
-        ok = gt_map16(&m.a[0], a, g.N, rows, 0, 64) && gt_map16(&m.b, b, g.K, rows, 0, 64);
-        for (int i = 1; i < kGtRows / kGtBox; ++i) m.a[i] = m.a[0];
+        ok = gt_map16(&m.a.whole, a, g.N, rows, 0, 64) && gt_map16(&m.b, b, g.K, rows, 0, 64);
+        m.a.part = m.a.whole;
         ok = ok && gt_map(&m.out, F32 ? 4 : 2, g.out, uint64_t(g.K) * (F32 ? 4 : 2), g.N, g.E, 32);
     } else {
         const int red = MODE == kGmmFwd ? g.K : g.N;
-        for (int i = 0; i < kGtRows / kGtBox; ++i)
-            ok = ok && gt_map16(&m.a[i], g.a, red, rows, 0, kGtBox * (i + 1));
-        ok = ok && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? Gt<MODE, BN, CL>::kCols : 64);
+        ok = gt_map16(&m.a.part, g.a, red, rows, 0, kGtBox) &&
+             gt_map16(&m.a.whole, g.a, red, rows, 0, kGtRows) && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? Gt<MODE, BN, CL>::kCols : 64);
         m.out = m.b;
     }
     if (!ok) return cudaErrorInvalidValue;
@@ -539,8 +540,8 @@ cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
     a.bf16 = g.dtype == STRATA_BF16;
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
     a.vec = gt_vec(g.out, pitch);
-    return gt_launch(k_gmm_tc<MODE, BN, F32, CL>, kGtThreads, cluster, grid,
-                     Gt<MODE, BN, CL>::kDyn, s, m, a);
+    return gt_launch<k_gmm_tc<MODE, BN, F32, CL>>(kGtThreads, cluster, grid, Gt<MODE, BN, CL>::kDyn,
+                                                  s, m, a);
 }
 
 template <int MODE, int BN, int CL>

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "grouped.cuh"
@@ -16,7 +17,7 @@ namespace strata {
 constexpr int kGtThreads = 320;
 constexpr int kGtEpiWarps = 8, kGtTmaWarp = 8, kGtMmaWarp = 9;
 constexpr int kGtRows = 128;                    // tile rows
-constexpr int kGtBox = 32;                      // row box heights: 32, 64, 96, 128
+constexpr int kGtBox = 32;                      // rows of the smaller row box
 
 // Bounded wait that gives up early once a timed-out wait has been latched.
 template <bool CLUSTER = false>
@@ -198,6 +199,12 @@ inline bool gt_map16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
     return gt_map(m, 2, base, inner * 2, rows, z, box_rows);
 }
 
+// Boxes of 32 and of 128 rows of the row operand: a tile that is nearly whole
+// takes the larger one, any other as many of the smaller as its rows need.
+struct GtRowMaps {
+    CUtensorMap part, whole;
+};
+
 inline int gt_vec(const void* out, size_t pitch) {
     const size_t mis = pitch | reinterpret_cast<uintptr_t>(out);
     return mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
@@ -205,12 +212,16 @@ inline int gt_vec(const void* out, size_t pitch) {
 
 // `grid` CTAs in clusters of `cluster`, after the grids before them
 // (programmatic dependent launch: the kernel's prologue overlaps their tail).
-template <typename... P, typename... A>
-cudaError_t gt_launch(void (*kernel)(P...), int threads, int cluster, int grid, size_t dyn,
-                      cudaStream_t s, const A&... args) {
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
+template <auto KERNEL, typename... A>
+cudaError_t gt_launch(int threads, int cluster, int grid, size_t dyn, cudaStream_t s,
+                      const A&... args) {
+    // the shared memory limit, raised once per device (again where a launch is
+    // refused: a device that was reset has forgotten it)
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
@@ -225,7 +236,18 @@ cudaError_t gt_launch(void (*kernel)(P...), int threads, int cluster, int grid, 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    for (int k = 0; k < 2; ++k) {
+        const bool known = dev < 64 && (raised.load(std::memory_order_relaxed) & bit) != 0;
+        if (!known || k > 0) {
+            e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
+            if (e != cudaSuccess) return e;
+            raised.fetch_or(bit, std::memory_order_relaxed);
+        }
+        e = cudaLaunchKernelEx(&cfg, KERNEL, args...);
+        if (e != cudaErrorInvalidValue || !known) break;
+        cudaGetLastError();
+    }
+    return e;
 }
 
 }  // namespace strata

@@ -415,23 +415,27 @@ def moe_grouped_workspace_bytes() -> int:
 
 
 # A decode call's host time is a good part of its whole, so the checks below
-# compare integers and sizes directly and format nothing unless they refuse.
-def _grouped(ws, stream, *tensors):
+# compare integers, sizes and types directly and format nothing unless they
+# refuse.
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _grouped(ws, stream, tensors):
     """Checks that the tensors are the binding's to pass on (the library sees
     pointers only): contiguous, on one CUDA device, the current one.  Returns
-    the stream handle and the workspace's size."""
+    the stream handle."""
     dev = ws.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != _get_device():
         raise ValueError("the workspace must be on the current CUDA device")
     for t in tensors:
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+        if t.get_device() != dev or not t.is_contiguous():
             raise ValueError("tensors must be on the workspace's device" if t.get_device() != dev
                              else "tensors passed to strata_moe must be contiguous")
-    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+    if ws.dtype is not _U8 or not ws.is_contiguous():
         raise ValueError("the workspace must be a contiguous uint8 tensor")
     # the raw handle: building torch's Stream object alone takes 5 us
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    return st, ws.numel()
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _dtype(t, what, allowed=_DTYPES):
@@ -442,12 +446,13 @@ def _dtype(t, what, allowed=_DTYPES):
 
 
 def _offsets(offsets, groups=None):
-    n = offsets.numel() - 1
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or n < 1:
+    """The number of groups that offsets name."""
+    shape = offsets.shape
+    if offsets.dtype is not _I32 or len(shape) != 1 or shape[0] < 2:
         raise ValueError("offsets must be an int32 vector of groups + 1 entries")
-    if groups is not None and n != groups:
-        raise ValueError(f"offsets must have {groups + 1} entries, not {n + 1}")
-    return n
+    if groups is not None and shape[0] != groups + 1:
+        raise ValueError(f"offsets must have {groups + 1} entries, not {shape[0]}")
+    return shape[0] - 1
 
 
 def _shape(t, shape, what):
@@ -456,17 +461,19 @@ def _shape(t, shape, what):
 
 
 def _grouped_mm(fn, a, b, offsets, out, ws, stream, M, K, N, E):
-    st, n = _grouped(ws, stream, a, b, offsets, out)
+    st = _grouped(ws, stream, (a, b, offsets, out))
     dt = _dtype(a, "the operands", _DTYPES16)
-    if b.dtype != a.dtype:
+    if b.dtype is not a.dtype:
         raise TypeError(f"the operands must have one type, not {a.dtype} and {b.dtype}")
     od = _dtype(out, "the output")
     if od != dt and od != 2:
         raise TypeError(f"the output must be {a.dtype} or fp32, not {out.dtype}")
     _offsets(offsets, E)
-    _check(fn, getattr(_lib or load(), fn)(dt, a.data_ptr(), b.data_ptr(), M, K, N, E,
-                                           offsets.data_ptr(), od, out.data_ptr(), ws.data_ptr(),
-                                           n, st))
+    status = getattr(_lib or load(), fn)(dt, a.data_ptr(), b.data_ptr(), M, K, N, E,
+                                         offsets.data_ptr(), od, out.data_ptr(), ws.data_ptr(),
+                                         ws.numel(), st)
+    if status:
+        _check(fn, status)
 
 
 def moe_grouped_mm(x, w, offsets, y, ws, stream=None):
@@ -504,20 +511,16 @@ def moe_fp4_scale_bytes(fmt: int, rows: int, cols: int, n_groups: int = 1,
                                           1 if ragged else 0))
 
 
-def _fp4_codes(q, scales):
-    if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
-        raise TypeError("codes and scales must be uint8")
-
-
 def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1,
                      scale_exp: int = 0, perm=None, top_k: int = 1, stream=None):
     """x [.][C] (bf16, fp16 or fp32) to codes q uint8 [rows][C / 2] and tiled
     scales, in groups by offsets, or n_groups equal ones; row s from x's row
     perm[s] / top_k where perm (int32) is given, which may be shorter than q
     when offsets end with it."""
-    st, n = _grouped(ws, stream, x, q, scales, offsets, perm)
+    st = _grouped(ws, stream, [t for t in (x, q, scales, offsets, perm) if t is not None])
     dt = _dtype(x, "x")
-    _fp4_codes(q, scales)
+    if q.dtype is not _U8 or scales.dtype is not _U8:
+        raise TypeError("codes and scales must be uint8")
     R, C = x.shape
     rows, half = q.shape
     if 2 * half != C:
@@ -526,29 +529,34 @@ def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1
         n_groups = _offsets(offsets)
         offsets = offsets.data_ptr()
     if perm is not None:
-        if perm.dtype != torch.int32 or perm.dim() != 1 or perm.numel() > rows:
+        if perm.dtype is not _I32 or perm.dim() != 1 or perm.numel() > rows:
             raise ValueError("perm must be an int32 vector of at most q's rows")
         rows = perm.numel()
         perm = perm.data_ptr()
-    _check("moe_fp4_quantize", (_lib or load()).moe_fp4_quantize(
+    status = (_lib or load()).moe_fp4_quantize(
         fmt, dt, x.data_ptr(), R, C, perm, top_k, rows, offsets, n_groups, scale_exp,
-        q.data_ptr(), scales.data_ptr(), scales.numel(), ws.data_ptr(), n, st))
+        q.data_ptr(), scales.data_ptr(), scales.numel(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_fp4_quantize", status)
 
 
 def moe_fp4_dequantize(q, scales, out, fmt: int, ws, offsets=None, n_groups: int = 1,
                        scale_exp: int = 0, stream=None):
     """The values of quantised rows into out [rows][C] (bf16, fp16 or fp32)."""
-    st, n = _grouped(ws, stream, q, scales, out, offsets)
+    st = _grouped(ws, stream, [t for t in (q, scales, out, offsets) if t is not None])
     od = _dtype(out, "out")
-    _fp4_codes(q, scales)
+    if q.dtype is not _U8 or scales.dtype is not _U8:
+        raise TypeError("codes and scales must be uint8")
     rows, C = out.shape
     _shape(q, (rows, C // 2), "q")
     if offsets is not None:
         n_groups = _offsets(offsets)
         offsets = offsets.data_ptr()
-    _check("moe_fp4_dequantize", (_lib or load()).moe_fp4_dequantize(
+    status = (_lib or load()).moe_fp4_dequantize(
         fmt, q.data_ptr(), scales.data_ptr(), scales.numel(), rows, C, offsets, n_groups,
-        scale_exp, od, out.data_ptr(), ws.data_ptr(), n, st))
+        scale_exp, od, out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_fp4_dequantize", status)
 
 
 def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
@@ -556,23 +564,26 @@ def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
     """y[s] = alpha[e] W[e] x[s] of two 4-bit operands (xq uint8 [M][K / 2] in
     groups by offsets, wq uint8 [E][N][K / 2]; scales tiled), or the SwiGLU of
     its interleaved gate/up rows (y [M][N / 2])."""
-    st, n = _grouped(ws, stream, xq, xs, wq, wsc, offsets, y, alpha)
+    st = _grouped(ws, stream, (xq, xs, wq, wsc, offsets, y) if alpha is None
+                  else (xq, xs, wq, wsc, offsets, y, alpha))
     E, N, half = wq.shape
+    if not (xq.dtype is _U8 and xs.dtype is _U8 and wq.dtype is _U8 and wsc.dtype is _U8):
+        raise TypeError("codes and scales must be uint8")
     M = xq.shape[0]
-    _fp4_codes(xq, xs)
-    _fp4_codes(wq, wsc)
     _shape(xq, (M, half), "xq")
+    _shape(y, (M, N // 2 if swiglu else N), "y")
     _offsets(offsets, E)
     od = _dtype(y, "y")
-    _shape(y, (M, N // 2 if swiglu else N), "y")
     if alpha is not None:
-        if alpha.dtype != torch.float32 or alpha.shape != (E,):
+        if alpha.dtype is not _F32 or alpha.shape != (E,):
             raise ValueError(f"alpha must be an fp32 vector of {E} entries")
         alpha = alpha.data_ptr()
-    _check("moe_grouped_mm_fp4", (_lib or load()).moe_grouped_mm_fp4(
+    status = (_lib or load()).moe_grouped_mm_fp4(
         fmt, xq.data_ptr(), xs.data_ptr(), xs.numel(), wq.data_ptr(), wsc.data_ptr(),
         wsc.numel(), M, 2 * half, N, E, offsets.data_ptr(), alpha, 1 if swiglu else 0, od,
-        y.data_ptr(), ws.data_ptr(), n, st))
+        y.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_grouped_mm_fp4", status)
 
 
 def strata_px_trace_read(nbytes: int = 1024 * 4 * 16 * 8):
