@@ -219,6 +219,12 @@ __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t ama
 // within one, and a row's group is looked up about once a run.
 struct Steps {
     int row, step, left;                 // the next step and the number that remain
+    __device__ __forceinline__ void skip(int to, int steps) {
+        const long long n = (long long)(to - row) * steps - step;
+        left = n < left ? left - int(n) : 0;
+        row = to;
+        step = 0;
+    }
 };
 __device__ __forceinline__ Steps warp_steps(int rows, int steps) {
     const long long total = (long long)rows * steps;
@@ -253,9 +259,7 @@ __global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, i
         if (row >= g.end) g = row_group(a.offsets, a.n_groups, a.rows, row, a.err);
         if (g.first < 0) {
             // on to the next row that may have a group
-            s.left -= (g.end - row) * steps - s.step;
-            s.row = g.end;
-            s.step = 0;
+            s.skip(g.end, steps);
             continue;
         }
         int src = row;
@@ -322,9 +326,7 @@ __global__ void __launch_bounds__(kQThreads, 6) k_fp4_dequantize(Fp4DequantArgs 
         const int row = s.row;
         if (row >= g.end) g = row_group(a.offsets, a.n_groups, a.rows, row, a.err);
         if (g.first < 0) {
-            s.left -= (g.end - row) * steps - s.step;
-            s.row = g.end;
-            s.step = 0;
+            s.skip(g.end, steps);
             continue;
         }
         const int r = row - g.first;

@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     if (wid == kGtTmaWarp) {
         if (elect_one()) {
             uint32_t st = 0;
-            for (auto it = first_tile; it.m < blocks; it.next()) {
+            bool ok = true;
+            for (auto it = first_tile; ok && it.m < blocks; it.next()) {
                 const int rb = it.m, ct = it.c;
                 const int e = group_of_block(t, a.E, rb);
                 const int in = (rb - t.pre[e]) * kGtRows, arow = t.row[e] + in;
@@ -149,16 +150,21 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                 const uint8_t* sb_g = a.wsc + (size_t(e) * nt + ct) * words * 512;
                 for (int ks = 0; ks < stages; ++ks, ++st) {
                     const uint32_t s = st % C::kStages, round = st / C::kStages;
-                    if (round > 0) gt_wait(&empty[s], (round - 1) & 1, a.err, 60, s);
+                    if (round > 0 && !gt_wait(&empty[s], (round - 1) & 1, a.err, 60, s)) {
+                        ok = false;
+                        break;
+                    }
                     uint8_t* sa = base + s * (2 * kF4Data);
                     uint8_t* sf = sf_base + s * (2 * C::kSf);
                     const int w0 = ks * C::kWords;
                     const uint32_t sf_bytes = uint32_t(min(C::kWords, words - w0)) * 512u;
                     mbar_expect_tx(&full[s],
                                    uint32_t(nbox) * kGtBox * 128u + kF4Data + 2 * sf_bytes);
-                    for (int j = 0; j < (whole ? 1 : nbox); ++j)
-                        tma_load_2d(sa + j * (kGtBox * 128), ma, ks * (kF4K / 2), arow + j * kGtBox,
-                                    &full[s]);
+                    tma_load_2d(sa, ma, ks * (kF4K / 2), arow, &full[s]);
+                    if (!whole)
+                        for (int j = 1; j < nbox; ++j)
+                            tma_load_2d(sa + j * (kGtBox * 128), ma, ks * (kF4K / 2),
+                                        arow + j * kGtBox, &full[s]);
                     tma_load_3d(sa + kF4Data, &maps.b, ks * (kF4K / 2), ct * kF4N, e, &full[s]);
                     bulk_g2s(sf, sa_g + size_t(w0) * 512, sf_bytes, &full[s]);
                     bulk_g2s(sf + C::kSf, sb_g + size_t(w0) * 512, sf_bytes, &full[s]);
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             }
             // every copy has landed before the CTA exits
             for (uint32_t k = st > C::kStages ? st - C::kStages : 0; k < st; ++k)
-                gt_wait(&full[k % C::kStages], (k / C::kStages) & 1, a.err, 61, k % C::kStages);
+                mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
         }
     } else if (wid >= kF4SfWarp) {
         // one operand's scales of each stage to tensor memory, on a thread of

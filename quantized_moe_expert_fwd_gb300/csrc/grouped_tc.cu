@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     if (wid == kGtTmaWarp) {
         if (elect_one()) {
             uint32_t st = 0;
-            for (auto it = first_tile; more(it); it.next()) {
+            bool ok = true;
+            for (auto it = first_tile; ok && more(it); it.next()) {
                 const GtTile i = gt_tile<MODE, BN, CL>(t, a, it, rank);
                 // a pair always loads whole boxes, so that rank 0 knows the bytes of both
                 const int nbox = PAIR || MODE == kGmmDw ? kGtRows / kGtBox
@@ -210,7 +211,10 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 const uint32_t bytes = uint32_t(nbox) * kGtBox * 128u + G::kBBytes;
                 for (int ks = i.k0; ks < i.k1; ++ks, ++st) {
                     const uint32_t s = st % STAGES, round = st / STAGES;
-                    if (round > 0) gt_wait(&empty[s], (round - 1) & 1, a.err, 50, s);
+                    if (round > 0 && !gt_wait(&empty[s], (round - 1) & 1, a.err, 50, s)) {
+                        ok = false;
+                        break;
+                    }
                     uint8_t* sa = base + s * STAGE;
                     uint8_t* sb = sa + kGtABytes;
                     const int r0 = ks * kGtK;
@@ -241,8 +245,11 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                             tma_load_2d(sb + j * kGtSub, &maps.b, b0 + 64 * j, i.slot0 + r0,
                                         &full[s]);
                     } else {
-                        for (int j = 0; j < (whole ? 1 : nbox); ++j)
-                            tma_load_2d(sa + j * (kGtBox * 128), ma, r0, i.arow + j * kGtBox, &full[s]);
+                        tma_load_2d(sa, ma, r0, i.arow, &full[s]);
+                        if (!whole)
+                            for (int j = 1; j < nbox; ++j)
+                                tma_load_2d(sa + j * (kGtBox * 128), ma, r0, i.arow + j * kGtBox,
+                                            &full[s]);
                         if (MODE == kGmmFwd) {
                             tma_load_3d(sb, &maps.b, r0, b0, i.e, &full[s]);
                         } else {
@@ -255,8 +262,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             }
             // every copy has landed (a pair's: has been consumed) before the CTA exits
             for (uint32_t k = st > STAGES ? st - STAGES : 0; k < st; ++k)
-                gt_wait(PAIR ? &empty[k % STAGES] : &full[k % STAGES], (k / STAGES) & 1, a.err, 51,
-                        k % STAGES);
+                mbar_wait(PAIR ? &empty[k % STAGES] : &full[k % STAGES], (k / STAGES) & 1);
         }
     } else if (wid == kGtMmaWarp) {
         const uint32_t idesc = idesc_f16(G::kBlock, BN, a.bf16) |
@@ -301,7 +307,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     if (PAIR) {
                         fence_proxy_async_all();
                         __syncwarp();
-                        if (rank == 0) gt_wait<true>(&fixed[s], (own_phase >> s) & 1u, a.err, 57, s);
+                        if (rank == 0)
+                            gt_wait<true>(&fixed[s], (own_phase >> s) & 1u, a.err, 57, s);
                         else if (elect_one()) mbar_arrive_rank0(&fixed[s]);
                         own_phase ^= 1u << s;
                     } else {

@@ -20,6 +20,11 @@ constexpr int kGtRows = 128;                    // tile rows
 constexpr int kGtBox = 32;                      // rows of the smaller row box
 
 // Bounded wait that gives up early once a timed-out wait has been latched.
+// A producer whose wait failed issues nothing more (a second expected count
+// in one phase would be undefined).  The other roles run on to their end over
+// values that nobody is to use: their arrivals only complete phases, and
+// stay within the CTA's own buffers.  (A check a stage that leaves the MMA
+// loop cost 5 %.)
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                         uint32_t site, uint32_t slot) {
@@ -31,7 +36,6 @@ __device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t
     latch_timeout(err, site, slot, parity, 0);
     return false;
 }
-
 // A CTA's (or CTA pair's) tiles in order: column tile c (of nt) fastest, then row block m, and
 // with MT row blocks an expert (dw) the expert e.  Steps of one tile a
 // worker are added digit by digit: a 64-bit division a tile took longer than the
