@@ -19,46 +19,6 @@ namespace {
 constexpr int kQThreads = 256;
 constexpr int kQAhead = 2;               // steps whose loads a warp has in flight
 
-// Where row `r` lies: its group's rows [first, end) and first row block, or
-// first = -1 for a row of no group (end = the next row that may have one).
-// Computed by a whole warp straight from the offsets: a warp works on
-// consecutive rows, so it looks a group up about once, and no table has to be
-// built by the CTA before the first row is read.
-struct RowGroup {
-    int first, end, block;
-};
-__device__ __forceinline__ RowGroup row_group(const int32_t* offsets, int E, int rows, int r,
-                                              uint32_t* err) {
-    if (offsets == nullptr) {
-        const int n = rows / E, e = r / n;
-        return RowGroup{e * n, (e + 1) * n, e * ((n + 127) / 128)};
-    }
-    int block = 0, first = -1, end = -1;
-    bool bad = false;
-    for (int e = int(threadIdx.x & 31); e < E; e += 32) {
-        const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
-        bad |= a < 0 || b < a || b > rows;
-        if (b <= r) {
-            block += (b - a + 127) / 128;
-        } else if (a <= r) {
-            first = a;
-            end = b;
-        }
-    }
-    if (__any_sync(0xffffffffu, bad)) {
-        if ((threadIdx.x & 31) == 0) latch(err, STRATA_EBADROUTE);
-        return RowGroup{-1, rows, 0};
-    }
-    block = __reduce_add_sync(0xffffffffu, block);
-    first = __reduce_max_sync(0xffffffffu, first);
-    end = __reduce_max_sync(0xffffffffu, end);
-    if (first < 0) {
-        const int o0 = __ldg(offsets);
-        return RowGroup{-1, r < o0 ? o0 : rows, 0};
-    }
-    return RowGroup{first, end, block};
-}
-
 // Eight values, already divided by the block's scale, as e2m1: rounded to
 // nearest, ties to the even code, saturated at 6.
 __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* y) {
@@ -253,7 +213,7 @@ __global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, i
     const float down = ldexpf(1.0f, -a.scale_exp);
     const T* x = static_cast<const T*>(a.x);
     Steps s = warp_steps(a.rows, steps);
-    RowGroup g{-1, -1, 0};
+    RowGroup g{-1, -1, 0, -1};
     while (s.left > 0) {
         const int row = s.row;
         if (row >= g.end) g = row_group(a.offsets, a.n_groups, a.rows, row, a.err);
@@ -321,7 +281,7 @@ __global__ void __launch_bounds__(kQThreads, 6) k_fp4_dequantize(Fp4DequantArgs 
     const float up = ldexpf(1.0f, a.scale_exp);
     T* out = static_cast<T*>(a.out);
     Steps s = warp_steps(a.rows, steps);
-    RowGroup g{-1, -1, 0};
+    RowGroup g{-1, -1, 0, -1};
     while (s.left > 0) {
         const int row = s.row;
         if (row >= g.end) g = row_group(a.offsets, a.n_groups, a.rows, row, a.err);

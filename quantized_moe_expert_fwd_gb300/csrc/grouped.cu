@@ -115,7 +115,10 @@ cudaError_t pick_simt(const GmmArgs& g, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_grouped_mm(GroupedMode mode, const GmmArgs& g, cudaStream_t s) {
-    if (mode == kGmmFwd && g.K % 8 == 0 && g.M <= kFewRowsMax) return launch_grouped_few(g, s);
+    if (mode == kGmmFwd && g.K % 8 == 0) {
+        if (g.M <= kFewRowsMax) return launch_grouped_few(g, s);
+        if (g.N <= kNarrowColsMax) return launch_grouped_narrow(g, s);
+    }
     if (grouped_tc_takes(mode, g)) return launch_grouped_tc(mode, g, s);
     switch (mode) {
         case kGmmFwd: return pick_simt<kGmmFwd>(g, s);

@@ -84,6 +84,47 @@ __device__ __forceinline__ int group_of_block(const GroupTable& t, int E, int b)
     return lo;
 }
 
+// Where row `r` lies: its group's rows [first, end) and first row block, or
+// first = -1 for a row of no group (end = the next row that may have one).
+// Computed by a whole warp straight from the offsets: a warp works on
+// consecutive rows, so it looks a group up about once, and no table has to be
+// built by the CTA before the first row is read.
+struct RowGroup {
+    int first, end, block, e;
+};
+__device__ __forceinline__ RowGroup row_group(const int32_t* offsets, int E, int rows, int r,
+                                              uint32_t* err) {
+    if (offsets == nullptr) {
+        const int n = rows / E, e = r / n;
+        return RowGroup{e * n, (e + 1) * n, e * ((n + 127) / 128), e};
+    }
+    int block = 0, first = -1, end = -1, group = -1;
+    bool bad = false;
+    for (int e = int(threadIdx.x & 31); e < E; e += 32) {
+        const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+        bad |= a < 0 || b < a || b > rows;
+        if (b <= r) {
+            block += (b - a + 127) / 128;
+        } else if (a <= r) {
+            first = a;
+            end = b;
+            group = e;
+        }
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+        if ((threadIdx.x & 31) == 0) latch(err, STRATA_EBADROUTE);
+        return RowGroup{-1, rows, 0, -1};
+    }
+    block = __reduce_add_sync(0xffffffffu, block);
+    first = __reduce_max_sync(0xffffffffu, first);
+    end = __reduce_max_sync(0xffffffffu, end);
+    if (first < 0) {
+        const int o0 = __ldg(offsets);
+        return RowGroup{-1, r < o0 ? o0 : rows, 0, -1};
+    }
+    return RowGroup{first, end, block, __reduce_max_sync(0xffffffffu, group)};
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
 template <>

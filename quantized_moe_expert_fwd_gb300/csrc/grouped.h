@@ -31,6 +31,9 @@ bool grouped_tc_takes(GroupedMode mode, const GmmArgs& g);
 // The forward product of at most kFewRowsMax rows on the CUDA cores.
 constexpr int kFewRowsMax = 8;
 cudaError_t launch_grouped_few(const GmmArgs& g, cudaStream_t s);
+// The forward product of at most kNarrowColsMax columns, there too.
+constexpr int kNarrowColsMax = 4;
+cudaError_t launch_grouped_narrow(const GmmArgs& g, cudaStream_t s);
 cudaError_t launch_grouped_tc(GroupedMode mode, const GmmArgs& g, cudaStream_t s);
 
 // Scales of `rows` rows by `cols` columns in `groups` groups, in bytes:

@@ -1,5 +1,5 @@
 // grouped_few.cu -- the forward product for a handful of rows (the slots of
-// one token): every touched expert's W is streamed through the CUDA cores.
+// one token) or of columns.  Rows: every touched expert's W is streamed through the CUDA cores.
 // The tensor-core kernel takes a reduction of 2048 as 32 pipeline stages in a
 // row, each a quarter of a microsecond however few rows there are; here all of
 // a warp's loads are in flight at once.
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kFewThreads = 256;
 constexpr int kFewX = 4;                 // x rows a pass over W serves
+constexpr int kNarrowCols = kNarrowColsMax;
 
 // The touched groups, keyed by their first row.
 struct FewTable {
@@ -127,11 +128,61 @@ __global__ void __launch_bounds__(kFewThreads) k_gmm_few(GmmArgs g) {
     }
 }
 
+// Few columns instead of few rows: a warp a row of x, every column's W row
+// from the caches (the warps of a CTA work on neighbouring rows, so mostly on
+// one expert's).  On the tensor cores a tile of any width takes every stage of
+// the reduction.  Tensor cores and here, us: 2500 rows of 317 experts, 1816
+// wide, 1 column 24.7 4.2, 4 columns 24.7 6.1, 8 columns 24.0 8.6; 32000 rows
+// of 4 experts, 4096 wide, 1 column 22.0 14.0, 4 columns 19.8 19.1, 8 columns
+// 18.9 30.7.  Hence at most 4 columns.
+template <bool BF16, typename TO>
+__global__ void __launch_bounds__(kFewThreads, 3) k_gmm_narrow(GmmArgs g) {
+    pdl_launch();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, pieces = g.K / 8;
+    const int warps = int(gridDim.x) * (kFewThreads / 32);
+    const int wi = int(blockIdx.x) * (kFewThreads / 32) + int(threadIdx.x >> 5);
+    const uint4* w = static_cast<const uint4*>(g.b);
+    TO* y = static_cast<TO*>(g.out);
+    RowGroup gr{-1, -1, 0, -1};
+    const int last = int((long long)g.M * (wi + 1) / warps);
+    for (int row = int((long long)g.M * wi / warps); row < last; ++row) {
+        if (row >= gr.end) gr = row_group(g.offsets, g.E, g.M, row, g.err);
+        if (gr.first < 0) {
+            row = gr.end - 1;
+            continue;
+        }
+        const uint4* x = static_cast<const uint4*>(g.a) + size_t(row) * pieces;
+        const uint4* we = w + size_t(gr.e) * g.N * pieces;
+        float acc[kNarrowCols] = {};
+        for (int p0 = lane; p0 < pieces; p0 += 32 * kFewLoads) {
+            uint4 v[kFewLoads];
+#pragma unroll
+            for (int l = 0; l < kFewLoads; ++l)
+                v[l] = p0 + 32 * l < pieces ? ldg_stream(x + p0 + 32 * l) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < kNarrowCols; ++n) {
+                if (n >= g.N) break;
+#pragma unroll
+                for (int l = 0; l < kFewLoads; ++l)
+                    if (p0 + 32 * l < pieces)
+                        acc[n] = dot8<BF16>(v[l], __ldg(we + size_t(n) * pieces + p0 + 32 * l), acc[n]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kNarrowCols; ++n) {
+            if (n >= g.N) break;
+            const float s = warp_sum(acc[n]);
+            if (lane == n) y[size_t(row) * g.N + n] = from_f32<TO>(s);
+        }
+    }
+}
+
 template <typename... P, typename A>
-cudaError_t few_launch(void (*kernel)(P...), int units, cudaStream_t s, const A& args) {
-    // at most two CTAs a SM: 16 warps keep 16 loads of 16 bytes a lane in flight
+cudaError_t few_launch(void (*kernel)(P...), int units, int per_sm, cudaStream_t s,
+                       const A& args) {
     const int want = (units + kFewThreads / 32 - 1) / (kFewThreads / 32);
-    const int most = device_info().sms * 2;
+    const int most = device_info().sms * per_sm;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(want < most ? want : most);
     cfg.blockDim = dim3(kFewThreads);
@@ -149,10 +200,19 @@ cudaError_t few_launch(void (*kernel)(P...), int units, cudaStream_t s, const A&
 cudaError_t launch_grouped_few(const GmmArgs& g, cudaStream_t s) {
     const int units = (g.M < g.E ? g.M : g.E) * ((g.N + kFewRows - 1) / kFewRows);
     if (g.dtype == STRATA_BF16)
-        return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_few<true, float>, units, s, g)
-                                         : few_launch(k_gmm_few<true, __nv_bfloat16>, units, s, g);
-    return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_few<false, float>, units, s, g)
-                                     : few_launch(k_gmm_few<false, __half>, units, s, g);
+        return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_few<true, float>, units, 2, s, g)
+                                         : few_launch(k_gmm_few<true, __nv_bfloat16>, units, 2, s, g);
+    return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_few<false, float>, units, 2, s, g)
+                                     : few_launch(k_gmm_few<false, __half>, units, 2, s, g);
+}
+
+cudaError_t launch_grouped_narrow(const GmmArgs& g, cudaStream_t s) {
+    if (g.dtype == STRATA_BF16)
+        return g.out_dtype == STRATA_F32
+                   ? few_launch(k_gmm_narrow<true, float>, g.M, 3, s, g)
+                   : few_launch(k_gmm_narrow<true, __nv_bfloat16>, g.M, 3, s, g);
+    return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_narrow<false, float>, g.M, 3, s, g)
+                                     : few_launch(k_gmm_narrow<false, __half>, g.M, 3, s, g);
 }
 
 }  // namespace strata

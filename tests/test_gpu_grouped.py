@@ -34,6 +34,7 @@ SHAPES = {
     "few_tiles_back": ([33, 0, 12], 200, 3016),
     "one_tile": ([100], 1048, 100),
     "narrow_out": ([60, 9, 130], 1992, 3),
+    "narrow_many": ([(5 * e) % 9 for e in range(200)], 1048, 4),
     "mid_groups": ([300, 129, 0, 1, 256, 255, 400, 350], 200, 144),
     "long_many": ([640 + 37 * (e % 5) for e in range(40)], 256, 392),
 }
@@ -106,7 +107,8 @@ def test_no_rows():
     _done(ws)
 
 
-@pytest.mark.parametrize("name", ["tile_edges", "token", "odd_wide", "unaligned"])
+@pytest.mark.parametrize("name", ["tile_edges", "token", "odd_wide", "unaligned", "narrow_out", "few_tiles",
+                                  "long_groups"])
 def test_rows_of_no_group_are_neither_read_nor_written(name):
     """Rows before the first and behind the last group hold NaN; outputs there stay."""
     first, spare = 3, 70
