@@ -81,12 +81,11 @@ __device__ __forceinline__ void gt_st8(void* p, const uint32_t* w) {
                  "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
-// WORDS words of a row, `have` bytes of which exist (aligned rows end with a
-// whole 16 bytes).
+// WORDS words of a row whose pieces of 32 bytes are aligned; `have` bytes of
+// them exist (a whole number of 16).
 template <int WORDS>
-__device__ __forceinline__ void gt_store_words(uint8_t* p, const uint32_t (&w)[WORDS], int vec,
-                                               int have) {
-    if (vec == 32 && have >= WORDS * 4) {
+__device__ __forceinline__ void gt_store_words(uint8_t* p, const uint32_t (&w)[WORDS], int have) {
+    if (have >= WORDS * 4) {
 #pragma unroll
         for (int i = 0; i < WORDS; i += 8) gt_st8(p + i * 4, w + i);
     } else {
@@ -94,6 +93,22 @@ __device__ __forceinline__ void gt_store_words(uint8_t* p, const uint32_t (&w)[W
         for (int i = 0; i < WORDS; i += 4)
             if (i * 4 < have)
                 *reinterpret_cast<uint4*>(p + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+}
+// The same of rows aligned to 16 bytes only, from the warp's staging (17
+// words a row): neighbouring lanes write a row's neighbouring 16 bytes.
+template <int WORDS>
+__device__ __forceinline__ void gt_store_staged(uint8_t* p, size_t pitch, int rows,
+                                                const uint32_t* stage, int have) {
+    constexpr int PER = WORDS / 4, STEP = 32 / PER;          // lanes a row, rows an instruction
+    const int lane = threadIdx.x & 31, q = lane % PER;
+    if (q * 16 >= have) return;
+#pragma unroll
+    for (int k = 0; k < 32 / STEP; ++k) {
+        const int r = k * STEP + lane / PER;
+        const uint32_t* s = stage + r * 17 + q * 4;
+        if (r < rows)
+            *reinterpret_cast<uint4*>(p + r * pitch + q * 16) = make_uint4(s[0], s[1], s[2], s[3]);
     }
 }
 __device__ __forceinline__ uint32_t gt_pack(float lo, float hi, int bf16) {
@@ -104,10 +119,11 @@ __device__ __forceinline__ uint32_t gt_pack(float lo, float hi, int bf16) {
 }
 // N columns (nv of them exist) of a warp's 32 output rows, `rows` of them
 // live, from each lane's fp32 values of its own row; `at` is the first row's
-// place, `pitch` the row length.  Rows that are not aligned go through shared
-// memory so that neighbouring lanes write neighbouring columns: a lane a row
-// wrote two bytes into each of 32 sectors at a time (118 columns of 3008
-// rows: 22 us, now 7).
+// place, `pitch` the row length.  Rows aligned to 32 bytes (vec) are written
+// by their lanes, whole sectors each.  Others go through shared memory, so
+// that neighbouring lanes write neighbouring columns: a lane a row wrote 2 or
+// 16 bytes into each of 32 sectors at a time (118 columns of 3008 rows: 22 us,
+// now 7; 1928 columns of 9056 rows: 23, now 19).
 constexpr uint32_t kGtStoreWords = 32 * 17;               // a warp's staging
 constexpr uint32_t kGtStoreBytes = kGtEpiWarps * kGtStoreWords * 4;
 template <bool F32, int N>
@@ -118,12 +134,12 @@ __device__ __forceinline__ void gt_store(void* out, size_t at, size_t pitch, int
     const int lane = threadIdx.x & 31;
     if (F32) {
         float* p = static_cast<float*>(out) + at;
-        if (vec) {
+        if (vec == 32) {
             uint32_t w[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) w[j] = __float_as_uint(v[j]);
             if (lane < rows)
-                gt_store_words(reinterpret_cast<uint8_t*>(p + lane * pitch), w, vec, nv * 4);
+                gt_store_words(reinterpret_cast<uint8_t*>(p + lane * pitch), w, nv * 4);
             return;
         }
         // 16 columns at a time, two rows an instruction
@@ -134,6 +150,11 @@ __device__ __forceinline__ void gt_store(void* out, size_t at, size_t pitch, int
 #pragma unroll
             for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = __float_as_uint(v[h + j]);
             __syncwarp();
+            if (vec) {
+                gt_store_staged<16>(reinterpret_cast<uint8_t*>(p + h), pitch * 4, rows, stage,
+                                    (nv - h) * 4);
+                continue;
+            }
             float* o = p + size_t(lane >> 4) * pitch + h + c;
             const uint32_t* s = stage + (lane >> 4) * 17 + c;
 #pragma unroll 4
@@ -145,15 +166,19 @@ __device__ __forceinline__ void gt_store(void* out, size_t at, size_t pitch, int
         uint32_t w[N / 2];
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) w[j] = gt_pack(v[2 * j], v[2 * j + 1], bf16);
-        if (vec) {
+        if (vec == 32) {
             if (lane < rows)
-                gt_store_words(reinterpret_cast<uint8_t*>(p + lane * pitch), w, vec, nv * 2);
+                gt_store_words(reinterpret_cast<uint8_t*>(p + lane * pitch), w, nv * 2);
             return;
         }
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) stage[lane * 17 + j] = w[j];
         __syncwarp();
+        if (vec) {
+            gt_store_staged<N / 2>(reinterpret_cast<uint8_t*>(p), pitch * 2, rows, stage, nv * 2);
+            return;
+        }
         constexpr int STEP = 32 / N;                        // rows an instruction
         const int c = lane % N;
         const uint16_t* s = reinterpret_cast<const uint16_t*>(stage) + (lane / N) * 34 + c;
