@@ -197,10 +197,9 @@ __device__ __forceinline__ Steps warp_steps(int rows, int steps) {
 // The 4 (NV) or 8 (MX) lanes of a scale word write it as one; units past the
 // row's end contribute the zeros of its last word.
 //
-// 16384 rows of 2048 (bf16, NV) gathered from 2048: 18 us before the steps
-// were dealt out evenly and the loads widened to 32 bytes.  Bound by
-// instructions (about 110 a unit) and, read from memory, by the 2.6 bytes an
-// element.
+// 16384 rows of 2048 in bf16: gathered from 2048 rows 15.0 us (MX) and 15.6
+// (NV), read from memory 15.3 and 16.2 (12.7 us of bytes; 19 and 20.5 with one
+// step's loads in flight).  Bound by instructions: about 185 a unit and warp.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, int wide) {
     __shared__ float recip[8];

@@ -10,6 +10,10 @@
 // quarters).  An NV scale word covers one K step (scale_vec::4X), an MX word
 // two (scale_vec::2X, the step's half of the word picked by the descriptor).
 //
+// Measured, NV, 16384 rows of 256 experts of 1024 x 2048 with SwiGLU: 56 us
+// (bytes at the copy's rate 50.5); 131072 rows of 8 experts of 2048 x 2048:
+// 286 us, 3.8 PFLOP/s, bound by the 36 KB a stage that every CTA takes from L2.
+//
 // Roles, buffers and waits as in grouped_tc.cu.  The epilogue multiplies by
 // alpha[e] and, for SwiGLU, joins the gate and up columns 2i and 2i + 1, which
 // one lane holds side by side.

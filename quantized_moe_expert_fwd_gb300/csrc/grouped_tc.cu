@@ -18,6 +18,12 @@
 // Persistent, one CTA of 10 warps per SM: warps 0..7 epilogue (warp w: lanes
 // 32 (w % 4) .. of column half w / 4), 8 TMA producer, 9 MMA.  Two
 // accumulator buffers, so a tile's epilogue overlaps the next tile's MMAs.
+// Long groups' tiles are made by pairs of CTAs, and few tiles' reductions are
+// split over a cluster (gt_pick has the rules and what they measured).
+//
+// Measured, 256 experts of 1024 x 2048 in bf16, 16384 rows (us; bytes at the
+// copy's rate 175.6): forward 183, dx 172, dw 193; 65536 rows into 32 experts,
+// dw in fp32: 203 (FLOPs at the burst rate 144.7).
 //
 // fp32 outputs: the tensor cores truncate as they add (relative error 2e-6 at
 // 2048 terms, growing with their number), so the accumulator is drained every
@@ -365,8 +371,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         float* part = reinterpret_cast<float*>(base) + r * kGtPartPitch + half * (BN / 2);
         uint32_t acc = 0;
         // dw: 128 bytes of each of the warp's 32 rows to memory by TMA, which
-        // writes whole lines (32-byte stores of a lane a row took 1.7 times
-        // as long); the lanes' 16-byte pieces are spread by the swizzle
+        // writes whole lines (32-byte stores of a lane a row: 304 us instead of
+        // 193 for 16384 rows into 256 experts); the lanes' 16-byte pieces are spread by the swizzle
         auto put = [&](const GtTile& i, int col, const uint32_t (&w)[32]) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();

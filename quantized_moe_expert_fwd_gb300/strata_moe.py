@@ -418,7 +418,8 @@ def moe_grouped_workspace_bytes() -> int:
 # compare integers, sizes and types directly and format nothing unless they
 # refuse.
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
-_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_get_device = getattr(torch._C, "_cuda_getDevice", None)          # None: torch without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _grouped(ws, stream, tensors):

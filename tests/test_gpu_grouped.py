@@ -107,6 +107,30 @@ def test_no_rows():
     _done(ws)
 
 
+def test_few_rows_of_no_group_and_nan():
+    """The kernel for a few rows: rows of no group, and a row of NaN beside finite ones."""
+    counts, first, spare = [1, 0, 2, 1], 1, 2
+    off = ref.offsets_of(counts, first).cuda()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(7, 520, generator=g, device="cuda").half()
+    w = torch.randn(4, 37, 520, generator=g, device="cuda").half()
+    x[0], x[5:] = float("nan"), float("nan")
+    y = torch.full((7, 37), 7.0, dtype=torch.float16, device="cuda")
+    ws = q.make_grouped_workspace()
+    q.moe_grouped_mm(x, w, off, y, ws)
+    want, mags = ref.mm(x, w, off)
+    assert (y[0] == 7).all() and (y[5:] == 7).all()
+    ref.check(y[1:5], want[1:5], mags[1:5], 520)
+    x[2, 519] = float("inf")
+    q.moe_grouped_mm(x, w, off, y, ws)
+    assert not torch.isfinite(y[2]).any()
+    ref.check(y[[1, 3, 4]], want[[1, 3, 4]], mags[[1, 3, 4]], 520)
+    for bad in ([1, 2, 1, 4, 5], [1, 2, 2, 4, 8]):
+        y.fill_(7)
+        q.moe_grouped_mm(x, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), y, ws)
+        assert q.moe_get_device_status(ws) == q.STRATA_EBADROUTE and (y == 7).all()
+
+
 @pytest.mark.parametrize("name", ["tile_edges", "token", "odd_wide", "unaligned", "narrow_out", "few_tiles",
                                   "long_groups"])
 def test_rows_of_no_group_are_neither_read_nor_written(name):
