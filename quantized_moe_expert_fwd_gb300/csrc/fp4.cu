@@ -125,28 +125,27 @@ template <int FMT, typename T>
 __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t amax, float down,
                                                int scale_exp, const float* recip, uint2& q) {
     const bool finite = amax < 0x7f800000u;
-    q = make_uint2(0u, 0u);
     float v[16];
+    // blocks without a finite scale above zero are computed along and replaced
+    // at the end: no branch
     if (FMT == 0) {
         // floor(log2 amax) - 2, at least -127: elements of the top binade
         // reach 4 .. 6 (above 6 they saturate)
         const int ex = max(int(amax >> 23) - 129, -127);
         const float inv = __uint_as_float(uint32_t(127 - ex) << 23);         // 2^-ex
-        if (!finite) return 255u;
-        if (amax == 0u) return 0u;
         raw_f32(raw, v);
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] *= inv;
-        q = make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(v + 8));
-        return uint32_t(ex + 127);
+        const bool codes = finite && amax != 0u;
+        q = make_uint2(codes ? cvt_e2m1x8(v) : 0u, codes ? cvt_e2m1x8(v + 8) : 0u);
+        return !finite ? 255u : codes ? uint32_t(ex + 127) : 0u;
     }
     const float top = __uint_as_float(amax) * down;
     const float want = sizeof(T) == 4 ? top / 6.0f : __fmul_rz(top, kSixthUp);
     uint16_t s2;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.0f), "f"(want));
     const uint32_t sbyte = uint32_t(s2 & 0xffu);
-    if (!finite) return 0x7fu;
-    if (sbyte == 0u) return 0u;
+    const bool codes = finite && sbyte != 0u;
     const float s = e4m3_to_f32(sbyte);
     raw_f32(raw, v);
     if constexpr (sizeof(T) == 4) {
@@ -161,7 +160,7 @@ __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t ama
             code |= __float_as_uint(v[j]) >> 31 << 3;
             w[j >> 3] |= code << (4 * (j & 7));
         }
-        q = make_uint2(w[0], w[1]);
+        q = make_uint2(codes ? w[0] : 0u, codes ? w[1] : 0u);
     } else {
         // the exponent of s and the tensor's power of two come off as integers
         const int e = int(__float_as_uint(s) >> 23) - 127 + scale_exp;
@@ -169,9 +168,9 @@ __device__ __forceinline__ uint32_t quantize16(const Raw16<T>& raw, uint32_t ama
             __float_as_uint(recip[__float_as_uint(s) >> 20 & 7u]) - (uint32_t(e) << 23));
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = __fmul_rz(v[j], inv);
-        q = make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(v + 8));
+        q = make_uint2(codes ? cvt_e2m1x8(v) : 0u, codes ? cvt_e2m1x8(v + 8) : 0u);
     }
-    return sbyte;
+    return finite ? sbyte : 0x7fu;
 }
 
 // The rows cut into steps of 512 columns (a lane 16 of them, a unit), a run of
@@ -186,13 +185,21 @@ struct Steps {
         step = 0;
     }
 };
-__device__ __forceinline__ Steps warp_steps(int rows, int steps) {
-    const long long total = (long long)rows * steps;
-    const int warps = int(gridDim.x) * (kQThreads / 32);
+// each, more: all warps take `each` steps, the first `more` one more.  (Worked
+// out by the host: the 64-bit divisions were a sixth of the instructions.)
+__device__ __forceinline__ Steps warp_steps(int steps, int each, int more) {
     const int w = int(blockIdx.x) * (kQThreads / 32) + int(threadIdx.x >> 5);
-    const long long lo = total * w / warps, hi = total * (w + 1) / warps;
-    return Steps{int(lo / steps), int(lo % steps), int(hi - lo)};
+    const long long lo = (long long)w * each + min(w, more);
+    const int left = each + (w < more ? 1 : 0);
+    if (lo < (1ll << 31)) {
+        const uint32_t l = uint32_t(lo), r = l / uint32_t(steps);
+        return Steps{int(r), int(l - r * uint32_t(steps)), left};
+    }
+    return Steps{int(lo / steps), int(lo % steps), left};
 }
+
+// 2^e for a small e.
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 
 // The 4 (NV) or 8 (MX) lanes of a scale word write it as one; units past the
 // row's end contribute the zeros of its last word.
@@ -201,7 +208,7 @@ __device__ __forceinline__ Steps warp_steps(int rows, int steps) {
 // (NV), read from memory 15.3 and 16.2 (12.7 us of bytes; 19 and 20.5 with one
 // step's loads in flight).  Bound by instructions: about 185 a unit and warp.
 template <int FMT, typename T>
-__global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, int wide) {
+__global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, int wide, int each, int more) {
     __shared__ float recip[8];
     if (threadIdx.x < 8) recip[threadIdx.x] = recip_up(threadIdx.x);
     __syncthreads();
@@ -209,9 +216,9 @@ __global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, i
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int units = a.cols / 16, words = fp4_words(a.cols, FMT), steps = (units + 31) / 32;
-    const float down = ldexpf(1.0f, -a.scale_exp);
+    const float down = pow2f(-a.scale_exp);
     const T* x = static_cast<const T*>(a.x);
-    Steps s = warp_steps(a.rows, steps);
+    Steps s = warp_steps(steps, each, more);
     RowGroup g{-1, -1, 0, -1};
     while (s.left > 0) {
         const int row = s.row;
@@ -272,14 +279,14 @@ __global__ void __launch_bounds__(kQThreads, 4) k_fp4_quantize(Fp4QuantArgs a, i
 }
 
 template <int FMT, typename T>
-__global__ void __launch_bounds__(kQThreads, 6) k_fp4_dequantize(Fp4DequantArgs a, int wide) {
+__global__ void __launch_bounds__(kQThreads, 6) k_fp4_dequantize(Fp4DequantArgs a, int wide, int each, int more) {
     pdl_launch();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int units = a.cols / 16, words = fp4_words(a.cols, FMT), steps = (units + 31) / 32;
-    const float up = ldexpf(1.0f, a.scale_exp);
+    const float up = pow2f(a.scale_exp);
     T* out = static_cast<T*>(a.out);
-    Steps s = warp_steps(a.rows, steps);
+    Steps s = warp_steps(steps, each, more);
     RowGroup g{-1, -1, 0, -1};
     while (s.left > 0) {
         const int row = s.row;
@@ -339,9 +346,11 @@ cudaError_t launch_steps(void (*kernel)(P...), int per_sm, cudaStream_t s, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    const long long warps = (long long)cfg.gridDim.x * (kQThreads / 32);
     // rows are multiples of 64 bytes, so the base decides for all of them
     return cudaLaunchKernelEx(&cfg, kernel, args,
-                              int((reinterpret_cast<uintptr_t>(wide_base) & 31u) == 0));
+                              int((reinterpret_cast<uintptr_t>(wide_base) & 31u) == 0),
+                              int(steps / warps), int(steps % warps));
 }
 
 template <int FMT>
