@@ -17,12 +17,7 @@
 
 namespace strata {
 
-template <int FMT>
-struct Fp4 {
-    static constexpr int kVec = FMT == 0 ? 32 : 16;      // elements a scale
-    static constexpr int kWord = 4 * kVec;               // elements a 4-byte scale word
-};
-
+// Scale words of a row.
 __host__ __device__ constexpr int fp4_words(int cols, int fmt) {
     return (cols + (fmt == 0 ? 127 : 63)) / (fmt == 0 ? 128 : 64);
 }
