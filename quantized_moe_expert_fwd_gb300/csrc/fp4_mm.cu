@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                     bulk_g2s(sf + C::kSf, sb_g + size_t(w0) * 512, sf_bytes, &full[s]);
                 }
             }
-            // every copy has landed before the CTA exits
+            // every copy has landed and has been consumed before the CTA exits
             for (uint32_t k = st > C::kStages ? st - C::kStages : 0; k < st; ++k)
-                mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
+                mbar_wait(&empty[k % C::kStages], (k / C::kStages) & 1);
         }
     } else if (wid >= kF4SfWarp) {
         // one operand's scales of each stage to tensor memory, on a thread of

@@ -266,9 +266,10 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     }
                 }
             }
-            // every copy has landed (a pair's: has been consumed) before the CTA exits
+            // every copy has landed, has been consumed, and the MMAs' arrivals are
+            // here, before the CTA exits
             for (uint32_t k = st > STAGES ? st - STAGES : 0; k < st; ++k)
-                mbar_wait(PAIR ? &empty[k % STAGES] : &full[k % STAGES], (k / STAGES) & 1);
+                mbar_wait(&empty[k % STAGES], (k / STAGES) & 1);
         }
     } else if (wid == kGtMmaWarp) {
         const uint32_t idesc = idesc_f16(G::kBlock, BN, a.bf16) |
@@ -360,6 +361,12 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         }
         __syncwarp();
         gt_wait(&done, 0, a.err, 54, 0);
+        // The other CTA's last arrivals at acc_empty.  The cluster barrier at the
+        // end does not cover them: one that came after this CTA's exit counted
+        // on a barrier of the CTA that followed it on the SM.
+        if (PAIR && rank == 0)
+            for (uint32_t k = acc > 2 ? acc - 2 : 0; k < acc; ++k)
+                gt_wait<true>(&acc_empty[k & 1u], (k >> 1) & 1, a.err, 58, k & 1u);
     } else {
         constexpr int CH = BN / 64;              // 32-column pieces of a warp's half
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
