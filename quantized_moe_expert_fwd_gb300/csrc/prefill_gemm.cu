@@ -76,6 +76,7 @@ constexpr uint32_t kSabWBytes = kBM * kSabWRowBytes;
 constexpr int kSabWStages = 3;
 static_assert(kSabStages * kSabACols + kSabACol0 <= kSabTmemCols, "TMEM columns");
 static_assert(kSabKS / 2 == int(kSabWRowBytes), "one weight stage a pipeline stage");
+static_assert(kSabWStages >= kSabStages, "a finished stage's weight slot use has landed");
 
 // A tile's scales land as [K / 256][128 rows][8 fp16]: the 8 scales of a
 // row for 256 inputs (one pipeline stage) side by side, so a stage's read
@@ -398,13 +399,21 @@ __global__ void __launch_bounds__(kSabThreads, 1)
                 }
                 if ((kst & 1u) != set) continue;
                 const uint32_t s = kst & (kSabStages - 1), round = kst / kSabStages;
-                if (!sab_wait(&wfull[cws], cwph, a.err)) latch_timeout(a.err, 37, cws, kst, tile);
                 const uint32_t wrow_s = smem_u32(w_base + cws * kSabWBytes) + uint32_t(m * 128);
                 // the stage's 8 scales (two a 64-wide sub-block)
                 const uint4 sc8 = lds128(scrow + uint32_t(ks) * (kBM * 16u));
                 const uint32_t scw[4] = {sc8.x, sc8.y, sc8.z, sc8.w};
                 if (round > 0 && !sab_wait(&empty[s], (round - 1) & 1, a.err))
                     latch_timeout(a.err, 38, s, round, tile);
+                // Only then the weights.  This set takes every second use of a
+                // weight slot (an odd number of slots, two sets), and a wait
+                // on a parity cannot tell the use before last from this one
+                // while the other set's use between them, step kst -
+                // kSabWStages, is still to land; copies land in any order.
+                // The wait above rules that out: the products of step kst -
+                // kSabStages are done, and they take the steps in order, so
+                // the other set has converted step kst - kSabWStages.
+                if (!sab_wait(&wfull[cws], cwph, a.err)) latch_timeout(a.err, 37, cws, kst, tile);
                 tc_fence_after();
 #pragma unroll
                 for (int sb = 0; sb < kSabKS / 64; ++sb) {
