@@ -361,9 +361,9 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         }
         __syncwarp();
         gt_wait(&done, 0, a.err, 54, 0);
-        // The other CTA's last arrivals at acc_empty.  The cluster barrier at the
-        // end does not cover them: one that came after this CTA's exit counted
-        // on a barrier of the CTA that followed it on the SM.
+        // The other CTA's last arrivals at acc_empty have to be here too before
+        // this CTA exits: one under way then would count on a barrier of the
+        // CTA that follows it on the SM.
         if (PAIR && rank == 0)
             for (uint32_t k = acc > 2 ? acc - 2 : 0; k < acc; ++k)
                 gt_wait<true>(&acc_empty[k & 1u], (k >> 1) & 1, a.err, 58, k & 1u);
