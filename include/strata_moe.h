@@ -392,9 +392,9 @@ STRATA_API strata_status moe_layer_bucketing(const strata_moe_dims* dims, int32_
  * device (int32 [E + 1], non-decreasing, within [0, M]); offsets that run
  * backwards anywhere or leave [0, M] latch STRATA_EBADROUTE, and every group
  * of that call counts as empty.
- *   - E in [1, 1024], M >= 0, K and N in [1, 2^20] unless a call says less.
- *     M == 0 launches nothing, except that moe_grouped_mm_dw still writes
- *     its zeros.
+ *   - E in [1, 1024], M in [0, 2^31 - 1024], K and N in [1, 2^20] unless a
+ *     call says less.  M == 0 launches nothing, except that moe_grouped_mm_dw
+ *     still writes its zeros.
  *   - Every tensor is contiguous, 16-byte aligned (offsets and alpha 4);
  *     outputs must not overlap inputs.
  *   - ws_dev: at least moe_grouped_workspace_bytes() bytes, with the rules

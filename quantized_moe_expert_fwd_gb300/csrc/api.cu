@@ -1014,6 +1014,8 @@ strata_status moe_layer_bucketing(const strata_moe_dims* dims, int32_t T, const 
 namespace {
 
 constexpr int kGroupedDimMax = 1 << 20;
+// A group's rows plus a tile's height (256 at most) are counted in 32 bits.
+constexpr int kGroupedRowsMax = INT32_MAX - 1023;
 
 bool grouped_ws_ok(const void* ws, size_t bytes) {
     return ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 &&
@@ -1026,7 +1028,7 @@ strata_status grouped_mm(GroupedMode mode, int32_t dtype, const void* a, const v
     if ((dtype != STRATA_BF16 && dtype != STRATA_F16) ||
         (out_dtype != dtype && out_dtype != STRATA_F32))
         return STRATA_EINVAL;
-    if (M < 0 || K < 1 || N < 1 || K > kGroupedDimMax || N > kGroupedDimMax || E < 1 ||
+    if (M < 0 || M > kGroupedRowsMax || K < 1 || N < 1 || K > kGroupedDimMax || N > kGroupedDimMax || E < 1 ||
         E > kMaxExperts)
         return STRATA_EINVAL;
     if (M == 0 && mode != kGmmDw) return STRATA_OK;
@@ -1052,7 +1054,7 @@ strata_status grouped_mm(GroupedMode mode, int32_t dtype, const void* a, const v
 
 bool fp4_shape_ok(int32_t format, int32_t rows, int32_t cols, int32_t n_groups, bool ragged) {
     if (format != STRATA_FP4_MX && format != STRATA_FP4_NV) return false;
-    if (rows < 0 || cols < 32 || cols > kGroupedDimMax || cols % 32 != 0) return false;
+    if (rows < 0 || rows > kGroupedRowsMax || cols < 32 || cols > kGroupedDimMax || cols % 32 != 0) return false;
     if (n_groups < 1 || n_groups > kMaxExperts) return false;
     return ragged || rows % n_groups == 0;
 }
