@@ -1028,8 +1028,8 @@ strata_status grouped_mm(GroupedMode mode, int32_t dtype, const void* a, const v
     if ((dtype != STRATA_BF16 && dtype != STRATA_F16) ||
         (out_dtype != dtype && out_dtype != STRATA_F32))
         return STRATA_EINVAL;
-    if (M < 0 || M > kGroupedRowsMax || K < 1 || N < 1 || K > kGroupedDimMax || N > kGroupedDimMax || E < 1 ||
-        E > kMaxExperts)
+    if (M < 0 || M > kGroupedRowsMax || K < 1 || N < 1 || K > kGroupedDimMax ||
+        N > kGroupedDimMax || E < 1 || E > kMaxExperts)
         return STRATA_EINVAL;
     if (M == 0 && mode != kGmmDw) return STRATA_OK;
     // an empty slot space has no rows to point at
@@ -1054,7 +1054,8 @@ strata_status grouped_mm(GroupedMode mode, int32_t dtype, const void* a, const v
 
 bool fp4_shape_ok(int32_t format, int32_t rows, int32_t cols, int32_t n_groups, bool ragged) {
     if (format != STRATA_FP4_MX && format != STRATA_FP4_NV) return false;
-    if (rows < 0 || rows > kGroupedRowsMax || cols < 32 || cols > kGroupedDimMax || cols % 32 != 0) return false;
+    if (rows < 0 || rows > kGroupedRowsMax) return false;
+    if (cols < 32 || cols > kGroupedDimMax || cols % 32 != 0) return false;
     if (n_groups < 1 || n_groups > kMaxExperts) return false;
     return ragged || rows % n_groups == 0;
 }

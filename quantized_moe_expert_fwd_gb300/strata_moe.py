@@ -439,6 +439,13 @@ def _grouped(ws, stream, tensors):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _int32(*values):
+    """Refuses sizes that the library's 32-bit arguments cannot hold (ctypes would pass them on
+    modulo 2^32)."""
+    if max(values) > 0x7fffffff or min(values) < -0x80000000:
+        raise ValueError("sizes and numbers passed to strata_moe must fit in 32 bits")
+
+
 def _dtype(t, what, allowed=_DTYPES):
     d = allowed.get(t.dtype)
     if d is None:
@@ -462,6 +469,7 @@ def _shape(t, shape, what):
 
 
 def _grouped_mm(fn, a, b, offsets, out, ws, stream, M, K, N, E):
+    _int32(M, K, N, E)
     st = _grouped(ws, stream, (a, b, offsets, out))
     dt = _dtype(a, "the operands", _DTYPES16)
     if b.dtype is not a.dtype:
@@ -508,8 +516,12 @@ def moe_grouped_mm_dw(dy, x, offsets, dw, ws, stream=None):
 
 def moe_fp4_scale_bytes(fmt: int, rows: int, cols: int, n_groups: int = 1,
                         ragged: bool = False) -> int:
-    return int(load().moe_fp4_scale_bytes(int(fmt), int(rows), int(cols), int(n_groups),
-                                          1 if ragged else 0))
+    args = int(fmt), int(rows), int(cols), int(n_groups)
+    try:
+        _int32(*args)
+    except ValueError:
+        return 0                                       # as for all that the calls refuse
+    return int(load().moe_fp4_scale_bytes(*args, 1 if ragged else 0))
 
 
 def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1,
@@ -518,12 +530,13 @@ def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1
     scales, in groups by offsets, or n_groups equal ones; row s from x's row
     perm[s] / top_k where perm (int32) is given, which may be shorter than q
     when offsets end with it."""
+    R, C = x.shape
+    rows, half = q.shape
+    _int32(R, C, rows, fmt, n_groups, scale_exp, top_k)
     st = _grouped(ws, stream, [t for t in (x, q, scales, offsets, perm) if t is not None])
     dt = _dtype(x, "x")
     if q.dtype is not _U8 or scales.dtype is not _U8:
         raise TypeError("codes and scales must be uint8")
-    R, C = x.shape
-    rows, half = q.shape
     if 2 * half != C:
         raise ValueError(f"q must have shape {(rows, C // 2)}, not {tuple(q.shape)}")
     if offsets is not None:
@@ -544,11 +557,12 @@ def moe_fp4_quantize(x, q, scales, fmt: int, ws, offsets=None, n_groups: int = 1
 def moe_fp4_dequantize(q, scales, out, fmt: int, ws, offsets=None, n_groups: int = 1,
                        scale_exp: int = 0, stream=None):
     """The values of quantised rows into out [rows][C] (bf16, fp16 or fp32)."""
+    rows, C = out.shape
+    _int32(rows, C, fmt, n_groups, scale_exp)
     st = _grouped(ws, stream, [t for t in (q, scales, out, offsets) if t is not None])
     od = _dtype(out, "out")
     if q.dtype is not _U8 or scales.dtype is not _U8:
         raise TypeError("codes and scales must be uint8")
-    rows, C = out.shape
     _shape(q, (rows, C // 2), "q")
     if offsets is not None:
         n_groups = _offsets(offsets)
@@ -565,12 +579,13 @@ def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
     """y[s] = alpha[e] W[e] x[s] of two 4-bit operands (xq uint8 [M][K / 2] in
     groups by offsets, wq uint8 [E][N][K / 2]; scales tiled), or the SwiGLU of
     its interleaved gate/up rows (y [M][N / 2])."""
+    E, N, half = wq.shape
+    M = xq.shape[0]
+    _int32(M, 2 * half, N, E, fmt)
     st = _grouped(ws, stream, (xq, xs, wq, wsc, offsets, y) if alpha is None
                   else (xq, xs, wq, wsc, offsets, y, alpha))
-    E, N, half = wq.shape
     if not (xq.dtype is _U8 and xs.dtype is _U8 and wq.dtype is _U8 and wsc.dtype is _U8):
         raise TypeError("codes and scales must be uint8")
-    M = xq.shape[0]
     _shape(xq, (M, half), "xq")
     _shape(y, (M, N // 2 if swiglu else N), "y")
     _offsets(offsets, E)
