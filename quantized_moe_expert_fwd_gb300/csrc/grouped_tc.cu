@@ -25,11 +25,12 @@
 // copy's rate 175.6): forward 183, dx 172, dw 193; 65536 rows into 32 experts,
 // dw in fp32: 203 (FLOPs at the burst rate 144.7).
 //
-// fp32 outputs: the tensor cores truncate as they add (relative error 2e-6 at
-// 2048 terms, growing with their number), so the accumulator is drained every
-// 512 terms into fp32 registers of the epilogue, where it is added with
-// rounding (5e-7 at any length).  16-bit outputs round away far more than
-// that and take the whole reduction in one accumulator.
+// The tensor cores truncate as they add, so terms of one sign lose about 1e-7
+// of the sum with every 16 of them (16-bit outputs of 2^18 such terms in one
+// accumulator: 1.7e-3 off).  The accumulator is therefore drained into fp32
+// registers of the epilogue, where the pieces are added with rounding: every
+// 512 terms for fp32 outputs, every 2048 for 16-bit ones (a loss of 1.3e-5,
+// next to half steps of 4.9e-4 and 3.9e-3).
 #include "grouped_tc.cuh"
 
 namespace strata {
@@ -37,7 +38,13 @@ namespace strata {
 namespace {
 
 constexpr int kGtK = 64;                        // reduction of a stage (128 bytes)
-constexpr int kGtPromote = 8;                   // stages between drains of an fp32 output
+// What a kernel writes: 16-bit outputs of a reduction of one piece, of any
+// number of pieces, and fp32.  (Forward with the single-piece kernel and with
+// the other, 32 experts of 1024 x 2048: 28.4 and 29.1 us at 64 rows a group,
+// 31.9 and 32.7 at 128, 58.4 and 59.2 at 512.)
+constexpr int kGt16 = 0, kGt16Pieces = 1, kGt32 = 2;
+// Stages of a piece (between two drains), for fp32 and for 16-bit outputs.
+constexpr int kGtDrain32 = 8, kGtDrain16 = 32;
 constexpr uint32_t kGtABytes = kGtRows * 128;
 constexpr uint32_t kGtSub = 64 * 128;           // a 64 x 64 MN-major sub-block
 
@@ -137,12 +144,14 @@ __device__ __forceinline__ void gt_part(float* p, const float* v) {
         *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
 }
 
-template <int MODE, int BN, bool F32, int CL>
+template <int MODE, int BN, int OUT, int CL>
 __global__ void __launch_bounds__(kGtThreads, 1)
     k_gmm_tc(const __grid_constant__ GtMaps maps, GtArgs a) {
     using G = Gt<MODE, BN, CL>;
     constexpr bool PAIR = CL == kGtPair, SPLIT = CL == kGtSplit;
     constexpr int STAGES = G::kStages;
+    constexpr bool F32 = OUT == kGt32, PIECES = OUT != kGt16;
+    constexpr int PIECE = F32 ? kGtDrain32 : kGtDrain16;
     constexpr uint32_t STAGE = G::kStage;
     extern __shared__ uint8_t gt_dyn[];
     __shared__ GroupTable t;
@@ -284,8 +293,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             for (int ks = i.k0; ks < i.k1; ++ks, ++st) {
                 const uint32_t s = st % STAGES;
                 const int nth = ks - i.k0;
-                const bool first = F32 ? nth % kGtPromote == 0 : nth == 0;
-                const bool last = ks == i.k1 - 1 || (F32 && nth % kGtPromote == kGtPromote - 1);
+                const bool first = PIECES ? nth % PIECE == 0 : nth == 0;
+                const bool last = ks == i.k1 - 1 || (PIECES && nth % PIECE == PIECE - 1);
                 const uint32_t buf = acc & 1u;
                 if ((!PAIR || rank == 0) && first && acc >= 2)
                     gt_wait<PAIR>(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 52, buf);
@@ -400,13 +409,49 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             const int c0 = i.c0 + half * (BN / 2);
             const size_t at = (i.orow + r - lane) * size_t(cols) + c0;
             const int live = min(32, i.rows - (r - lane));       // of the warp's rows
-            if (F32) {
+            auto taken = [&](uint32_t buf) {             // the accumulator is free again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_rank0(&acc_empty[buf]);
+                    else mbar_arrive(&acc_empty[buf]);
+                }
+            };
+            if constexpr (!PIECES) {             // stored as it is read
+                const uint32_t buf = acc & 1u;
+                if (i.k1 > i.k0) {
+                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t v[32];
+                    if (i.k1 > i.k0) {
+                        tmem_ld32(tl + buf * BN + c * 32, v);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+                    const float* f = reinterpret_cast<const float*>(v);
+                    if (SPLIT) gt_part(part + c * 32, f);
+                    else
+                        gt_store<false, 32>(a.out, at + c * 32, cols, live, f, cols - c0 - c * 32,
+                                            a.vec, a.bf16, store);
+                }
+                if (i.k1 > i.k0) {
+                    taken(buf);
+                    ++acc;
+                }
+            } else {
+                // The accumulator is free before the stores (dw, an output tile for
+                // every few stages, 512 rows a group: 62 -> 55 us).
                 float sum[CH][32];
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
-                for (int ks = i.k0; ks < i.k1; ks += kGtPromote, ++acc) {
+                for (int ks = i.k0; ks < i.k1; ks += PIECE, ++acc) {
                     const uint32_t buf = acc & 1u;
                     gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
                     tc_fence_after();
@@ -418,65 +463,24 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) sum[c][j] += __uint_as_float(v[j]);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR) mbar_arrive_rank0(&acc_empty[buf]);
-                        else mbar_arrive(&acc_empty[buf]);
-                    }
+                    taken(buf);
                 }
-                if (MODE == kGmmDw) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        put(i, c0 + c * 32, reinterpret_cast<const uint32_t(&)[32]>(sum[c]));
-                } else {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        if (SPLIT) gt_part(part + c * 32, sum[c]);
-                        else
-                            gt_store<true, 32>(a.out, at + c * 32, cols, live, sum[c],
-                                               cols - c0 - c * 32, a.vec, 0, store);
-                    }
-                }
-            } else {
-                const uint32_t buf = acc & 1u;
-                if (i.k1 > i.k0) {
-                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
-                    tc_fence_after();
-                }
-                uint32_t w[32];                  // dw: 64 columns, packed
+                uint32_t w[32];                      // dw in 16 bits: 64 columns, packed
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    uint32_t v[32];
-                    if (i.k1 > i.k0) {
-                        tmem_ld32(tl + buf * BN + c * 32, v);
-                        tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0u;
-                    }
-                    if (MODE == kGmmDw) {
+                    if (MODE == kGmmDw && F32) {
+                        put(i, c0 + c * 32, reinterpret_cast<const uint32_t(&)[32]>(sum[c]));
+                    } else if (MODE == kGmmDw) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            w[16 * (c & 1) + j] = gt_pack(__uint_as_float(v[2 * j]),
-                                                          __uint_as_float(v[2 * j + 1]), a.bf16);
+                            w[16 * (c & 1) + j] = gt_pack(sum[c][2 * j], sum[c][2 * j + 1], a.bf16);
                         if (c & 1) put(i, c0 + (c - 1) * 32, w);
                     } else if (SPLIT) {
-                        gt_part(part + c * 32, reinterpret_cast<const float*>(v));
+                        gt_part(part + c * 32, sum[c]);
                     } else {
-                        gt_store<false, 32>(a.out, at + c * 32, cols, live,
-                                            reinterpret_cast<const float*>(v), cols - c0 - c * 32,
-                                            a.vec, a.bf16, store);
+                        gt_store<F32, 32>(a.out, at + c * 32, cols, live, sum[c], cols - c0 - c * 32,
+                                          a.vec, a.bf16, store);
                     }
-                }
-                if (i.k1 > i.k0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR) mbar_arrive_rank0(&acc_empty[buf]);
-                        else mbar_arrive(&acc_empty[buf]);
-                    }
-                    ++acc;
                 }
             }
         }
@@ -530,8 +534,9 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 }
 
 // ------------------------------------------------------------------- host
-template <int MODE, int BN, bool F32, int CL>
+template <int MODE, int BN, int OUT, int CL>
 cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
+    constexpr bool F32 = OUT == kGt32;
     GtMaps m;
     bool ok = true;
     const uint64_t rows = uint64_t(g.M > 0 ? g.M : 1);
@@ -560,14 +565,18 @@ cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
     a.bf16 = g.dtype == STRATA_BF16;
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
     a.vec = gt_vec(g.out, pitch);
-    return gt_launch<k_gmm_tc<MODE, BN, F32, CL>>(kGtThreads, cluster, grid, Gt<MODE, BN, CL>::kDyn,
+    return gt_launch<k_gmm_tc<MODE, BN, OUT, CL>>(kGtThreads, cluster, grid, Gt<MODE, BN, CL>::kDyn,
                                                   s, m, a);
 }
 
 template <int MODE, int BN, int CL>
 cudaError_t gt_typed(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
-    return g.out_dtype == STRATA_F32 ? gt_run<MODE, BN, true, CL>(g, cluster, grid, s)
-                                     : gt_run<MODE, BN, false, CL>(g, cluster, grid, s);
+    if (g.out_dtype == STRATA_F32) return gt_run<MODE, BN, kGt32, CL>(g, cluster, grid, s);
+    // dw's reduction is a group's rows, which only the device knows
+    if constexpr (MODE != kGmmDw)
+        if ((MODE == kGmmFwd ? g.K : g.N) <= kGtDrain16 * kGtK)
+            return gt_run<MODE, BN, kGt16, CL>(g, cluster, grid, s);
+    return gt_run<MODE, BN, kGt16Pieces, CL>(g, cluster, grid, s);
 }
 
 // Which tiles.  dw: a CTA pair from 512 rows a group on average (us, 32
