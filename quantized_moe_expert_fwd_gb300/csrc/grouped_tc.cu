@@ -594,36 +594,37 @@ cudaError_t gt_typed(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
 template <int MODE>
 cudaError_t gt_pick(const GmmArgs& g, cudaStream_t s) {
     const int sms = device_info().sms, pairs = sms >= 2 ? sms / 2 * 2 : 2;
-    if (MODE == kGmmDw) {
+    if constexpr (MODE == kGmmDw) {
         if (g.M / g.E >= 512) return gt_typed<MODE, 256, kGtPair>(g, 2, pairs, s);
         return gt_typed<MODE, 256, 0>(g, 1, sms, s);
+    } else {
+        const long long cols = MODE == kGmmFwd ? g.N : g.K;
+        const int stages = ((MODE == kGmmFwd ? g.K : g.N) + kGtK - 1) / kGtK;
+        const long long groups = g.M < g.E ? g.M : g.E;
+        const long long nt128 = (cols + 127) / 128, nt256 = (cols + 255) / 256;
+        auto blocks = [&](int rows) {
+            const long long b = g.M / rows + groups / 2;
+            return b > groups ? b : groups;
+        };
+        auto cost = [&](long long tiles, int workers, double stage) {
+            return double((tiles + workers - 1) / workers) * stages * stage;
+        };
+        const double c128 = cost(blocks(128) * nt128, sms, 0.25);
+        const double c256 = cost(blocks(128) * nt256, sms, 0.385);
+        const double cpair = cost(blocks(256) * nt256, pairs / 2, 0.35);
+        // the most tiles that the offsets can make, so that a cluster takes one
+        const long long most = (groups + g.M / kGtRows) * nt128;
+        for (int parts = 8; parts >= 2; parts /= 2) {
+            // clusters of 8 do not fill every part of the GPU
+            if (most * parts > (parts == 8 ? sms - 24 : sms) || stages < 4 * parts) continue;
+            const double split = (stages + parts - 1) / parts * 0.25 + 1.5;
+            if (split < c128 && split < c256 && split < cpair)
+                return gt_typed<MODE, 128, kGtSplit>(g, parts, int(most) * parts, s);
+        }
+        if (cpair < c128 && cpair < c256) return gt_typed<MODE, 256, kGtPair>(g, 2, pairs, s);
+        if (c128 < c256) return gt_typed<MODE, 128, 0>(g, 1, sms, s);
+        return gt_typed<MODE, 256, 0>(g, 1, sms, s);
     }
-    const long long cols = MODE == kGmmFwd ? g.N : g.K;
-    const int stages = ((MODE == kGmmFwd ? g.K : g.N) + kGtK - 1) / kGtK;
-    const long long groups = g.M < g.E ? g.M : g.E;
-    const long long nt128 = (cols + 127) / 128, nt256 = (cols + 255) / 256;
-    auto blocks = [&](int rows) {
-        const long long b = g.M / rows + groups / 2;
-        return b > groups ? b : groups;
-    };
-    auto cost = [&](long long tiles, int workers, double stage) {
-        return double((tiles + workers - 1) / workers) * stages * stage;
-    };
-    const double c128 = cost(blocks(128) * nt128, sms, 0.25);
-    const double c256 = cost(blocks(128) * nt256, sms, 0.385);
-    const double cpair = cost(blocks(256) * nt256, pairs / 2, 0.35);
-    // the most tiles that the offsets can make, so that a cluster takes one
-    const long long most = (groups + g.M / kGtRows) * nt128;
-    for (int parts = 8; parts >= 2; parts /= 2) {
-        // clusters of 8 do not fill every part of the GPU
-        if (most * parts > (parts == 8 ? sms - 24 : sms) || stages < 4 * parts) continue;
-        const double split = (stages + parts - 1) / parts * 0.25 + 1.5;
-        if (split < c128 && split < c256 && split < cpair)
-            return gt_typed<MODE, 128, kGtSplit>(g, parts, int(most) * parts, s);
-    }
-    if (cpair < c128 && cpair < c256) return gt_typed<MODE, 256, kGtPair>(g, 2, pairs, s);
-    if (c128 < c256) return gt_typed<MODE, 128, 0>(g, 1, sms, s);
-    return gt_typed<MODE, 256, 0>(g, 1, sms, s);
 }
 
 }  // namespace
