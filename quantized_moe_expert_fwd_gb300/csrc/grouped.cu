@@ -11,6 +11,9 @@ namespace strata {
 namespace {
 
 constexpr int kSimtTile = 64, kSimtK = 16, kSimtThreads = 256;
+// Terms of a partial sum.  Added one by one, 2^18 equal terms came out 2e-3
+// off: within a binade all their roundings go one way.
+constexpr int kSimtPiece = 512;
 
 // One 64 x 64 output tile a CTA step, 4 x 4 outputs a thread, operands
 // through shared memory as fp32.
@@ -44,8 +47,18 @@ __global__ void __launch_bounds__(kSimtThreads) k_gmm_simt(GmmArgs g) {
             rows = min(kSimtTile, t.cnt[e] - in);
             red = MODE == kGmmFwd ? g.K : g.N;
         }
-        float acc[4][4] = {};
+        float sum[4][4] = {}, acc[4][4] = {};
+        auto join = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum[i][j] += acc[i][j];
+                    acc[i][j] = 0.0f;
+                }
+        };
         for (int k0 = 0; k0 < red; k0 += kSimtK) {
+            if (k0 % kSimtPiece == 0) join();
             __syncthreads();
             for (int i = threadIdx.x; i < kSimtTile * kSimtK; i += kSimtThreads) {
                 // the lane order follows memory: along k, or along the tile where
@@ -85,6 +98,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_gmm_simt(GmmArgs g) {
                     for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
             }
         }
+        join();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -92,7 +106,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_gmm_simt(GmmArgs g) {
                 const int r = ty * 4 + i, c = c0 + tx * 4 + j;
                 if (r >= rows || c >= cols) continue;
                 const size_t at = MODE == kGmmDw ? size_t(e) * g.N + row0 + r : size_t(row0 + r);
-                out[at * cols + c] = from_f32<TO>(acc[i][j]);
+                out[at * cols + c] = from_f32<TO>(sum[i][j]);
             }
     }
 }

@@ -11,7 +11,9 @@
 // Every CTA finds the touched groups itself (one load of the offsets), then
 // the warps of the grid take (group, rows of W) units in turn.  A lane loads
 // 16 bytes of several W rows at once; the row's sum is closed by shuffles, so
-// its order is fixed.
+// its order is fixed.  A lane's sum is set aside every 8192 columns: one by
+// one, equal terms of a reduction of 2^20 came out 4e-4 off, as within a
+// binade all their roundings go one way.
 #include "grouped.cuh"
 #include "grouped.h"
 
@@ -70,10 +72,15 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float c) {
 
 constexpr int kFewRows = 4;              // W rows a warp works on (16-bit operands)
 constexpr int kFewLoads = 4;             // 16-byte pieces of each a lane has in flight
+constexpr int kFewChunk = 1024;          // 16-byte pieces of a row between two such sums
+// The kernels of longer rows are their own (LONG): the checks alone cost the
+// others 3 to 6 % (8 rows of 2048: 5.25 and 5.4 us).
+inline bool few_long(const GmmArgs& g) { return g.K > kFewChunk * 8; }
 
 // X rows of x (row ..) by kFewRows rows of W.
-template <int X, bool BF16, typename TO>
-__device__ __forceinline__ void few_unit(const GmmArgs& g, int e, int n0, int row) {
+// aside (LONG): X x kFewRows x 32 floats of the warp's own.
+template <int X, bool BF16, bool LONG, typename TO>
+__device__ __forceinline__ void few_unit(const GmmArgs& g, int e, int n0, int row, float* aside) {
     const int lane = threadIdx.x & 31, pieces = g.K / 8;     // 16-byte pieces of a row
     const uint4* x = static_cast<const uint4*>(g.a) + size_t(row) * pieces;
     const uint4* w = static_cast<const uint4*>(g.b) + size_t(e) * g.N * pieces;
@@ -83,6 +90,16 @@ __device__ __forceinline__ void few_unit(const GmmArgs& g, int e, int n0, int ro
     for (int i = 0; i < kFewRows; ++i) wr[i] = w + size_t(min(n0 + i, g.N - 1)) * pieces;
     float acc[X][kFewRows] = {};
     for (int p0 = lane; p0 < pieces; p0 += 32 * kFewLoads) {
+        if (LONG && p0 >= kFewChunk && p0 % kFewChunk == lane) {
+#pragma unroll
+            for (int r = 0; r < X; ++r)
+#pragma unroll
+                for (int i = 0; i < kFewRows; ++i) {
+                    float* t = aside + (r * kFewRows + i) * 32 + lane;
+                    *t = p0 == kFewChunk + lane ? acc[r][i] : *t + acc[r][i];
+                    acc[r][i] = 0.0f;
+                }
+        }
         uint4 v[kFewRows][kFewLoads];
 #pragma unroll
         for (int l = 0; l < kFewLoads; ++l)
@@ -106,16 +123,20 @@ __device__ __forceinline__ void few_unit(const GmmArgs& g, int e, int n0, int ro
     for (int r = 0; r < X; ++r)
 #pragma unroll
         for (int i = 0; i < kFewRows; ++i) {
+            // what a lane has set aside is its own
+            if (LONG && pieces > kFewChunk + lane) acc[r][i] += aside[(r * kFewRows + i) * 32 + lane];
             const float s = warp_sum(acc[r][i]);
             if (lane == i && n0 + i < g.N) y[size_t(r) * g.N + n0 + i] = from_f32<TO>(s);
         }
 }
 
-template <bool BF16, typename TO>
+template <bool BF16, bool LONG, typename TO>
 __global__ void __launch_bounds__(kFewThreads) k_gmm_few(GmmArgs g) {
     __shared__ FewTable t;
+    __shared__ float aside[LONG ? kFewThreads / 32 : 1][LONG ? kFewX * kFewRows * 32 : 1];
     pdl_launch();
     pdl_wait();
+    float* own = aside[LONG ? threadIdx.x >> 5 : 0];
     const int chunks = (g.N + kFewRows - 1) / kFewRows;
     const int units = few_groups(t, g.offsets, g.E, g.M, g.err) * chunks;
     for (int u = int(blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5)); u < units;
@@ -123,8 +144,8 @@ __global__ void __launch_bounds__(kFewThreads) k_gmm_few(GmmArgs g) {
         const int row = t.row[u / chunks], n0 = (u % chunks) * kFewRows;
         const int e = t.e[row], cnt = t.cnt[row];
         int r = 0;
-        for (; r + kFewX <= cnt; r += kFewX) few_unit<kFewX, BF16, TO>(g, e, n0, row + r);
-        for (; r < cnt; ++r) few_unit<1, BF16, TO>(g, e, n0, row + r);
+        for (; r + kFewX <= cnt; r += kFewX) few_unit<kFewX, BF16, LONG, TO>(g, e, n0, row + r, own);
+        for (; r < cnt; ++r) few_unit<1, BF16, LONG, TO>(g, e, n0, row + r, own);
     }
 }
 
@@ -135,7 +156,7 @@ __global__ void __launch_bounds__(kFewThreads) k_gmm_few(GmmArgs g) {
 // wide, 1 column 24.7 4.2, 4 columns 24.7 6.1, 8 columns 24.0 8.6; 32000 rows
 // of 4 experts, 4096 wide, 1 column 22.0 14.0, 4 columns 19.8 19.1, 8 columns
 // 18.9 30.7.  Hence at most 4 columns.
-template <bool BF16, typename TO>
+template <bool BF16, bool LONG, typename TO>
 __global__ void __launch_bounds__(kFewThreads, 3) k_gmm_narrow(GmmArgs g) {
     pdl_launch();
     pdl_wait();
@@ -154,8 +175,15 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_gmm_narrow(GmmArgs g) {
         }
         const uint4* x = static_cast<const uint4*>(g.a) + size_t(row) * pieces;
         const uint4* we = w + size_t(gr.e) * g.N * pieces;
-        float acc[kNarrowCols] = {};
+        float acc[kNarrowCols] = {}, aside[kNarrowCols] = {};
         for (int p0 = lane; p0 < pieces; p0 += 32 * kFewLoads) {
+            if (LONG && p0 >= kFewChunk && p0 % kFewChunk == lane) {
+#pragma unroll
+                for (int n = 0; n < kNarrowCols; ++n) {
+                    aside[n] += acc[n];
+                    acc[n] = 0.0f;
+                }
+            }
             uint4 v[kFewLoads];
 #pragma unroll
             for (int l = 0; l < kFewLoads; ++l)
@@ -172,7 +200,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_gmm_narrow(GmmArgs g) {
 #pragma unroll
         for (int n = 0; n < kNarrowCols; ++n) {
             if (n >= g.N) break;
-            const float s = warp_sum(acc[n]);
+            const float s = warp_sum(LONG ? aside[n] + acc[n] : acc[n]);
             if (lane == n) y[size_t(row) * g.N + n] = from_f32<TO>(s);
         }
     }
@@ -195,24 +223,33 @@ cudaError_t few_launch(void (*kernel)(P...), int units, int per_sm, cudaStream_t
     return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
+template <bool BF16, typename TO>
+cudaError_t run_few(const GmmArgs& g, cudaStream_t s) {
+    const int units = (g.M < g.E ? g.M : g.E) * ((g.N + kFewRows - 1) / kFewRows);
+    return few_long(g) ? few_launch(k_gmm_few<BF16, true, TO>, units, 2, s, g)
+                       : few_launch(k_gmm_few<BF16, false, TO>, units, 2, s, g);
+}
+template <bool BF16, typename TO>
+cudaError_t run_narrow(const GmmArgs& g, cudaStream_t s) {
+    return few_long(g) ? few_launch(k_gmm_narrow<BF16, true, TO>, g.M, 3, s, g)
+                       : few_launch(k_gmm_narrow<BF16, false, TO>, g.M, 3, s, g);
+}
+
 }  // namespace
 
 cudaError_t launch_grouped_few(const GmmArgs& g, cudaStream_t s) {
-    const int units = (g.M < g.E ? g.M : g.E) * ((g.N + kFewRows - 1) / kFewRows);
     if (g.dtype == STRATA_BF16)
-        return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_few<true, float>, units, 2, s, g)
-                                         : few_launch(k_gmm_few<true, __nv_bfloat16>, units, 2, s, g);
-    return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_few<false, float>, units, 2, s, g)
-                                     : few_launch(k_gmm_few<false, __half>, units, 2, s, g);
+        return g.out_dtype == STRATA_F32 ? run_few<true, float>(g, s)
+                                         : run_few<true, __nv_bfloat16>(g, s);
+    return g.out_dtype == STRATA_F32 ? run_few<false, float>(g, s) : run_few<false, __half>(g, s);
 }
 
 cudaError_t launch_grouped_narrow(const GmmArgs& g, cudaStream_t s) {
     if (g.dtype == STRATA_BF16)
-        return g.out_dtype == STRATA_F32
-                   ? few_launch(k_gmm_narrow<true, float>, g.M, 3, s, g)
-                   : few_launch(k_gmm_narrow<true, __nv_bfloat16>, g.M, 3, s, g);
-    return g.out_dtype == STRATA_F32 ? few_launch(k_gmm_narrow<false, float>, g.M, 3, s, g)
-                                     : few_launch(k_gmm_narrow<false, __half>, g.M, 3, s, g);
+        return g.out_dtype == STRATA_F32 ? run_narrow<true, float>(g, s)
+                                         : run_narrow<true, __nv_bfloat16>(g, s);
+    return g.out_dtype == STRATA_F32 ? run_narrow<false, float>(g, s)
+                                     : run_narrow<false, __half>(g, s);
 }
 
 }  // namespace strata

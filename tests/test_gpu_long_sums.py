@@ -84,3 +84,49 @@ def test_products(name, dtype, out):
             want[lo:hi] = a[lo:hi].double() @ (we if way == "dx" else we.T)
     _check(got, want, _sum_limit(terms, PIECE[out]))
     assert q.moe_get_device_status(ws) == q.STRATA_OK
+
+
+# direction, rows, K, N, terms of a piece of the sum: the kernels on the CUDA cores (few rows, few
+# columns, widths of any kind), and two on the tensor cores
+EQUAL = {
+    "few_rows": ("forward", 5, 1 << 20, 40, 256),
+    "few_columns": ("forward", 700, 1 << 18, 3, 256),
+    "any_width": ("forward", 70, (1 << 17) + 3, 51, 512),
+    "any_width_dx": ("dx", 70, 51, (1 << 17) + 3, 512),
+    "any_width_dw": ("dw", (1 << 18) - 7, 37, 51, 512),
+    "tensor_cores": ("forward", 40, 1 << 18, 136, None),
+    "tensor_cores_dw": ("dw", (1 << 18) - 7, 264, 136, None),
+}
+
+
+@pytest.mark.parametrize("value", [1.1, 1.3])
+@pytest.mark.parametrize("dtype,out", TYPES)
+@pytest.mark.parametrize("name", EQUAL)
+def test_equal_terms(name, dtype, out, value):
+    """Equal terms round the same way within a binade.  On the CUDA cores an addition is off by at most
+    2^-24 of its partial sum, and n partial sums add up to (n + 1) / 2 whole ones: (p + 1) / 2 for the
+    p terms of a piece, (c + 1) / 2 for a lane's c pieces, 6 for the lanes' sum."""
+    way, M, K, N, piece = EQUAL[name]
+    terms = {"forward": K, "dx": N, "dw": M}[way]
+    off, ws = ref.offsets_of([M]).cuda(), q.make_grouped_workspace()
+    v = torch.tensor(value * terms ** -0.5, device="cuda").to(DT[dtype])
+
+    def same(*shape):
+        return v.expand(*shape).contiguous()
+    if way == "dw":
+        got = torch.zeros(1, N, K, dtype=DT[out], device="cuda")
+        q.moe_grouped_mm_dw(same(M, N), same(M, K), off, got, ws)
+    else:
+        got = torch.zeros(M, K if way == "dx" else N, dtype=DT[out], device="cuda")
+        call = q.moe_grouped_mm_dx if way == "dx" else q.moe_grouped_mm
+        call(same(M, N if way == "dx" else K), same(1, N, K), off, got, ws)
+    want = float(v.double()) ** 2 * terms
+    if piece is None:
+        limit = _sum_limit(terms, PIECE[out])
+    else:
+        lanes = 32 if piece == 256 else 1
+        limit = ((piece + 1) / 2 + (terms / lanes / piece + 2) / 2 + 6) * 2.0 ** -24
+    half = torch.finfo(DT[out]).eps / 2
+    worst = float(((got.double() - want) / want).abs().max())
+    assert worst <= limit + half * (1 + limit), f"{worst:.2e}"
+    assert q.moe_get_device_status(ws) == q.STRATA_OK
