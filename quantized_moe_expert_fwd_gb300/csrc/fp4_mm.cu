@@ -14,6 +14,11 @@
 // (bytes at the copy's rate 50.5); 131072 rows of 8 experts of 2048 x 2048:
 // 286 us, 3.8 PFLOP/s, bound by the 36 KB a stage that every CTA takes from L2.
 //
+// The accumulator is drained into fp32 registers of the epilogue every 2048
+// terms for fp32 outputs, every 8192 for 16-bit ones, for the reason that
+// grouped_tc.cu gives: 2^20 terms of one sign in one accumulator came out
+// 2.4e-4 (MX) and 3.6e-4 (NV) low.
+//
 // Roles, buffers and waits as in grouped_tc.cu.  The epilogue multiplies by
 // alpha[e] and, for SwiGLU, joins the gate and up columns 2i and 2i + 1, which
 // one lane holds side by side.
@@ -28,6 +33,8 @@ constexpr int kF4Threads = kGtThreads + 64;     // two warps more: the scales' c
 constexpr int kF4SfWarp = 10;                   // warp 10: A's, 11: B's
 constexpr int kF4N = 128;                       // tile columns
 constexpr int kF4K = 256;                       // K of a stage
+// Stages between drains, for fp32 and for 16-bit outputs.
+constexpr int kF4Drain32 = 8, kF4Drain16 = 32;
 constexpr uint32_t kF4Data = 128 * 128;         // one operand's packed rows of a stage
 
 template <int FMT>
@@ -91,10 +98,14 @@ __device__ __forceinline__ float f4_swiglu(float g, float u) {
     return F32 ? silu_mul(g, u) : __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-template <int FMT, bool F32, bool SWIGLU>
+// PIECES: the reduction is longer than a piece, a kernel of its own (in one
+// with the other, that lost up to 5 %).  Without drains and with them, NV, fp32
+// outputs: 32768 rows of 8 experts, 4096 to 1024 columns, 76.8 and 78.5 us.
+template <int FMT, bool F32, bool SWIGLU, bool PIECES>
 __global__ void __launch_bounds__(kF4Threads, 1)
     k_gmm_f4(const __grid_constant__ F4Maps maps, Fp4GmmArgs a, int vec) {
     using C = F4<FMT>;
+    constexpr int PIECE = F32 ? kF4Drain32 : kF4Drain16;
     extern __shared__ uint8_t f4_dyn[];
     __shared__ GroupTable t;
     // full: a stage's copies landed; sf_full: its scales are in tensor memory
@@ -202,9 +213,19 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     } else if (wid == kGtMmaWarp) {
         uint32_t st = 0, acc = 0;
         for (auto it = first_tile; it.m < blocks; it.next(), ++acc) {
-            const uint32_t buf = acc & 1u;
-            if (acc >= 2) gt_wait(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 62, buf);
+            auto free_acc = [&]() {
+                if (acc >= 2)
+                    gt_wait(&acc_empty[acc & 1u], ((acc >> 1) - 1) & 1, a.err, 62, acc & 1u);
+            };
+            free_acc();
             for (int ks = 0; ks < stages; ++ks, ++st) {
+                const int nth = PIECES ? ks % PIECE : ks;      // of the piece
+                const bool last = ks == stages - 1 || (PIECES && nth == PIECE - 1);
+                if (PIECES && ks > 0 && nth == 0) {
+                    ++acc;
+                    free_acc();
+                }
+                const uint32_t buf = acc & 1u;
                 const uint32_t s = st % C::kStages;
                 gt_wait(&sf_full[s], (st / C::kStages) & 1, a.err, 63, s);
                 tc_fence_after();
@@ -221,10 +242,10 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                             const int w = FMT == 0 ? j / 2 : j;
                             umma_f4<FMT>(tmem + buf * kF4N, da + 2 * j, db + 2 * j,
                                          idesc_f4(kGtRows, kF4N, FMT == 0, FMT == 0 ? 2 * (j & 1) : 0),
-                                         ca + 4 * w, cb + 4 * w, (ks | j) != 0 ? 1u : 0u);
+                                         ca + 4 * w, cb + 4 * w, (nth | j) != 0 ? 1u : 0u);
                         }
                     umma_commit(&empty[s]);
-                    if (ks == stages - 1) umma_commit(&acc_full[buf]);
+                    if (last) umma_commit(&acc_full[buf]);
                 }
                 __syncwarp();
             }
@@ -240,7 +261,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         uint32_t* stage =
             reinterpret_cast<uint32_t*>(sf_base + C::kStages * 2 * C::kSf) + wid * kGtStoreWords;
         uint32_t acc = 0;
-        for (auto it = first_tile; it.m < blocks; it.next(), ++acc) {
+        for (auto it = first_tile; it.m < blocks; it.next()) {
             const int rb = it.m, ct = it.c;
             const int e = group_of_block(t, a.E, rb);
             const int in = (rb - t.pre[e]) * kGtRows;
@@ -249,19 +270,11 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             // the warp's rows, and the first one's place
             const int rows = t.cnt[e] - in - (r - lane);
             const size_t row = size_t(t.row[e] + in + r - lane) * cols;
-            const uint32_t buf = acc & 1u;
-            gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
-            tc_fence_after();
-            // warps whose rows all lie behind the group's end have nothing to do
-            if (rows > 0)
-#pragma unroll
-            for (int c = 0; c < kF4N / 64; ++c) {
-                uint32_t u[32];
-                tmem_ld32(tl + buf * kF4N + c * 32, u);
-                tmem_ld_wait();
+            // piece c of 32 columns, from its sums
+            auto finish = [&](int c, const float* p) {
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = live ? al * __uint_as_float(u[j]) : 0.0f;
+                for (int j = 0; j < 32; ++j) v[j] = live ? al * p[j] : 0.0f;
                 const int c0 = ct * kF4N + half * (kF4N / 2) + c * 32;
                 if (SWIGLU) {
                     float h[16];
@@ -273,10 +286,53 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                     gt_store<F32, 32>(a.out, row + c0, cols, min(rows, 32), v, cols - c0, vec,
                                       a.out_dtype == STRATA_BF16, stage);
                 }
+            };
+            auto taken = [&](uint32_t buf) {             // the accumulator is free again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            };
+            // warps whose rows all lie behind the group's end have nothing to do
+            // but to free the accumulators
+            if constexpr (!PIECES) {                     // stored as it is read
+                const uint32_t buf = acc & 1u;
+                gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
+                tc_fence_after();
+                if (rows > 0)
+#pragma unroll
+                    for (int c = 0; c < kF4N / 64; ++c) {
+                        uint32_t u[32];
+                        tmem_ld32(tl + buf * kF4N + c * 32, u);
+                        tmem_ld_wait();
+                        finish(c, reinterpret_cast<const float*>(u));
+                    }
+                taken(buf);
+                ++acc;
+            } else {
+                float sum[kF4N / 64][32];
+#pragma unroll
+                for (int c = 0; c < kF4N / 64; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
+                for (int ks = 0; ks < stages; ks += PIECE, ++acc) {
+                    const uint32_t buf = acc & 1u;
+                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
+                    tc_fence_after();
+                    if (rows > 0)
+#pragma unroll
+                        for (int c = 0; c < kF4N / 64; ++c) {
+                            uint32_t u[32];
+                            tmem_ld32(tl + buf * kF4N + c * 32, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[c][j] += __uint_as_float(u[j]);
+                        }
+                    taken(buf);
+                }
+                if (rows > 0)
+#pragma unroll
+                    for (int c = 0; c < kF4N / 64; ++c) finish(c, sum[c]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
     }
     tc_fence_before();
@@ -293,8 +349,12 @@ cudaError_t f4_run(const Fp4GmmArgs& g, cudaStream_t s) {
                     gt_map(&m.a.whole, 1, g.xq, g.K / 2, g.M, 0, kGtRows);
     if (!ok) return cudaErrorInvalidValue;
     const int vec = gt_vec(g.out, size_t(SWIGLU ? g.N / 2 : g.N) * (F32 ? 4 : 2));
-    return gt_launch<k_gmm_f4<FMT, F32, SWIGLU>>(kF4Threads, 1, device_info().sms, F4<FMT>::kDyn, s,
-                                                 m, g, vec);
+    const int sms = device_info().sms;
+    if (g.K > (F32 ? kF4Drain32 : kF4Drain16) * kF4K)
+        return gt_launch<k_gmm_f4<FMT, F32, SWIGLU, true>>(kF4Threads, 1, sms, F4<FMT>::kDyn, s, m, g,
+                                                           vec);
+    return gt_launch<k_gmm_f4<FMT, F32, SWIGLU, false>>(kF4Threads, 1, sms, F4<FMT>::kDyn, s, m, g,
+                                                        vec);
 }
 
 template <int FMT>

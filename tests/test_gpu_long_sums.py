@@ -22,6 +22,7 @@ pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 PIECE = {"bf16": 2048, "fp16": 2048, "fp32": 512}
+PIECE_FP4 = {"bf16": 8192, "fp16": 8192, "fp32": 2048}
 TYPES = [("bf16", "fp32"), ("bf16", "bf16"), ("fp16", "fp16")]
 
 
@@ -129,4 +130,42 @@ def test_equal_terms(name, dtype, out, value):
     half = torch.finfo(DT[out]).eps / 2
     worst = float(((got.double() - want) / want).abs().max())
     assert worst <= limit + half * (1 + limit), f"{worst:.2e}"
+    assert q.moe_get_device_status(ws) == q.STRATA_OK
+
+
+def _places(rows, n, words):
+    """The byte of each scale of one group's rows."""
+    r = torch.arange(rows, device="cuda")[:, None]
+    c = torch.arange(n, device="cuda")[None]
+    return (r // 128 * words + c // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + c % 4
+
+
+def _fp4(g, fmt, rows, K, nbytes):
+    """Positive codes (1 to 6) and scales near one: (packed, tiled scales, float64 values)."""
+    vec = ref.VEC[fmt]
+    codes = torch.randint(2, 8, (rows, K), generator=g, device="cuda", dtype=torch.uint8)
+    lo, hi = (126, 129) if fmt == 0 else (0x30, 0x40)
+    sb = torch.randint(lo, hi, (rows, K // vec), generator=g, device="cuda", dtype=torch.uint8)
+    if fmt == 0:
+        s = torch.exp2(sb.double() - 127)
+    else:
+        s = (8 + (sb & 7)).double() * torch.exp2((sb >> 3).double() - 10)
+    tiles = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    tiles[_places(rows, K // vec, -(-K // (4 * vec)))] = sb
+    v = torch.from_numpy(ref.GRID).cuda()[codes.long()] * s.repeat_interleave(vec, dim=1)
+    return codes[:, 0::2] | codes[:, 1::2] << 4, tiles, v
+
+
+@pytest.mark.parametrize("out", DT)
+@pytest.mark.parametrize("fmt", [pytest.param(0, id="mx"), pytest.param(1, id="nv")])
+def test_4bit_product(fmt, out):
+    M, K, N = 33, 1 << 20, 72
+    g = torch.Generator(device="cuda").manual_seed(fmt)
+    xq, xs, xv = _fp4(g, fmt, M, K, q.moe_fp4_scale_bytes(fmt, M, K, 1, True))
+    wq, wsc, wv = _fp4(g, fmt, N, K, q.moe_fp4_scale_bytes(fmt, N, K, 1))
+    off, ws = ref.offsets_of([M]).cuda(), q.make_grouped_workspace()
+    y = torch.zeros(M, N, dtype=DT[out], device="cuda")
+    alpha = torch.full((1,), 2.0 ** -20, device="cuda")
+    q.moe_grouped_mm_fp4(xq, xs, wq[None], wsc, off, y, fmt, ws, alpha=alpha)
+    _check(y, xv @ wv.T * 2.0 ** -20, _sum_limit(K, PIECE_FP4[out]))
     assert q.moe_get_device_status(ws) == q.STRATA_OK
