@@ -498,6 +498,7 @@ STRATA_API strata_status moe_fp4_dequantize(int32_t format, const uint8_t* q_dev
  *   p[s][n] = alpha[e] * sum_k x[s][k] W[e][n][k]       (scales applied)
  *   y = p, or with swiglu != 0 (N even, rows 2i gate and 2i + 1 up as in the
  *   packed layer) y[s][i] = p[s][2i] / (1 + exp(-p[s][2i])) * p[s][2i + 1]
+ *     (gates below -87 lose bits with exp's, below -104 they give zero)
  * xq_dev uint8 [M][K / 2] and its scales in groups by offsets_dev; wq_dev
  * uint8 [E][N][K / 2] and its scales in E equal groups of N rows; K a multiple
  * of 32.  Both operands in `format`; the powers of two of NV operands go into

@@ -91,11 +91,18 @@ __device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t smem) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// 16-bit outputs take the fast exponential and quotient (relative error near
-// 1e-6, next to a rounding of 2^-9 or 2^-12).
+// silu(g) u with an exponential that never passes 1: e^-g leaves fp32 (and the
+// fast quotient's range before) where g is below -87, the result does not when
+// u is large.  Below -87.3 the exponential loses bits, at -104 it is 0.  16-bit
+// outputs take the fast exponential and quotient (relative error 2 + 1.2 |g|
+// steps of 2^-23, next to roundings of 2^-8 or 2^-11).  Against g / (1 + e^-g):
+// 71.8 and 73.4 us for 32768 rows of 8 experts of 2048 x 2048, 55.5 either way
+// for a prompt.
 template <bool F32>
 __device__ __forceinline__ float f4_swiglu(float g, float u) {
-    return F32 ? silu_mul(g, u) : __fdividef(g, 1.0f + __expf(-g)) * u;
+    const float e = F32 ? expf(-fabsf(g)) : __expf(-fabsf(g));
+    const float n = g < 0.0f ? g * e : g;
+    return (F32 ? n / (1.0f + e) : __fdividef(n, 1.0f + e)) * u;
 }
 
 // PIECES: the reduction is longer than a piece, a kernel of its own (in one

@@ -440,3 +440,42 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="perm"):
         q.moe_fp4_quantize(torch.zeros(8, 64, device="cuda"), xq, xs, 1, ws,
                            perm=torch.zeros(8, dtype=torch.int64, device="cuda"))
+
+
+@pytest.mark.parametrize("out", DT)
+def test_swiglu_of_gates_far_below_zero(out):
+    """Gates from -110 to 110, each with an up value that brings the result near one where a power of
+    two up to 2^120 can: e^-g passes 2^126 at -87.3 and leaves fp32 at -88.7, the result does not."""
+    gates = np.arange(-220, 221) / 2.0
+    I, K = len(gates), 32
+    silu = gates / (1 + np.exp(-gates))
+    up = np.clip(-np.round(np.log2(np.abs(silu) + 1e-60)), -100, 120)
+    codes = np.zeros((2 * I, K), dtype=np.uint8)
+    byte = np.full((2 * I, 1), 127, dtype=np.uint8)
+    for i, g in enumerate(gates):                       # the gate row adds up to g
+        left = abs(g)
+        for k in range(K):
+            c = int(np.searchsorted(ref.GRID, min(left, 6.0), side="right")) - 1
+            codes[2 * i, k] = c + (8 if g < 0 and c else 0)
+            left -= ref.GRID[c]
+        assert left == 0
+        codes[2 * i + 1, 0] = 2                         # one times the scale
+        byte[2 * i + 1] = 127 + int(up[i])
+    wsc = torch.from_numpy(ref.tiled(byte, [2 * I], K, 0, q.moe_fp4_scale_bytes(0, 2 * I, K))).cuda()
+    xs = torch.from_numpy(ref.tiled(np.full((1, 1), 127), [1], K, 0, 512)).cuda()
+    xq = torch.full((1, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    off, ws = ref.offsets_of([1]).cuda(), q.make_grouped_workspace()
+    y = torch.full((1, I), 7.0, dtype=DT[out], device="cuda")
+    q.moe_grouped_mm_fp4(xq, xs, torch.from_numpy(ref.pack(codes)).cuda()[None], wsc, off, y, 0, ws,
+                         swiglu=True)
+    u = np.exp2(up)
+    want = torch.from_numpy(silu * u)
+    # the exponential: 2 + 1.173 |g| steps (__expf's bound; expf's is smaller) and, below its normal
+    # range, two of the smallest ones; 8 steps for the rest
+    tol = torch.from_numpy((10 + 1.173 * np.abs(gates)) * 2.0 ** -23 * np.abs(silu * u)
+                           + np.abs(gates) * u * 2.0 ** -148)
+    tol = tol + ref.half_step(DT[out], want.abs() + tol)
+    err = (y[0].double().cpu() - want).abs()
+    bad = torch.nonzero(~(err <= tol)).flatten()
+    assert not len(bad), [(gates[i], float(y[0, i]), float(want[i])) for i in bad[:8]]
+    _done(ws)
