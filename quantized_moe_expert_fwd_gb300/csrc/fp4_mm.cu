@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     __shared__ __align__(8) uint64_t full[C::kStages], sf_full[C::kStages], empty[C::kStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done;
     __shared__ uint32_t tmem_base;
+    __shared__ GtStop stop;
+    const GtWaits<false> waits{a.err, &stop};
     const int tid = threadIdx.x, lane = tid & 31;
     const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(f4_dyn) + 1023) &
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             mbar_init(&acc_empty[i], kGtEpiWarps);
         }
         mbar_init(&done, 1);
+        stop = GtStop{};
         mbar_fence_init();
         tma_prefetch_map(&maps.b);
         tma_prefetch_map(&maps.a.part);
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                 const uint8_t* sb_g = a.wsc + (size_t(e) * nt + ct) * words * 512;
                 for (int ks = 0; ks < stages; ++ks, ++st) {
                     const uint32_t s = st % C::kStages, round = st / C::kStages;
-                    if (round > 0 && !gt_wait(&empty[s], (round - 1) & 1, a.err, 60, s)) {
+                    if (round > 0 && !gt_wait(&empty[s], (round - 1) & 1, waits, 60, s)) {
                         ok = false;
                         break;
                     }
@@ -193,8 +196,15 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                 }
             }
             // every copy has landed and has been consumed before the CTA exits
-            for (uint32_t k = st > C::kStages ? st - C::kStages : 0; k < st; ++k)
-                mbar_wait(&empty[k % C::kStages], (k / C::kStages) & 1);
+            const uint32_t tail = st > C::kStages ? st - C::kStages : 0;
+            for (uint32_t k = tail; ok && k < st; ++k)
+                ok = gt_wait(&empty[k % C::kStages], (k / C::kStages) & 1, waits, 61, k % C::kStages);
+            if (!ok) {
+                // a wait ran out: the copies have landed
+                waits.mark(&stop.halted, 1u);
+                for (uint32_t k = tail; k < st; ++k)
+                    mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
+            }
         }
     } else if (wid >= kF4SfWarp) {
         // one operand's scales of each stage to tensor memory, on a thread of
@@ -205,7 +215,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             for (auto it = first_tile; it.m < blocks; it.next()) {
                 for (int ks = 0; ks < stages; ++ks, ++st) {
                     const uint32_t s = st % C::kStages;
-                    gt_wait(&full[s], (st / C::kStages) & 1, a.err, 66 + op, s);
+                    gt_wait<false, true>(&full[s], (st / C::kStages) & 1, waits, 66 + op, s);
                     tc_fence_after();
                     const uint32_t sf = smem_u32(sf_base + s * (2 * C::kSf) + op * C::kSf);
                     const uint32_t col = tmem + C::kSfCol + (2 * s + op) * C::kSfCols;
@@ -222,7 +232,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         for (auto it = first_tile; it.m < blocks; it.next(), ++acc) {
             auto free_acc = [&]() {
                 if (acc >= 2)
-                    gt_wait(&acc_empty[acc & 1u], ((acc >> 1) - 1) & 1, a.err, 62, acc & 1u);
+                    gt_wait<false, true>(&acc_empty[acc & 1u], ((acc >> 1) - 1) & 1, waits, 62,
+                                         acc & 1u);
             };
             free_acc();
             for (int ks = 0; ks < stages; ++ks, ++st) {
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                 }
                 const uint32_t buf = acc & 1u;
                 const uint32_t s = st % C::kStages;
-                gt_wait(&sf_full[s], (st / C::kStages) & 1, a.err, 63, s);
+                gt_wait<false, true>(&sf_full[s], (st / C::kStages) & 1, waits, 63, s);
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t sa = smem_u32(base + s * (2 * kF4Data));
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         // no product may still be writing the TMEM when it is freed
         if (elect_one()) umma_commit(&done);
         __syncwarp();
-        gt_wait(&done, 0, a.err, 64, 0);
+        gt_wait<false, false, false>(&done, 0, waits, 64, 0);
     } else if (wid < kGtEpiWarps) {
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (kF4N / 2));
@@ -303,7 +314,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             // but to free the accumulators
             if constexpr (!PIECES) {                     // stored as it is read
                 const uint32_t buf = acc & 1u;
-                gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
+                gt_wait(&acc_full[buf], (acc >> 1) & 1, waits, 65, buf);
                 tc_fence_after();
                 if (rows > 0)
 #pragma unroll
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                     for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
                 for (int ks = 0; ks < stages; ks += PIECE, ++acc) {
                     const uint32_t buf = acc & 1u;
-                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 65, buf);
+                    gt_wait(&acc_full[buf], (acc >> 1) & 1, waits, 65, buf);
                     tc_fence_after();
                     if (rows > 0)
 #pragma unroll
@@ -344,6 +355,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // a wait ran out: scales may still be on their way to tensor memory
+    if (!waits.seen(&stop.stop, 0u)) gt_settle();
     tc_fence_after();
     if (wid == kGtMmaWarp) tmem_dealloc(tmem, 512);
 }

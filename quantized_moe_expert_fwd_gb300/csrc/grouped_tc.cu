@@ -162,7 +162,9 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     // empty, acc_full and done signal in both CTAs, acc_empty at rank 0.
     __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], both[STAGES], fixed[STAGES];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done;
-    __shared__ uint32_t tmem_base;
+    __shared__ uint32_t tmem_base, pieces;
+    __shared__ GtStop stop;
+    const GtWaits<PAIR> waits{a.err, &stop};
     const int tid = threadIdx.x, lane = tid & 31;
     const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
     const int rank = CL != 0 ? int(cluster_rank()) : 0;
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             mbar_init(&acc_empty[i], PAIR ? 2 * kGtEpiWarps : kGtEpiWarps);
         }
         mbar_init(&done, 1);
+        stop = GtStop{};
         mbar_fence_init();
         tma_prefetch_map(&maps.b);
         tma_prefetch_map(&maps.a.part);
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 const uint32_t bytes = uint32_t(nbox) * kGtBox * 128u + G::kBBytes;
                 for (int ks = i.k0; ks < i.k1; ++ks, ++st) {
                     const uint32_t s = st % STAGES, round = st / STAGES;
-                    if (round > 0 && !gt_wait(&empty[s], (round - 1) & 1, a.err, 50, s)) {
+                    if (round > 0 && !gt_wait(&empty[s], (round - 1) & 1, waits, 50, s)) {
                         ok = false;
                         break;
                     }
@@ -277,8 +280,17 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             }
             // every copy has landed, has been consumed, and the MMAs' arrivals are
             // here, before the CTA exits
-            for (uint32_t k = st > STAGES ? st - STAGES : 0; k < st; ++k)
-                mbar_wait(&empty[k % STAGES], (k / STAGES) & 1);
+            const uint32_t tail = st > STAGES ? st - STAGES : 0;
+            for (uint32_t k = tail; ok && k < st; ++k)
+                ok = gt_wait(&empty[k % STAGES], (k / STAGES) & 1, waits, 51, k % STAGES);
+            if (!ok) {
+                // a wait ran out: the copies have landed (a pair's second CTA's
+                // report to the first)
+                waits.mark(&stop.halted, 1u << rank);
+                for (uint32_t k = tail; !PAIR && k < st; ++k)
+                    mbar_wait(&full[k % STAGES], (k / STAGES) & 1);
+                gt_settle();
+            }
         }
     } else if (wid == kGtMmaWarp) {
         const uint32_t idesc = idesc_f16(G::kBlock, BN, a.bf16) |
@@ -297,21 +309,21 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 const bool last = ks == i.k1 - 1 || (PIECES && nth % PIECE == PIECE - 1);
                 const uint32_t buf = acc & 1u;
                 if ((!PAIR || rank == 0) && first && acc >= 2)
-                    gt_wait<PAIR>(&acc_empty[buf], ((acc >> 1) - 1) & 1, a.err, 52, buf);
+                    gt_wait<PAIR, true>(&acc_empty[buf], ((acc >> 1) - 1) & 1, waits, 52, buf);
                 uint8_t* sa = base + s * STAGE;
                 uint8_t* sb = sa + kGtABytes;
                 const int dead = gt_dead<MODE>(i, ks);         // rows of the next group
                 int steps = kGtK / 16;
                 if (MODE == kGmmDw) steps = (min(kGtK, i.cnt - ks * kGtK) + 15) / 16;
                 if (!PAIR) {
-                    gt_wait(&full[s], (st / STAGES) & 1, a.err, 53, s);
+                    gt_wait<false, true>(&full[s], (st / STAGES) & 1, waits, 53, s);
                 } else if (dead == 0) {
                     if (rank == 0) {
-                        gt_wait(&both[s], (both_phase >> s) & 1u, a.err, 56, s);
+                        gt_wait<false, true>(&both[s], (both_phase >> s) & 1u, waits, 56, s);
                         both_phase ^= 1u << s;
                     }
                 } else {
-                    gt_wait(&full[s], (own_phase >> s) & 1u, a.err, 53, s);
+                    gt_wait<false, true>(&full[s], (own_phase >> s) & 1u, waits, 53, s);
                 }
                 if (dead > 0) {
                     const int valid = steps * 16 - dead;
@@ -324,7 +336,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                         fence_proxy_async_all();
                         __syncwarp();
                         if (rank == 0)
-                            gt_wait<true>(&fixed[s], (own_phase >> s) & 1u, a.err, 57, s);
+                            gt_wait<true, true>(&fixed[s], (own_phase >> s) & 1u, waits, 57, s);
                         else if (elect_one()) mbar_arrive_rank0(&fixed[s]);
                         own_phase ^= 1u << s;
                     } else {
@@ -363,19 +375,14 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                 if (last) ++acc;
             }
         }
-        // no product may still be writing the TMEM when it is freed
         if ((!PAIR || rank == 0) && elect_one()) {
             if (PAIR) umma2_commit(&done);
             else umma_commit(&done);
         }
         __syncwarp();
-        gt_wait(&done, 0, a.err, 54, 0);
-        // The other CTA's last arrivals at acc_empty have to be here too before
-        // this CTA exits: one under way then would count on a barrier of the
-        // CTA that follows it on the SM.
-        if (PAIR && rank == 0)
-            for (uint32_t k = acc > 2 ? acc - 2 : 0; k < acc; ++k)
-                gt_wait<true>(&acc_empty[k & 1u], (k >> 1) & 1, a.err, 58, k & 1u);
+        // no product may still be writing the TMEM when it is freed
+        if (!PAIR) gt_wait<false, false, false>(&done, 0, waits, 54, 0);
+        else if (lane == 0) pieces = acc;
     } else {
         constexpr int CH = BN / 64;              // 32-column pieces of a warp's half
         const int half = wid >> 2, r = (wid & 3) * 32 + lane;
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             if constexpr (!PIECES) {             // stored as it is read
                 const uint32_t buf = acc & 1u;
                 if (i.k1 > i.k0) {
-                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
+                    gt_wait(&acc_full[buf], (acc >> 1) & 1, waits, 55, buf);
                     tc_fence_after();
                 }
 #pragma unroll
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
                 for (int ks = i.k0; ks < i.k1; ks += PIECE, ++acc) {
                     const uint32_t buf = acc & 1u;
-                    gt_wait(&acc_full[buf], (acc >> 1) & 1, a.err, 55, buf);
+                    gt_wait(&acc_full[buf], (acc >> 1) & 1, waits, 55, buf);
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
@@ -488,6 +495,17 @@ __global__ void __launch_bounds__(kGtThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR && wid == kGtMmaWarp) {
+        // A pair waits for its products only here, where the other roles are done:
+        // rank 0 issues rank 1's, and a call may last longer than one wait.
+        gt_wait<true, false, false>(&done, 0, waits, 54, 0);
+        // The other CTA's last arrivals at acc_empty have to be here too before
+        // this CTA exits: one under way then would count on a barrier of the
+        // CTA that follows it on the SM.
+        if (rank == 0)
+            for (uint32_t k = pieces > 2 ? pieces - 2 : 0; k < pieces; ++k)
+                gt_wait<true, false, false>(&acc_empty[k & 1u], (k >> 1) & 1, waits, 58, k & 1u);
+    }
     if (SPLIT) {
         // the partial sums of all parts, added in their order; this CTA
         // stores its share of the tile's rows, a warp 128 columns of one row

@@ -19,23 +19,61 @@ constexpr int kGtEpiWarps = 8, kGtTmaWarp = 8, kGtMmaWarp = 9;
 constexpr int kGtRows = 128;                    // tile rows
 constexpr int kGtBox = 32;                      // rows of the smaller row box
 
-// Bounded wait that gives up early once a timed-out wait has been latched.
-// A producer whose wait failed issues nothing more (a second expected count
-// in one phase would be undefined).  The other roles run on to their end over
-// values that nobody is to use: their arrivals only complete phases, and
-// stay within the CTA's own buffers.  (A check a stage that leaves the MMA
-// loop cost 5 %.)
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+// What the waits of a CTA share beside the workspace's error word: two words of
+// shared memory, which a pair's CTAs keep alike.  stop is set once a wait has
+// run out; the others then give up early.  (Not by the error word: a code
+// latched by an earlier call, and not read yet, must not cut this call's waits
+// short.)  halted: a bit for each CTA whose producer then issues nothing more.
+struct GtStop {
+    uint32_t stop, halted;
+};
+template <bool PAIR>
+struct GtWaits {
+    uint32_t* err;
+    GtStop* s;
+    __device__ __forceinline__ bool seen(const uint32_t* word, uint32_t value) const {
+        return *reinterpret_cast<const volatile uint32_t*>(word) == value;
+    }
+    __device__ __forceinline__ void mark(uint32_t* word, uint32_t bit) const {
+        if (PAIR) {
+            or_cluster_u32(word, 0, bit);
+            or_cluster_u32(word, 1, bit);
+        } else {
+            atomicOr(word, bit);
+        }
+    }
+};
+
+// Bounded wait (a poll lasts about 2 us, the limit 8 s; CLUSTER: sees what both
+// CTAs of a pair did).  After one that ran out, the producers issue nothing
+// more.  The MMA warp and the 4-bit kernel's scale warps (HOLD) go on once they
+// have seen that: they hand stages back that may not have landed, and a second
+// expected count in one phase would be undefined.  Without them the producers
+// come to wait themselves, so their own limit is twice as long.  All but the
+// producers run on to their end over values that nobody is to use: their
+// arrivals only complete phases, and stay within the CTA's own buffers.  (A
+// check a stage that leaves the MMA loop cost 5 %; a look at the words every 16
+// polls instead of 256, up to 5 too.)  EARLY = false: to the limit in any case,
+// for what has to be over before the CTA gives its memory back.
+template <bool CLUSTER = false, bool HOLD = false, bool EARLY = true, bool PAIR>
+__device__ __forceinline__ bool gt_wait(uint64_t* bar, uint32_t parity, const GtWaits<PAIR>& w,
                                         uint32_t site, uint32_t slot) {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    for (uint32_t i = 0; i < (HOLD ? 2 * kWaitLimit : kWaitLimit); ++i) {
         if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if ((i & 255u) == 255u && *reinterpret_cast<const volatile uint32_t*>(err) == 4u)
+        if (EARLY && (i & 255u) == 255u &&
+            (HOLD ? w.seen(&w.s->halted, PAIR ? 3u : 1u) : w.seen(&w.s->stop, 1u)))
             return false;
     }
-    latch_timeout(err, site, slot, parity, 0);
+    w.mark(&w.s->stop, 1u);
+    latch_timeout(w.err, site, slot, parity, 0);
     return false;
 }
+// About a millisecond, far more than a copy under way takes: for copies of a
+// call whose waits ran out and that no barrier here reports.
+__device__ __forceinline__ void gt_settle() {
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
+
 // A CTA's (or CTA pair's) tiles in order: column tile c (of nt) fastest, then row block m, and
 // with MT row blocks an expert (dw) the expert e.  Steps of one tile a
 // worker are added digit by digit: a 64-bit division a tile took longer than the

@@ -243,6 +243,15 @@ __device__ __forceinline__ float4 ld_cluster_f4(const void* p, uint32_t rank) {
         : "memory");
     return v;
 }
+// Bits set in a word of the shared memory of CTA `rank`, at the place that `p`
+// has in this one.
+__device__ __forceinline__ void or_cluster_u32(uint32_t* p, uint32_t rank, uint32_t bits) {
+    asm volatile(
+        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, %1; "
+        "red.relaxed.cluster.shared::cluster.or.b32 [a], %2; }" ::"r"(smem_u32(p)),
+        "r"(rank), "r"(bits)
+        : "memory");
+}
 // The address of rank 0's copy of a barrier, and loads into this CTA's shared
 // memory that complete on it.
 __device__ __forceinline__ uint32_t rank0_addr(const void* p) {

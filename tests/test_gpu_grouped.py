@@ -330,3 +330,32 @@ def test_large_places():
     ref.check(dw[-1:], want, mags, 5)
     assert int(dw[:-1].count_nonzero()) == 0
     _done(ws)
+
+
+@pytest.mark.parametrize("name", ["tile_edges", "few_tiles", "long_groups", "token"])
+def test_a_timeout_latched_before_cuts_no_wait_short(name):
+    """A workspace whose error word still holds an earlier call's timeout: the waits of these calls are
+    their own, so the results are the same bits, and the code stays for moe_get_device_status."""
+    x, w, dy, off, ws = _case(name, "bf16")
+    E, M, K, N = w.shape[0], x.shape[0], x.shape[1], w.shape[1]
+    fmt = q.FP4_NV
+    xq, xs = torch.zeros(M, K // 2, dtype=torch.uint8, device="cuda"), torch.zeros(
+        q.moe_fp4_scale_bytes(fmt, M, K, E, True), dtype=torch.uint8, device="cuda")
+    wq, wsc = torch.zeros(E * N, K // 2, dtype=torch.uint8, device="cuda"), torch.zeros(
+        q.moe_fp4_scale_bytes(fmt, E * N, K, E), dtype=torch.uint8, device="cuda")
+    results = []
+    for code in (0, q.STRATA_ETIMEOUT):
+        ws[:4].view(torch.int32).fill_(code)
+        out = [torch.zeros(*s, dtype=dt, device="cuda") for dt in (torch.bfloat16, torch.float32)
+               for s in ((M, N), (M, K), (E, N, K), (M, N))]
+        for y, dx, dw, y4 in (out[:4], out[4:]):
+            q.moe_grouped_mm(x, w, off, y, ws)
+            q.moe_grouped_mm_dx(dy, w, off, dx, ws)
+            q.moe_grouped_mm_dw(dy, x, off, dw, ws)
+            q.moe_fp4_quantize(x, xq, xs, fmt, ws, offsets=off)
+            q.moe_fp4_quantize(w.view(E * N, K), wq, wsc, fmt, ws, n_groups=E)
+            q.moe_grouped_mm_fp4(xq, xs, wq.view(E, N, K // 2), wsc, off, y4, fmt, ws)
+        assert q.moe_get_device_status(ws) == code
+        results.append(out)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    _done(ws)
