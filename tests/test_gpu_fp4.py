@@ -479,3 +479,34 @@ def test_swiglu_of_gates_far_below_zero(out):
     bad = torch.nonzero(~(err <= tol)).flatten()
     assert not len(bad), [(gates[i], float(y[0, i]), float(want[i])) for i in bad[:8]]
     _done(ws)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_rows_before_the_first_group(fmt):
+    """Rows before the first and behind the last group hold NaN and stay as they were; the groups' row
+    blocks of scales are counted from the first group."""
+    counts, first, spare, C, N = [130, 0, 1, 40], 5, 7, 160, 96
+    M = first + sum(counts) + spare
+    live = slice(first, M - spare)
+    x = _rows(M, C, "bf16", 8, fmt)
+    codes, sb = ref.quantize(x[live].double().numpy(), fmt)
+    x[:first], x[M - spare:] = float("nan"), float("nan")
+    off, ws = ref.offsets_of(counts, first).cuda(), q.make_grouped_workspace()
+    qd, sc = _bufs(M, C, fmt, len(counts))
+    q.moe_fp4_quantize(x.cuda(), qd, sc, fmt, ws, offsets=off)
+    place, used = ref.tile_places(counts, C, fmt)
+    got, scb = qd.cpu().numpy(), sc.cpu().numpy()
+    assert np.array_equal(ref.unpack(got[live]), codes) and np.array_equal(scb[place], sb)
+    assert (got[:first] == 0xAB).all() and (got[M - spare:] == 0xAB).all() and (scb[used:] == 0xAB).all()
+    v = torch.full((M, C), 7.0, device="cuda")
+    q.moe_fp4_dequantize(qd, sc, v, fmt, ws, offsets=off)
+    values = torch.from_numpy(ref.values(codes, sb, fmt)).cuda()
+    assert torch.equal(v[live].double(), values)
+    assert (v[:first] == 7).all() and (v[M - spare:] == 7).all()
+    wq, wsc, wv = _operand([N] * len(counts), C, fmt, 2, False)
+    y = torch.full((M, N), 7.0, device="cuda")
+    q.moe_grouped_mm_fp4(qd, sc, wq.view(len(counts), N, C // 2), wsc, off, y, fmt, ws)
+    want, mags = ref.mm(values, wv.view(len(counts), N, C), ref.offsets_of(counts))
+    ref.check(y[live], want, mags, C)
+    assert (y[:first] == 7).all() and (y[M - spare:] == 7).all()
+    _done(ws)
