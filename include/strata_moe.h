@@ -387,11 +387,11 @@ STRATA_API strata_status moe_layer_bucketing(const strata_moe_dims* dims, int32_
  *
  * These calls work on the slot space of moe_permute: M rows, of which group e
  * (e in [0, E)) holds rows offsets[e] .. offsets[e + 1].  Groups may be empty;
- * rows before offsets[0] and behind offsets[E] belong to no group: they are
- * not read, and outputs keep what they held there.  offsets_dev stays on the
- * device (int32 [E + 1], non-decreasing, within [0, M]); offsets that run
- * backwards anywhere or leave [0, M] latch STRATA_EBADROUTE, and every group
- * of that call counts as empty.
+ * rows before offsets[0] and behind offsets[E] belong to no group: their values
+ * are not used (a tile's copy may take them along), and outputs keep what they
+ * held there.  offsets_dev stays on the device (int32 [E + 1], non-decreasing,
+ * within [0, M]); offsets that run backwards anywhere or leave [0, M] latch
+ * STRATA_EBADROUTE, and every group of that call counts as empty.
  *   - E in [1, 1024], M in [0, 2^31 - 1024], K and N in [1, 2^20] unless a
  *     call says less.  M == 0 launches nothing, except that moe_grouped_mm_dw
  *     still writes its zeros.
@@ -403,8 +403,10 @@ STRATA_API strata_status moe_layer_bucketing(const strata_moe_dims* dims, int32_
  *     too.  Captured graphs that may run at the same time need one each.
  *   - No call allocates, synchronises or copies to the host, so all can be
  *     captured into a graph and replayed with other offsets.
- *   - fp32 sums, one rounding to nearest even into the output's type;
- *     infinities and NaNs in a row (a column of W) stay in that row (column).
+ *   - fp32 sums, one rounding to nearest even into the output's type.  Long
+ *     reductions are summed in pieces: 2^18 terms of one sign come out within
+ *     2e-5 of their sum before that rounding (fp32 outputs: mostly 3e-6).
+ *     Infinities and NaNs in a row (a column of W) stay in that row (column).
  */
 typedef enum { STRATA_BF16 = 0, STRATA_F16 = 1, STRATA_F32 = 2 } strata_dtype;
 
@@ -444,8 +446,8 @@ STRATA_API strata_status moe_grouped_mm_dw(int32_t dtype, const void* dy_dev, co
  * their negatives; two a byte, the first in the low half), and one scale byte
  * for V consecutive elements of a row.
  *   STRATA_FP4_MX  V = 32, scale 2^(byte - 127) (ue8m0; 255 is NaN)
- *   STRATA_FP4_NV  V = 16, scale an e4m3 value, times 2^scale_exp for the
- *                  whole tensor
+ *   STRATA_FP4_NV  V = 16, scale an e4m3 value without sign, times 2^scale_exp
+ *                  for the whole tensor
  * Scales lie in 512-byte tiles of 128 rows by 4 consecutive scales of a row:
  * the 4 bytes of the tile's row r at (r % 32) * 16 + (r / 32) * 4.  Tiles of
  * one block of 128 rows follow each other along the row (the last one filled

@@ -16,7 +16,10 @@ constexpr int kSimtTile = 64, kSimtK = 16, kSimtThreads = 256;
 constexpr int kSimtPiece = 512;
 
 // One 64 x 64 output tile a CTA step, 4 x 4 outputs a thread, operands
-// through shared memory as fp32.
+// through shared memory as fp32.  For widths whose rows TMA cannot address (not
+// a multiple of 16 bytes); bound by shared memory and FMAs, far from the tensor
+// cores: 1024 rows of 8 experts, 1023 to 1024 columns, 204 us (1024 columns, on
+// the tensor cores: 8.3), their dw over 8192 rows 868 (17).
 template <int MODE, typename TI, typename TO>
 __global__ void __launch_bounds__(kSimtThreads) k_gmm_simt(GmmArgs g) {
     __shared__ GroupTable t;

@@ -152,10 +152,11 @@ __global__ void __launch_bounds__(kFewThreads) k_gmm_few(GmmArgs g) {
 // Few columns instead of few rows: a warp a row of x, every column's W row
 // from the caches (the warps of a CTA work on neighbouring rows, so mostly on
 // one expert's).  On the tensor cores a tile of any width takes every stage of
-// the reduction.  Tensor cores and here, us: 2500 rows of 317 experts, 1816
-// wide, 1 column 24.7 4.2, 4 columns 24.7 6.1, 8 columns 24.0 8.6; 32000 rows
-// of 4 experts, 4096 wide, 1 column 22.0 14.0, 4 columns 19.8 19.1, 8 columns
-// 18.9 30.7.  Hence at most 4 columns.
+// the reduction.  Tensor cores and here, us, calls back to back: 2536 rows of
+// 317 experts, 1816 wide, 1 column 24.2 4.4, 4 columns 24.3 6.6, 8 columns 24.0
+// 9.3; 8000 rows of 4 experts, 4096 wide (in the L2), 21.7 9.3, 17.2 19.5, 16.4
+// 33.1; 32000 such rows, 62.0 41.6, 46.0 58.2, 45.7 113.7.  Hence at most 4
+// columns: 5 to 8 would gain only where the experts have few rows.
 template <bool BF16, bool LONG, typename TO>
 __global__ void __launch_bounds__(kFewThreads, 3) k_gmm_narrow(GmmArgs g) {
     pdl_launch();

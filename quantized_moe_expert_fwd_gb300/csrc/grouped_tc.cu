@@ -22,8 +22,9 @@
 // split over a cluster (gt_pick has the rules and what they measured).
 //
 // Measured, 256 experts of 1024 x 2048 in bf16, 16384 rows (us; bytes at the
-// copy's rate 175.6): forward 183, dx 172, dw 193; 65536 rows into 32 experts,
-// dw in fp32: 203 (FLOPs at the burst rate 144.7).
+// copy's rate 175.6): forward 184, dx 173, dw 199; 65536 rows into 32 experts,
+// dw in fp32: 200 in a captured graph, 220 as calls with changing inputs (FLOPs
+// at the burst rate 144.7).
 //
 // The tensor cores truncate as they add, so terms of one sign lose about 1e-7
 // of the sum with every 16 of them (16-bit outputs of 2^18 such terms in one
@@ -602,8 +603,10 @@ cudaError_t gt_typed(const GmmArgs& g, int cluster, int grid, cudaStream_t s) {
 }
 
 // Which tiles.  dw: a CTA pair from 512 rows a group on average (us, 32
-// experts of 1024 x 2048 in bf16, single and pair: 51.4 55.8 at 256 rows,
-// 77.2 74.1 at 512, 124.7 107.2 at 1024).
+// experts of 1024 x 2048, single and pair, bf16: 44.4 51.6 at 256 rows, 57.6
+// 52.0 at 384, 68.3 54.5 at 512, 115.2 88.5 at 1024; fp32: 56.9 68.1, 71.6 75.5,
+// 84.7 74.5, 131.1 107.2).  The average is of the buffer's rows: 2048 rows of
+// these groups in a buffer of 16384 take the pair, 39.5 instead of 28.2.
 //
 // Forward and dx: the shortest by a count of waves and stages.  A stage takes
 // a CTA about 0.25 us with 128 columns, 0.385 with 256, a pair (256 rows, 256
