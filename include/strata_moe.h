@@ -515,6 +515,147 @@ STRATA_API strata_status moe_grouped_mm_fp4(int32_t format, const uint8_t* xq_de
                                             int32_t y_dtype, void* y_dev, void* ws_dev,
                                             size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A tuning step's operators around bf16 / fp16 experts (and the same block in
+ * serving).  Slot space, offsets, limits and workspace as for the grouped
+ * products above: every tensor contiguous and 16-byte aligned (offsets,
+ * inv_perm, perm, weights, gate and rstd 4), outputs not overlapping inputs
+ * but where a call says so, nothing allocated or synchronised.  With
+ * moe_grouped_mm, _dx and _dw they make the block's step:
+ *   moe_norm_residual -> moe_route, moe_permute -> moe_slots_spread (gather)
+ *   -> moe_grouped_swiglu -> moe_grouped_mm -> moe_slots_combine, and back
+ *   moe_norm_residual_bwd -> moe_slots_spread -> moe_grouped_swiglu_bwd,
+ *   moe_grouped_mm_dw -> moe_grouped_mm_dx, _dw -> moe_slots_combine.
+ */
+
+/* The gate and up products with SwiGLU, one kernel:
+ *   p[s][n] = sum_k x[s][k] W[e][n][k]         (rows 2i of W gate, 2i + 1 up)
+ *   h[s][i] = p[s][2i] / (1 + exp(-p[s][2i])) * p[s][2i + 1]
+ * for every row s of every group e; h from the fp32 sums, rounded once (gates
+ * below -87 lose bits with exp's, below -104 they give zero).
+ * dtype: STRATA_BF16 or STRATA_F16, of x_dev [M][K], w_dev [E][2I][K] and
+ * h_dev [M][I] (out); I in [1, 2^19].
+ * p_dev: NULL, or where p is kept for the backward pass (out, interleaved as
+ * it is): p_scales_dev NULL: [M][2I] in dtype; otherwise in 8 bits (the format
+ * of moe_act8_save): uint8 [M][2I] and uint8 [M][2I / 32], 2I a multiple of 32. */
+STRATA_API strata_status moe_grouped_swiglu(int32_t dtype, const void* x_dev, const void* w_dev,
+                                            int32_t M, int32_t K, int32_t I, int32_t E,
+                                            const int32_t* offsets_dev, void* h_dev, void* p_dev,
+                                            uint8_t* p_scales_dev, void* ws_dev, size_t ws_bytes,
+                                            void* stream);
+
+/* Its backward pass from the down product on, one kernel: with p as
+ * moe_grouped_swiglu kept it, g = p[s][2i], u = p[s][2i + 1],
+ * sg = 1 / (1 + exp(-g)),
+ *   dh[s][i]     = sum_n dy[s][n] W[e][n][i]   (W the down product's weights)
+ *   dp[s][2i]    = dh u sg (1 + g (1 - sg)),   dp[s][2i + 1] = dh g sg
+ *   h[s][i]      = g sg u                      (again, for the down product's dw)
+ * dy_dev [M][N], w_dev [E][N][I], p_dev [M][2I] in dtype (p_scales_dev NULL) or
+ * in 8 bits; dp_dev [M][2I] and, unless NULL, h_dev [M][I] (out) in dtype.
+ * The gradients by W and x are moe_grouped_mm_dw(dp, x) and
+ * moe_grouped_mm_dx(dp, W). */
+STRATA_API strata_status moe_grouped_swiglu_bwd(int32_t dtype, const void* dy_dev, const void* w_dev,
+                                                const void* p_dev, const uint8_t* p_scales_dev,
+                                                int32_t M, int32_t N, int32_t I, int32_t E,
+                                                const int32_t* offsets_dev, void* dp_dev,
+                                                void* h_dev, void* ws_dev, size_t ws_bytes,
+                                                void* stream);
+
+/* Rows kept in 8 bits between the forward and the backward pass.  Blocks of 32
+ * consecutive elements of a row have one scale byte b: with m their largest
+ * magnitude, 2^(b - 127) is the smallest power of two, at least 2^-126, with
+ * m <= 448 2^(b - 127); an element's code is e4m3(x / 2^(b - 127)), to nearest
+ * even.  A block that holds an infinity or a NaN gets b = 255 and reads as
+ * NaN.  x_dev [rows][cols] in dtype (STRATA_BF16, _F16 or _F32), cols a
+ * multiple of 32; q_dev uint8 [rows][cols], scales_dev uint8 [rows][cols / 32]. */
+STRATA_API strata_status moe_act8_save(int32_t dtype, const void* x_dev, int32_t rows, int32_t cols,
+                                       uint8_t* q_dev, uint8_t* scales_dev, void* stream);
+
+/* The values of kept rows, code * 2^(b - 127): destination row s takes row
+ * perm[s] / top_k (perm_dev as moe_permute writes it; NULL: row s, and rows
+ * equal to q_rows).  Exact in fp32 and bf16 (values below 2^-126 aside),
+ * rounded in fp16, where a finite value past 65504 reads as +-65504.  A source
+ * row out of range latches STRATA_EBADROUTE and reads as zeros.
+ * out_dev [rows][cols] in out_dtype (STRATA_BF16, _F16 or _F32). */
+STRATA_API strata_status moe_act8_load(const uint8_t* q_dev, const uint8_t* scales_dev,
+                                       int32_t q_rows, int32_t cols, const int32_t* perm_dev,
+                                       int32_t top_k, int32_t rows, int32_t out_dtype,
+                                       void* out_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/* A token's slots weighted into its row:
+ *   out[t][c] = sum_k weights[t][k] y[inv_perm[t * top_k + k]][c]  (fp32, k ascending)
+ * weights_dev fp32 [T][top_k], or NULL for ones (then it is the gradient of
+ * the gather below).  y_dev [M][H] in dtype (STRATA_BF16 or _F16), out_dev
+ * [T][H] in dtype or STRATA_F32; top_k in [1, 16].  A slot outside [0, M) is
+ * left out and latches STRATA_EBADROUTE. */
+STRATA_API strata_status moe_slots_combine(int32_t dtype, const void* y_dev, int32_t M, int32_t H,
+                                           const int32_t* inv_perm_dev, const float* weights_dev,
+                                           int32_t T, int32_t top_k, int32_t out_dtype,
+                                           void* out_dev, void* ws_dev, size_t ws_bytes,
+                                           void* stream);
+
+/* Its gradients:
+ *   dy[inv_perm[t * top_k + k]][c] = weights[t][k] dout[t][c]
+ *   dweights[t][k] = sum_c dout[t][c] y[inv_perm[t * top_k + k]][c]
+ * With weights_dev NULL (ones) and dy alone it is the gather of token rows into
+ * slot order.  dout_dev [T][H], dy_dev [M][H] (out, or NULL; rows of no slot
+ * keep what they held; no slot may be named twice) and y_dev [M][H] in dtype;
+ * dweights_dev fp32 [T][top_k] (out), given together with y_dev or both NULL.
+ * A slot outside [0, M) latches STRATA_EBADROUTE, and its weight's gradient
+ * is 0. */
+STRATA_API strata_status moe_slots_spread(int32_t dtype, const void* dout_dev,
+                                          const int32_t* inv_perm_dev, const float* weights_dev,
+                                          const void* y_dev, int32_t T, int32_t top_k, int32_t M,
+                                          int32_t H, void* dy_dev, float* dweights_dev,
+                                          void* ws_dev, size_t ws_bytes, void* stream);
+
+/* Workspace of moe_norm_residual_bwd's weight gradients for rows of H columns
+ * (0 for an H that is refused); 256-byte aligned, any contents. */
+STRATA_API size_t moe_norm_workspace_bytes(int32_t H);
+
+/* The norm after a block, its gate, the residual, and the norm before the next
+ * block, one kernel:
+ *   n  = f s0 w_post,  s0 = 1 / sqrt(mean f^2 + eps)      (post_norm == 0: n = f)
+ *   r' = alpha r + beta gate[t] n                         (f_dev NULL: alpha r)
+ *   x  = r' s1 w_pre,  s1 = 1 / sqrt(mean r'^2 + eps)     (x_dev NULL: not taken)
+ * per row; x is of r' as it is stored (rounded to resid_dtype).
+ * dtype: STRATA_BF16 or STRATA_F16, of f_dev and x_dev (out) [T][H];
+ * resid_dtype: dtype or STRATA_F32, of resid_dev and resid_out_dev (out, may be
+ * resid_dev; NULL: not written) [T][H].  w_post_dev, w_pre_dev fp32 [H] and
+ * gate_dev fp32 [T] (moe_route's shared_gate, say): NULL for ones.  rstd_dev
+ * fp32 [T][2] (out, or NULL): s0 and s1 for the backward pass, 1 for a norm
+ * that is not taken.  alpha, beta and eps >= 0 finite; H in [1, 2^20].  A row
+ * whose sum of squares leaves fp32 is not normalised to unit size. */
+STRATA_API strata_status moe_norm_residual(int32_t dtype, int32_t resid_dtype, const void* f_dev,
+                                           const void* resid_dev, const float* w_post_dev,
+                                           const float* w_pre_dev, const float* gate_dev, int32_t T,
+                                           int32_t H, int32_t post_norm, float alpha, float beta,
+                                           float eps, void* resid_out_dev, void* x_dev,
+                                           float* rstd_dev, void* stream);
+
+/* Its gradients from dx (by x; NULL: x was not taken) and dresid_out (by r'
+ * from elsewhere; NULL: zeros; one of the two at least).  With
+ *   D = dresid_out + s1 (dx w_pre - r' s1^2 mean(dx w_pre r'))
+ *   dresid = alpha D          dgate[t] = beta sum(D n)       dn = beta gate D
+ *   df = s0 (dn w_post - f s0^2 mean(dn w_post f))           (post_norm == 0: dn)
+ *   dw_pre = sum over rows of dx r' s1     dw_post = sum over rows of dn f s0
+ * resid_out_dev: r' as the forward call wrote it (needed with dx); f_dev
+ * needed with post_norm or dgate; rstd_dev the forward call's.  df_dev in
+ * dtype, dresid_dev in resid_dtype (may be dresid_out_dev), dgate_dev fp32 [T]
+ * (only with gate_dev), dw_post_dev (only with post_norm) and dw_pre_dev (only
+ * with dx) fp32 [H]: each out, or NULL.  The weights' gradients are written
+ * whole (zeros for T == 0), their sums in a fixed order; they alone need the
+ * workspace (moe_norm_workspace_bytes(H)). */
+STRATA_API strata_status moe_norm_residual_bwd(int32_t dtype, int32_t resid_dtype, const void* dx_dev,
+                                               const void* dresid_out_dev, const void* f_dev,
+                                               const void* resid_out_dev, const float* w_post_dev,
+                                               const float* w_pre_dev, const float* gate_dev,
+                                               const float* rstd_dev, int32_t T, int32_t H,
+                                               int32_t post_norm, float alpha, float beta,
+                                               void* df_dev, void* dresid_dev, float* dgate_dev,
+                                               float* dw_post_dev, float* dw_pre_dev, void* ws_dev,
+                                               size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, returns the status latched in the workspace's error
  * word (STRATA_OK when none) and clears the word.  For tests and debugging;
  * it is the one call that synchronises. */

@@ -8,4 +8,4 @@ it (strata_moe.py) and packs canonical weights into its layout (pack.py).
 from . import build  # noqa: F401
 from .strata_moe import *  # noqa: F401,F403
 from .strata_moe import (DeviceLayer, StrataError, load, make_grouped_workspace,  # noqa: F401
-                         make_workspace)
+                         make_norm_workspace, make_workspace)

@@ -1017,6 +1017,8 @@ constexpr int kGroupedDimMax = 1 << 20;
 // A group's rows plus a tile's height (256 at most) are counted in 32 bits.
 constexpr int kGroupedRowsMax = INT32_MAX - 1023;
 
+constexpr int kAct8Cols = 32;                 // elements of an 8-bit block
+
 bool grouped_ws_ok(const void* ws, size_t bytes) {
     return ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 &&
            bytes >= kGroupedWsBytes;
@@ -1194,6 +1196,289 @@ strata_status moe_grouped_mm_fp4(int32_t format, const uint8_t* xq_dev, const ui
     g.fmt = format;
     g.swiglu = swiglu != 0;
     return cuda_status(launch_grouped_mm_fp4(g, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------- a tuning step around the experts
+namespace {
+
+bool dtype16_ok(int32_t t) { return t == STRATA_BF16 || t == STRATA_F16; }
+bool opt16(const void* p) { return p == nullptr || al16(p); }
+
+// Rows [M] of `cols` columns kept in 8 bits, or in the operands' type.
+bool kept_ok(const void* p, const void* scales, int32_t cols) {
+    return al16(p) && (scales == nullptr || (al16(scales) && cols % kAct8Cols == 0));
+}
+bool swiglu_shape_ok(int32_t dtype, int32_t M, int32_t K, int32_t I, int32_t E) {
+    return dtype16_ok(dtype) && M >= 0 && M <= kGroupedRowsMax && K >= 1 && K <= kGroupedDimMax && I >= 1 &&
+           I <= kGroupedDimMax / 2 && E >= 1 && E <= kMaxExperts;
+}
+
+}  // namespace
+
+strata_status moe_grouped_swiglu(int32_t dtype, const void* x_dev, const void* w_dev, int32_t M,
+                                 int32_t K, int32_t I, int32_t E, const int32_t* offsets_dev,
+                                 void* h_dev, void* p_dev, uint8_t* p_scales_dev, void* ws_dev,
+                                 size_t ws_bytes, void* stream) {
+    if (!swiglu_shape_ok(dtype, M, K, I, E) || (p_dev == nullptr && p_scales_dev != nullptr))
+        return STRATA_EINVAL;
+    if (p_scales_dev != nullptr && 2 * I % kAct8Cols != 0) return STRATA_EINVAL;
+    if (M == 0) return STRATA_OK;
+    if (!al16(x_dev) || !al16(w_dev) || !al4(offsets_dev) || !al16(h_dev) ||
+        (p_dev != nullptr && !kept_ok(p_dev, p_scales_dev, 2 * I)) || !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    SwigluArgs a{};
+    a.x = x_dev;
+    a.w = w_dev;
+    a.offsets = offsets_dev;
+    a.h = h_dev;
+    a.p = p_dev;
+    a.scales = p_scales_dev;
+    a.err = &at<Ctl>(ws_dev, 0)->err;
+    a.M = M;
+    a.K = K;
+    a.I = I;
+    a.E = E;
+    a.dtype = dtype;
+    return cuda_status(launch_swiglu(a, static_cast<cudaStream_t>(stream)));
+}
+
+strata_status moe_grouped_swiglu_bwd(int32_t dtype, const void* dy_dev, const void* w_dev,
+                                     const void* p_dev, const uint8_t* p_scales_dev, int32_t M,
+                                     int32_t N, int32_t I, int32_t E, const int32_t* offsets_dev,
+                                     void* dp_dev, void* h_dev, void* ws_dev, size_t ws_bytes,
+                                     void* stream) {
+    if (!swiglu_shape_ok(dtype, M, N, I, E) || (p_scales_dev != nullptr && 2 * I % kAct8Cols != 0))
+        return STRATA_EINVAL;
+    if (M == 0) return STRATA_OK;
+    if (!al16(dy_dev) || !al16(w_dev) || !kept_ok(p_dev, p_scales_dev, 2 * I) || !al4(offsets_dev) ||
+        !al16(dp_dev) || !opt16(h_dev) || !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    SwigluBwdArgs a{};
+    a.dy = dy_dev;
+    a.w = w_dev;
+    a.p = p_dev;
+    a.scales = p_scales_dev;
+    a.offsets = offsets_dev;
+    a.dp = dp_dev;
+    a.h = h_dev;
+    a.err = &at<Ctl>(ws_dev, 0)->err;
+    a.M = M;
+    a.N = N;
+    a.I = I;
+    a.E = E;
+    a.dtype = dtype;
+    return cuda_status(launch_swiglu_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+strata_status moe_act8_save(int32_t dtype, const void* x_dev, int32_t rows, int32_t cols,
+                            uint8_t* q_dev, uint8_t* scales_dev, void* stream) {
+    if (!dtype_ok(dtype) || rows < 0 || rows > kGroupedRowsMax || cols < kAct8Cols ||
+        cols > kGroupedDimMax || cols % kAct8Cols != 0)
+        return STRATA_EINVAL;
+    if (rows == 0) return STRATA_OK;
+    if (!al16(x_dev) || !al16(q_dev) || !al16(scales_dev)) return STRATA_EINVAL;
+    Act8SaveArgs a{};
+    a.x = x_dev;
+    a.q = q_dev;
+    a.scales = scales_dev;
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    return cuda_status(launch_act8_save(a, static_cast<cudaStream_t>(stream)));
+}
+
+strata_status moe_act8_load(const uint8_t* q_dev, const uint8_t* scales_dev, int32_t q_rows,
+                            int32_t cols, const int32_t* perm_dev, int32_t top_k, int32_t rows,
+                            int32_t out_dtype, void* out_dev, void* ws_dev, size_t ws_bytes,
+                            void* stream) {
+    if (!dtype_ok(out_dtype) || rows < 0 || rows > kGroupedRowsMax || q_rows < 0 || cols < kAct8Cols ||
+        cols > kGroupedDimMax || cols % kAct8Cols != 0 || top_k < 1 ||
+        (perm_dev == nullptr && q_rows != rows))
+        return STRATA_EINVAL;
+    if (rows == 0) return STRATA_OK;
+    // no source rows: nothing to point at, and every entry of perm is out of range
+    if ((q_rows > 0 && (!al16(q_dev) || !al16(scales_dev))) || !opt4(perm_dev) || !al16(out_dev) ||
+        !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    Act8LoadArgs a{};
+    a.q = q_dev;
+    a.scales = scales_dev;
+    a.perm = perm_dev;
+    a.top_k = top_k;
+    a.out = out_dev;
+    a.err = &at<Ctl>(ws_dev, 0)->err;
+    a.q_rows = q_rows;
+    a.rows = rows;
+    a.cols = cols;
+    a.out_dtype = out_dtype;
+    return cuda_status(launch_act8_load(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool slots_shape_ok(int32_t dtype, int32_t M, int32_t H, int32_t T, int32_t top_k) {
+    return dtype16_ok(dtype) && M >= 0 && M <= kGroupedRowsMax && H >= 1 && H <= kGroupedDimMax && T >= 0 &&
+           T <= kGroupedRowsMax && top_k >= 1 && top_k <= kMaxTopK &&
+           int64_t(T) * top_k <= kGroupedRowsMax;
+}
+
+}  // namespace
+
+strata_status moe_slots_combine(int32_t dtype, const void* y_dev, int32_t M, int32_t H,
+                                const int32_t* inv_perm_dev, const float* weights_dev, int32_t T,
+                                int32_t top_k, int32_t out_dtype, void* out_dev, void* ws_dev,
+                                size_t ws_bytes, void* stream) {
+    if (!slots_shape_ok(dtype, M, H, T, top_k) || (out_dtype != dtype && out_dtype != STRATA_F32))
+        return STRATA_EINVAL;
+    if (T == 0) return STRATA_OK;
+    if ((M > 0 && !al16(y_dev)) || !al4(inv_perm_dev) || !opt4(weights_dev) || !al16(out_dev) ||
+        !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    SlotsArgs a{};
+    a.y = y_dev;
+    a.inv = inv_perm_dev;
+    a.weights = weights_dev;
+    a.out = out_dev;
+    a.err = &at<Ctl>(ws_dev, 0)->err;
+    a.T = T;
+    a.top_k = top_k;
+    a.M = M;
+    a.H = H;
+    a.dtype = dtype;
+    a.out_dtype = out_dtype;
+    return cuda_status(launch_slots_combine(a, static_cast<cudaStream_t>(stream)));
+}
+
+strata_status moe_slots_spread(int32_t dtype, const void* dout_dev, const int32_t* inv_perm_dev,
+                               const float* weights_dev, const void* y_dev, int32_t T,
+                               int32_t top_k, int32_t M, int32_t H, void* dy_dev,
+                               float* dweights_dev, void* ws_dev, size_t ws_bytes, void* stream) {
+    if (!slots_shape_ok(dtype, M, H, T, top_k)) return STRATA_EINVAL;
+    if (T == 0) return STRATA_OK;
+    if ((dy_dev == nullptr && dweights_dev == nullptr) || (dweights_dev == nullptr) != (y_dev == nullptr))
+        return STRATA_EINVAL;
+    if (!al16(dout_dev) || !al4(inv_perm_dev) || !opt4(weights_dev) || !opt16(y_dev) || !opt16(dy_dev) ||
+        !opt4(dweights_dev) || !grouped_ws_ok(ws_dev, ws_bytes))
+        return STRATA_EINVAL;
+    SlotsArgs a{};
+    a.y = y_dev;
+    a.dout = dout_dev;
+    a.inv = inv_perm_dev;
+    a.weights = weights_dev;
+    a.dy = dy_dev;
+    a.dweights = dweights_dev;
+    a.err = &at<Ctl>(ws_dev, 0)->err;
+    a.T = T;
+    a.top_k = top_k;
+    a.M = M;
+    a.H = H;
+    a.dtype = dtype;
+    return cuda_status(launch_slots_spread(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool norm_shape_ok(int32_t dtype, int32_t resid_dtype, int32_t T, int32_t H) {
+    return dtype16_ok(dtype) && (resid_dtype == dtype || resid_dtype == STRATA_F32) && T >= 0 &&
+           T <= kGroupedRowsMax && H >= 1 && H <= kGroupedDimMax;
+}
+bool finite(float v) { return v - v == 0.0f; }
+
+}  // namespace
+
+size_t moe_norm_workspace_bytes(int32_t H) {
+    return H < 1 || H > kGroupedDimMax ? 0 : kGroupedWsBytes + size_t(kNormParts) * 2 * H * sizeof(float);
+}
+
+strata_status moe_norm_residual(int32_t dtype, int32_t resid_dtype, const void* f_dev,
+                                const void* resid_dev, const float* w_post_dev,
+                                const float* w_pre_dev, const float* gate_dev, int32_t T, int32_t H,
+                                int32_t post_norm, float alpha, float beta, float eps,
+                                void* resid_out_dev, void* x_dev, float* rstd_dev, void* stream) {
+    if (!norm_shape_ok(dtype, resid_dtype, T, H) || !finite(alpha) || !finite(beta) || !finite(eps) ||
+        eps < 0.0f)
+        return STRATA_EINVAL;
+    if (T == 0) return STRATA_OK;            // (an empty tensor's address may be NULL)
+    if ((resid_out_dev == nullptr && x_dev == nullptr) ||
+        (f_dev == nullptr && (post_norm != 0 || gate_dev != nullptr)) ||
+        (post_norm == 0 && w_post_dev != nullptr) || (x_dev == nullptr && w_pre_dev != nullptr))
+        return STRATA_EINVAL;
+    if (!opt16(f_dev) || !al16(resid_dev) || !opt16(w_post_dev) || !opt16(w_pre_dev) || !opt4(gate_dev) ||
+        !opt16(resid_out_dev) || !opt16(x_dev) || !opt4(rstd_dev))
+        return STRATA_EINVAL;
+    NormArgs a{};
+    a.f = f_dev;
+    a.resid = resid_dev;
+    a.w_post = w_post_dev;
+    a.w_pre = w_pre_dev;
+    a.gate = gate_dev;
+    a.resid_out = resid_out_dev;
+    a.x = x_dev;
+    a.rstd = rstd_dev;
+    a.T = T;
+    a.H = H;
+    a.dtype = dtype;
+    a.resid_dtype = resid_dtype;
+    a.post = post_norm != 0;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.eps = eps;
+    return cuda_status(launch_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+strata_status moe_norm_residual_bwd(int32_t dtype, int32_t resid_dtype, const void* dx_dev,
+                                    const void* dresid_out_dev, const void* f_dev,
+                                    const void* resid_out_dev, const float* w_post_dev,
+                                    const float* w_pre_dev, const float* gate_dev,
+                                    const float* rstd_dev, int32_t T, int32_t H, int32_t post_norm,
+                                    float alpha, float beta, void* df_dev, void* dresid_dev,
+                                    float* dgate_dev, float* dw_post_dev, float* dw_pre_dev,
+                                    void* ws_dev, size_t ws_bytes, void* stream) {
+    const bool weights = dw_post_dev != nullptr || dw_pre_dev != nullptr;
+    if (!norm_shape_ok(dtype, resid_dtype, T, H) || !finite(alpha) || !finite(beta) ||
+        (post_norm == 0 && (w_post_dev != nullptr || dw_post_dev != nullptr)))
+        return STRATA_EINVAL;
+    if (!opt16(dw_post_dev) || !opt16(dw_pre_dev) ||
+        (weights && ((T > 0 && ws_dev == nullptr) || (reinterpret_cast<uintptr_t>(ws_dev) & 255u) != 0 ||
+                     ws_bytes < (T > 0 ? moe_norm_workspace_bytes(H) : 0))))
+        return STRATA_EINVAL;
+    if (T > 0) {
+        // weights and gradients only of what the forward call had
+        if ((df_dev == nullptr && dresid_dev == nullptr && dgate_dev == nullptr && !weights) ||
+            (gate_dev == nullptr && dgate_dev != nullptr) ||
+            (dx_dev == nullptr && dresid_out_dev == nullptr) ||
+            (dx_dev == nullptr && (w_pre_dev != nullptr || dw_pre_dev != nullptr)) ||
+            (dx_dev != nullptr && resid_out_dev == nullptr) ||
+            (f_dev == nullptr && (post_norm != 0 || dgate_dev != nullptr)))
+            return STRATA_EINVAL;
+        if (!opt16(dx_dev) || !opt16(dresid_out_dev) || !opt16(f_dev) || !opt16(resid_out_dev) ||
+            !opt16(w_post_dev) || !opt16(w_pre_dev) || !opt4(gate_dev) || !al4(rstd_dev) ||
+            !opt16(df_dev) || !opt16(dresid_dev) || !opt4(dgate_dev))
+            return STRATA_EINVAL;
+    }
+    NormBwdArgs a{};
+    a.dx = dx_dev;
+    a.dresid_out = dresid_out_dev;
+    a.f = f_dev;
+    a.resid_out = resid_out_dev;
+    a.w_post = w_post_dev;
+    a.w_pre = w_pre_dev;
+    a.gate = gate_dev;
+    a.rstd = rstd_dev;
+    a.df = df_dev;
+    a.dresid = dresid_dev;
+    a.dgate = dgate_dev;
+    a.dw_post = dw_post_dev;
+    a.dw_pre = dw_pre_dev;
+    a.parts = ws_dev == nullptr ? nullptr : at<float>(ws_dev, kGroupedWsBytes);
+    a.T = T;
+    a.H = H;
+    a.dtype = dtype;
+    a.resid_dtype = resid_dtype;
+    a.post = post_norm != 0;
+    a.alpha = alpha;
+    a.beta = beta;
+    return cuda_status(launch_norm_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 void strata_set_grid_wait_limit(uint32_t polls) { set_grid_wait_limit(polls); }

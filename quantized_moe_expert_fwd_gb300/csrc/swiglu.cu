@@ -1,0 +1,64 @@
+// swiglu.cu -- the gated feed-forward block over grouped rows: gate and up
+// products with SwiGLU, and the down product's input gradient with SwiGLU's
+// gradient, each one kernel.
+#include "grouped_simt.cuh"
+#include "swiglu.cuh"
+
+namespace strata {
+
+namespace {
+
+struct KeepQuad {
+    SwigluKeep k;
+    __device__ __forceinline__ void operator()(size_t row, int c, const float* v, bool live) const {
+        swiglu_quad(k, row, c, v, live);
+    }
+};
+struct BackQuad {
+    SwigluBack k;
+    __device__ __forceinline__ void operator()(size_t row, int c, const float* v, bool live) const {
+        swiglu_back_quad(k, row, c, v, live);
+    }
+};
+
+template <int MODE, typename EPI>
+cudaError_t swiglu_simt(const GmmArgs& g, const EPI& epi, cudaStream_t s) {
+    const int grid = device_info().sms * 4;
+    if (g.dtype == STRATA_BF16) k_gmm_simt<MODE, __nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(g, epi);
+    else k_gmm_simt<MODE, __half><<<grid, kSimtThreads, 0, s>>>(g, epi);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t s) {
+    GmmArgs g{};
+    g.a = a.x;
+    g.b = a.w;
+    g.offsets = a.offsets;
+    g.err = a.err;
+    g.M = a.M;
+    g.K = a.K;
+    g.N = 2 * a.I;
+    g.E = a.E;
+    g.dtype = a.dtype;
+    const SwigluKeep k{a.h, a.p, a.scales, a.I, a.dtype == STRATA_BF16};
+    return swiglu_simt<kGmmFwd>(g, KeepQuad{k}, s);
+}
+
+cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s) {
+    GmmArgs g{};
+    g.a = a.dy;
+    g.b = a.w;
+    g.offsets = a.offsets;
+    g.err = a.err;
+    g.M = a.M;
+    g.K = a.I;
+    g.N = a.N;
+    g.E = a.E;
+    g.dtype = a.dtype;
+    const SwigluBack k{a.p, a.scales, a.dp, a.h, a.I, a.dtype == STRATA_BF16};
+    return swiglu_simt<kGmmDx>(g, BackQuad{k}, s);
+}
+
+}  // namespace strata

@@ -1,0 +1,134 @@
+// swiglu.cuh -- SwiGLU and its gradient in the epilogue of a grouped product.
+//
+// With p = W x (rows 2i of W gate, 2i + 1 up), g = p[2i], u = p[2i + 1]:
+//   h = g s u,  s = 1 / (1 + e^-g)
+// and, with dh the gradient by h,
+//   du = dh g s,   dg = dh u (s + g s (1 - s)).
+// Both are taken from e^-|g|, which never passes 1 (1 + e^-g leaves the fast
+// quotient's range at g = -87), and 1 - s from it too, so that nothing
+// cancels.  The outputs have 16 bits: the fast exponential and quotient are off
+// by 2 + 1.2 |g| steps of 2^-23, next to roundings of 2^-9 or 2^-12.
+#pragma once
+
+#include "act8.cuh"
+#include "grouped.cuh"
+
+namespace strata {
+
+struct Silu {
+    float s, t;                              // sigmoid(g) and 1 - sigmoid(g)
+};
+__device__ __forceinline__ Silu silu_parts(float g) {
+    const float e = __expf(-fabsf(g));
+    const float r = __fdividef(1.0f, 1.0f + e);
+    return g < 0.0f ? Silu{e * r, r} : Silu{r, e * r};
+}
+__device__ __forceinline__ float swiglu(float g, float u) { return g * silu_parts(g).s * u; }
+struct SwigluGrads {
+    float dg, du, h;
+};
+__device__ __forceinline__ SwigluGrads swiglu_grads(float g, float u, float dh) {
+    const Silu f = silu_parts(g);
+    const float a = g * f.s;
+    return SwigluGrads{dh * u * fmaf(a, f.t, f.s), dh * a, a * u};
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
+    uint32_t r;
+    if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float unpack16(uint32_t half, int bf16) {
+    return bf16 ? __uint_as_float(half << 16) : f16_to_f32(uint16_t(half));
+}
+
+// What the forward epilogue writes: h, and p where it is kept (in the operands'
+// type, or with scales in 8 bits).
+struct SwigluKeep {
+    void* h;
+    void* p;
+    uint8_t* scales;
+    int I, bf16;
+};
+// What the backward epilogue reads and writes.
+struct SwigluBack {
+    const void* p;
+    const uint8_t* scales;
+    void* dp;
+    void* h;                                 // or NULL
+    int I, bf16;
+};
+
+__device__ __forceinline__ void store_u16(void* p, size_t at, uint32_t v) {
+    static_cast<uint16_t*>(p)[at] = uint16_t(v);
+}
+
+// Four columns of p of one row, c (a multiple of 4) on.  Whole warps call it;
+// eight neighbouring lanes hold 32 columns of one row.  live: the row exists
+// (columns past the width are left out here).
+__device__ __forceinline__ void swiglu_quad(const SwigluKeep& k, size_t row, int c, const float* v,
+                                            bool live) {
+    const int cols = 2 * k.I;
+    live = live && c < cols;
+    const bool both = c + 2 < cols;
+    if (k.p != nullptr && k.scales != nullptr) {             // the width is a multiple of 32
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        if (!live) m = 0;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t b = act8_byte(m);
+        if (live) {
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(k.p) + row * cols + c) =
+                b == 255u ? kAct8Nan : act8_codes(v[0], v[1], v[2], v[3], act8_inverse(b));
+            if (c % kAct8Block == 0) k.scales[row * (cols / kAct8Block) + c / kAct8Block] = uint8_t(b);
+        }
+    }
+    if (!live) return;
+    if (k.p != nullptr && k.scales == nullptr) {
+        const size_t at = row * cols + c;
+        const uint32_t a = pack16(v[0], v[1], k.bf16), b = pack16(v[2], v[3], k.bf16);
+        store_u16(k.p, at, a);
+        store_u16(k.p, at + 1, a >> 16);
+        if (both) {
+            store_u16(k.p, at + 2, b);
+            store_u16(k.p, at + 3, b >> 16);
+        }
+    }
+    const uint32_t h = pack16(swiglu(v[0], v[1]), both ? swiglu(v[2], v[3]) : 0.0f, k.bf16);
+    const size_t at = row * k.I + c / 2;
+    store_u16(k.h, at, h);
+    if (both) store_u16(k.h, at + 1, h >> 16);
+}
+
+// Four columns of dh of one row, c (a multiple of 4) on.
+__device__ __forceinline__ void swiglu_back_quad(const SwigluBack& k, size_t row, int c,
+                                                 const float* v, bool live) {
+    if (!live) return;
+    const int n = min(4, k.I - c);
+    const size_t at = row * 2 * k.I + 2 * c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j >= n) break;
+        float g, u;
+        if (k.scales != nullptr) {                            // I is a multiple of 16
+            const uint32_t w = static_cast<const uint16_t*>(k.p)[at / 2 + j];
+            float q[4];
+            act8_values(w, act8_scale(k.scales[(at + 2 * j) / kAct8Block]), q);
+            g = q[0];
+            u = q[1];
+        } else {
+            g = unpack16(static_cast<const uint16_t*>(k.p)[at + 2 * j], k.bf16);
+            u = unpack16(static_cast<const uint16_t*>(k.p)[at + 2 * j + 1], k.bf16);
+        }
+        const SwigluGrads d = swiglu_grads(g, u, v[j]);
+        const uint32_t w = pack16(d.dg, d.du, k.bf16);
+        store_u16(k.dp, at + 2 * j, w);
+        store_u16(k.dp, at + 2 * j + 1, w >> 16);
+        if (k.h != nullptr) store_u16(k.h, row * k.I + c + j, pack16(d.h, 0.0f, k.bf16));
+    }
+}
+
+}  // namespace strata

@@ -75,6 +75,7 @@ def load() -> ctypes.CDLL:
                                " (the CUDA library is required; there is no fallback)")
         lib = ctypes.CDLL(path)
         P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        F = ctypes.c_float
         D, L = ctypes.POINTER(Dims), ctypes.POINTER(LayerPtrs)
         sigs = {
             "moe_workspace_bytes": (SZ, [D, I32]),
@@ -109,6 +110,16 @@ def load() -> ctypes.CDLL:
             "moe_fp4_dequantize": (I32, [I32, P, P, SZ, I32, I32, P, I32, I32, I32, P, P, SZ, P]),
             "moe_grouped_mm_fp4": (I32, [I32, P, P, SZ, P, P, SZ, I32, I32, I32, I32, P, P, I32,
                                          I32, P, P, SZ, P]),
+            "moe_grouped_swiglu": (I32, [I32, P, P, I32, I32, I32, I32, P, P, P, P, P, SZ, P]),
+            "moe_grouped_swiglu_bwd": (I32, [I32, P, P, P, P, I32, I32, I32, I32, P, P, P, P, SZ, P]),
+            "moe_act8_save": (I32, [I32, P, I32, I32, P, P, P]),
+            "moe_act8_load": (I32, [P, P, I32, I32, P, I32, I32, I32, P, P, SZ, P]),
+            "moe_slots_combine": (I32, [I32, P, I32, I32, P, P, I32, I32, I32, P, P, SZ, P]),
+            "moe_slots_spread": (I32, [I32, P, P, P, P, I32, I32, I32, I32, P, P, P, SZ, P]),
+            "moe_norm_workspace_bytes": (SZ, [I32]),
+            "moe_norm_residual": (I32, [I32, I32, P, P, P, P, P, I32, I32, I32, F, F, F, P, P, P, P]),
+            "moe_norm_residual_bwd": (I32, [I32, I32, P, P, P, P, P, P, P, P, I32, I32, I32, F, F, P, P,
+                                            P, P, P, P, SZ, P]),
             "moe_get_device_status": (I32, [P, P]),
             "strata_set_grid_wait_limit": (None, [ctypes.c_uint32]),
             "strata_px_trace_read": (I32, [P, SZ]),
@@ -133,6 +144,9 @@ EXPORTED = ("moe_workspace_bytes", "moe_decode_max_tokens", "moe_layer_decode_ma
             "moe_layer_path", "moe_layer_bucketing", "moe_grouped_workspace_bytes",
             "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw", "moe_fp4_scale_bytes",
             "moe_fp4_quantize", "moe_fp4_dequantize", "moe_grouped_mm_fp4",
+            "moe_grouped_swiglu", "moe_grouped_swiglu_bwd", "moe_act8_save", "moe_act8_load",
+            "moe_slots_combine", "moe_slots_spread", "moe_norm_workspace_bytes",
+            "moe_norm_residual", "moe_norm_residual_bwd",
             "moe_get_device_status",
             "strata_set_grid_wait_limit", "strata_px_trace_read",
             "strata_status_str", "strata_last_cuda_error")
@@ -600,6 +614,275 @@ def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
         y.data_ptr(), ws.data_ptr(), ws.numel(), st)
     if status:
         _check("moe_grouped_mm_fp4", status)
+
+
+# ------------------------------------------- a tuning step around the experts
+def _on_device(dev, stream, tensors):
+    """As _grouped, for calls without a workspace of their own: `dev` is their first tensor's."""
+    if dev < 0 or dev != _get_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("tensors must be on one device" if t.get_device() != dev
+                             else "tensors passed to strata_moe must be contiguous")
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kept(p, p_scales, M, cols, dtype):
+    """Checks p as moe_grouped_swiglu keeps it."""
+    _shape(p, (M, cols), "p")
+    if p_scales is None:
+        if p.dtype is not dtype:
+            raise TypeError(f"p must be {dtype} (or uint8 with p_scales), not {p.dtype}")
+        return
+    if p.dtype is not _U8 or p_scales.dtype is not _U8:
+        raise TypeError("p kept in 8 bits and its scales must be uint8")
+    if cols % 32:
+        raise ValueError("p is kept in 8 bits where its width is a multiple of 32")
+    _shape(p_scales, (M, cols // 32), "p_scales")
+
+
+def moe_grouped_swiglu(x, w, offsets, h, ws, p=None, p_scales=None, stream=None):
+    """h[s] = SwiGLU of w[e] x[s] for the rows s of each group e (x [M][K],
+    w [E][2I][K] with gate and up rows interleaved, h [M][I]); p [M][2I] is
+    kept for the backward pass where it is given, in x's type, or in 8 bits
+    (uint8, with p_scales uint8 [M][2I / 32])."""
+    E, N, K = w.shape
+    M = x.shape[0]
+    _int32(M, K, N, E)
+    st = _grouped(ws, stream, [t for t in (x, w, offsets, h, p, p_scales) if t is not None])
+    dt = _dtype(x, "x", _DTYPES16)
+    if w.dtype is not x.dtype or h.dtype is not x.dtype:
+        raise TypeError(f"x, w and h must have one type, not {x.dtype}, {w.dtype} and {h.dtype}")
+    if N % 2:
+        raise ValueError("w must have a gate and an up row for each column of h")
+    _shape(x, (M, K), "x")
+    _shape(h, (M, N // 2), "h")
+    if p is not None:
+        _kept(p, p_scales, M, N, x.dtype)
+    elif p_scales is not None:
+        raise ValueError("p_scales without p")
+    _offsets(offsets, E)
+    status = (_lib or load()).moe_grouped_swiglu(
+        dt, x.data_ptr(), w.data_ptr(), M, K, N // 2, E, offsets.data_ptr(), h.data_ptr(), _at(p),
+        _at(p_scales), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_grouped_swiglu", status)
+
+
+def moe_grouped_swiglu_bwd(dy, w, p, offsets, dp, ws, p_scales=None, h=None, stream=None):
+    """dp [M][2I], the gradient by the p that moe_grouped_swiglu kept, from the
+    down product's dy [M][N] and weights w [E][N][I]; h [M][I] is computed again
+    where it is given."""
+    E, N, I = w.shape
+    M = dy.shape[0]
+    _int32(M, N, 2 * I, E)
+    st = _grouped(ws, stream, [t for t in (dy, w, p, offsets, dp, p_scales, h) if t is not None])
+    dt = _dtype(dy, "dy", _DTYPES16)
+    if w.dtype is not dy.dtype or dp.dtype is not dy.dtype or (h is not None and h.dtype is not dy.dtype):
+        raise TypeError("dy, w, dp and h must have one type")
+    _shape(dy, (M, N), "dy")
+    _shape(dp, (M, 2 * I), "dp")
+    if h is not None:
+        _shape(h, (M, I), "h")
+    _kept(p, p_scales, M, 2 * I, dy.dtype)
+    _offsets(offsets, E)
+    status = (_lib or load()).moe_grouped_swiglu_bwd(
+        dt, dy.data_ptr(), w.data_ptr(), p.data_ptr(), _at(p_scales), M, N, I, E, offsets.data_ptr(),
+        dp.data_ptr(), _at(h), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_grouped_swiglu_bwd", status)
+
+
+def _act8(q, scales, rows, cols):
+    if q.dtype is not _U8 or scales.dtype is not _U8:
+        raise TypeError("codes and scales must be uint8")
+    _shape(q, (rows, cols), "q")
+    _shape(scales, (rows, cols // 32), "scales")
+
+
+def moe_act8_save(x, q, scales, stream=None):
+    """Rows of x [R][C] (bf16, fp16 or fp32; C a multiple of 32) kept in 8 bits:
+    q uint8 [R][C] and scales uint8 [R][C / 32]."""
+    R, C = x.shape
+    _int32(R, C)
+    st = _on_device(x.get_device(), stream, (x, q, scales))
+    dt = _dtype(x, "x")
+    _act8(q, scales, R, C)
+    status = (_lib or load()).moe_act8_save(dt, x.data_ptr(), R, C, q.data_ptr(), scales.data_ptr(), st)
+    if status:
+        _check("moe_act8_save", status)
+
+
+def moe_act8_load(q, scales, out, ws, perm=None, top_k: int = 1, stream=None):
+    """The values of kept rows into out [rows][C] (bf16, fp16 or fp32); row s from
+    q's row perm[s] / top_k where perm (int32) is given, which may be shorter
+    than out: the rows behind it stay as they are."""
+    R, C = q.shape
+    rows = out.shape[0]
+    _int32(R, C, rows, top_k)
+    st = _grouped(ws, stream, (q, scales, out) if perm is None else (q, scales, out, perm))
+    od = _dtype(out, "out")
+    _act8(q, scales, R, C)
+    _shape(out, (rows, C), "out")
+    if perm is not None:
+        if perm.dtype is not _I32 or perm.dim() != 1 or perm.numel() > rows:
+            raise ValueError("perm must be an int32 vector of at most out's rows")
+        rows = perm.numel()
+        perm = perm.data_ptr()
+    status = (_lib or load()).moe_act8_load(q.data_ptr(), scales.data_ptr(), R, C, perm, top_k, rows, od,
+                                            out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_act8_load", status)
+
+
+def _slots(inv_perm, T, weights):
+    """Slots a token, of inv_perm as moe_permute writes it (or [T][top_k])."""
+    n = inv_perm.numel()
+    if inv_perm.dtype is not _I32 or (n % T if T else n):
+        raise ValueError("inv_perm must be an int32 tensor of tokens x top_k entries")
+    top_k = n // T if T else 1
+    if weights is not None and (weights.dtype is not _F32 or weights.numel() != n):
+        raise ValueError(f"weights must be an fp32 tensor of {n} entries")
+    return top_k
+
+
+def moe_slots_combine(y, inv_perm, out, ws, weights=None, stream=None):
+    """out[t] = sum over k of weights[t][k] y[inv_perm[t][k]] (y [M][H], out
+    [T][H] in y's type or fp32; weights fp32 [T][top_k], None for ones)."""
+    M, H = y.shape
+    T = out.shape[0]
+    _int32(M, H, T)
+    st = _grouped(ws, stream, (y, inv_perm, out) if weights is None else (y, inv_perm, out, weights))
+    dt, od = _dtype(y, "y", _DTYPES16), _dtype(out, "out")
+    if od != dt and od != 2:
+        raise TypeError(f"out must be {y.dtype} or fp32, not {out.dtype}")
+    _shape(out, (T, H), "out")
+    status = (_lib or load()).moe_slots_combine(
+        dt, y.data_ptr(), M, H, inv_perm.data_ptr(), _at(weights), T, _slots(inv_perm, T, weights), od,
+        out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_slots_combine", status)
+
+
+def moe_slots_spread(dout, inv_perm, ws, dy=None, weights=None, y=None, dweights=None, stream=None):
+    """moe_slots_combine's gradients: dy[inv_perm[t][k]] = weights[t][k] dout[t]
+    and, with y, dweights[t][k] = <dout[t], y[inv_perm[t][k]]> (fp32 [T][top_k]).
+    Without weights, dy is the gather of token rows into slot order."""
+    T, H = dout.shape
+    slots = dy if dy is not None else y
+    if slots is None:
+        raise ValueError("nothing to compute: give dy, or y and dweights")
+    M = slots.shape[0]
+    _int32(M, H, T)
+    st = _grouped(ws, stream,
+                  [t for t in (dout, inv_perm, dy, weights, y, dweights) if t is not None])
+    dt = _dtype(dout, "dout", _DTYPES16)
+    for t, what in ((dy, "dy"), (y, "y")):
+        if t is not None:
+            _shape(t, (M, H), what)
+            if t.dtype is not dout.dtype:
+                raise TypeError(f"{what} must be {dout.dtype}, not {t.dtype}")
+    top_k = _slots(inv_perm, T, weights)
+    if dweights is not None and (dweights.dtype is not _F32 or dweights.numel() != T * top_k):
+        raise ValueError(f"dweights must be an fp32 tensor of {T * top_k} entries")
+    status = (_lib or load()).moe_slots_spread(
+        dt, dout.data_ptr(), inv_perm.data_ptr(), _at(weights), _at(y), T, top_k, M, H, _at(dy),
+        _at(dweights), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check("moe_slots_spread", status)
+
+
+def moe_norm_workspace_bytes(H: int) -> int:
+    H = int(H)
+    return 0 if H > 0x7fffffff or H < 0 else int(load().moe_norm_workspace_bytes(H))
+
+
+def make_norm_workspace(H: int, device="cuda") -> torch.Tensor:
+    """A workspace of moe_norm_residual_bwd for rows of H columns."""
+    n = moe_norm_workspace_bytes(H)
+    if n == 0:
+        raise StrataError("moe_norm_workspace_bytes", STRATA_EINVAL)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _norm_types(act, resid, rows, vectors, T, H):
+    """dtype and resid_dtype numbers; rows: (tensor, its type, name) of [T][H] tensors; vectors:
+    (fp32 tensor, length, name)."""
+    for t, dtype, what in rows:
+        if t is not None:
+            if t.dtype is not dtype:
+                raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+            if t.shape != (T, H):
+                raise ValueError(f"{what} must have shape {(T, H)}, not {tuple(t.shape)}")
+    for t, n, what in vectors:
+        if t is not None and (t.dtype is not _F32 or t.numel() != n):
+            raise ValueError(f"{what} must be an fp32 tensor of {n} entries")
+    dt, rt = _DTYPES16.get(act), _DTYPES.get(resid)
+    if dt is None or (rt != dt and rt != 2):
+        raise TypeError(f"f and x must be bf16 or fp16 and the residual of that type or fp32, not {act} "
+                        f"and {resid}")
+    return dt, rt
+
+
+def moe_norm_residual(resid, resid_out=None, f=None, x=None, w_pre=None, w_post=None, gate=None,
+                      post_norm: bool = False, alpha: float = 1.0, beta: float = 1.0,
+                      eps: float = 1e-6, rstd=None, stream=None):
+    """resid_out = alpha resid + beta gate[t] n(f) and x = n(resid_out), the RMS
+    norms after a block (post_norm) and before the next one with their weights
+    (fp32 [H]); resid fp32 or f's type, resid_out may be resid; rstd fp32 [T][2]
+    keeps what the backward pass needs."""
+    T, H = resid.shape
+    _int32(T, H)
+    st = _on_device(resid.get_device(), stream,
+                    [t for t in (resid, resid_out, f, x, w_pre, w_post, gate, rstd) if t is not None])
+    act = f.dtype if f is not None else x.dtype if x is not None else None
+    if act is None:                      # a residual alone: its own type, or any
+        act = resid.dtype if resid.dtype in _DTYPES16 else torch.bfloat16
+    dt, rt = _norm_types(act, resid.dtype, ((f, act, "f"), (x, act, "x"), (resid_out, resid.dtype, "resid_out")),
+                         ((w_pre, H, "w_pre"), (w_post, H, "w_post"), (gate, T, "gate"),
+                          (rstd, 2 * T, "rstd")), T, H)
+    status = (_lib or load()).moe_norm_residual(
+        dt, rt, _at(f), resid.data_ptr(), _at(w_post), _at(w_pre), _at(gate), T, H, 1 if post_norm else 0,
+        alpha, beta, eps, _at(resid_out), _at(x), _at(rstd), st)
+    if status:
+        _check("moe_norm_residual", status)
+
+
+def moe_norm_residual_bwd(resid_out, rstd, ws=None, dx=None, dresid_out=None, f=None, w_pre=None,
+                          w_post=None, gate=None, post_norm: bool = False, alpha: float = 1.0,
+                          beta: float = 1.0, dresid=None, df=None, dgate=None, dw_pre=None,
+                          dw_post=None, stream=None):
+    """moe_norm_residual's gradients from dx and dresid_out (each may be None),
+    with the resid_out and rstd that it wrote: dresid (may be dresid_out), df,
+    dgate fp32 [T], dw_pre and dw_post fp32 [H], each where given (the last two
+    need ws, make_norm_workspace(H))."""
+    T, H = resid_out.shape
+    _int32(T, H)
+    st = _on_device(resid_out.get_device(), stream,
+                    [t for t in (resid_out, rstd, ws, dx, dresid_out, f, w_pre, w_post, gate, dresid, df,
+                                 dgate, dw_pre, dw_post) if t is not None])
+    act = next((t.dtype for t in (dx, f, df) if t is not None), None)
+    if act is None:
+        act = resid_out.dtype if resid_out.dtype in _DTYPES16 else torch.bfloat16
+    rd = resid_out.dtype
+    dt, rt = _norm_types(act, rd, ((dx, act, "dx"), (f, act, "f"), (df, act, "df"),
+                                   (dresid_out, rd, "dresid_out"), (dresid, rd, "dresid")),
+                         ((w_pre, H, "w_pre"), (w_post, H, "w_post"), (gate, T, "gate"),
+                          (rstd, 2 * T, "rstd"), (dgate, T, "dgate"), (dw_pre, H, "dw_pre"),
+                          (dw_post, H, "dw_post")), T, H)
+    if ws is not None and ws.dtype is not _U8:
+        raise ValueError("the workspace must be a contiguous uint8 tensor")
+    status = (_lib or load()).moe_norm_residual_bwd(
+        dt, rt, _at(dx), _at(dresid_out), _at(f), resid_out.data_ptr(), _at(w_post), _at(w_pre), _at(gate),
+        _at(rstd), T, H, 1 if post_norm else 0, alpha, beta, _at(df), _at(dresid), _at(dgate),
+        _at(dw_post), _at(dw_pre), _at(ws), 0 if ws is None else ws.numel(), st)
+    if status:
+        _check("moe_norm_residual_bwd", status)
 
 
 def strata_px_trace_read(nbytes: int = 1024 * 4 * 16 * 8):

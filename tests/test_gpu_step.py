@@ -1,0 +1,180 @@
+"""A tuning step of one residual block of bf16 experts, forward and backward, put
+together from the calls as a program uses them: routed by the layer's own
+router, with p and the block's input kept in 16 or in 8 bits, eager and as a
+captured graph, against the same block in 64 bits under automatic
+differentiation."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_moe_expert_fwd_gb300 as q
+from workloads import gen
+
+pytestmark = pytest.mark.gpu
+
+DIMS = gen.LayerDims(hidden=512, n_experts=32, top_k=4, inter=256, shared_inter=256)
+ALPHA, BETA, EPS = 1.0, 0.5, 1e-6
+
+
+class Block:
+    def __init__(self, T, keep8, seed=0):
+        self.dims, self.keep8 = DIMS, keep8
+        d = self.dims
+        H, E, I, self.k = d.hidden, d.n_experts, d.inter, d.top_k
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        bf = torch.bfloat16
+
+        def draw(*s, scale=1.0, dt=bf):
+            return (scale * torch.randn(*s, generator=g, device="cuda")).to(dt)
+
+        def empty(*s, dt=bf):
+            return torch.zeros(*s, dtype=dt, device="cuda")
+        M, f32, i32 = T * self.k, torch.float32, torch.int32
+        self.T, self.H, self.E, self.I, self.M = T, H, E, I, M
+        self.layer = q.DeviceLayer(gen.draw_layer(d, seed), "cuda")
+        self.r = draw(T, H, scale=2.0, dt=f32)
+        self.w_pre, self.w_post = 1 + draw(H, scale=0.1, dt=f32), 1 + draw(H, scale=0.1, dt=f32)
+        self.wgu, self.wdn = draw(E, 2 * I, H, scale=H ** -0.5), draw(E, H, I, scale=I ** -0.5)
+        self.dr2 = draw(T, H, dt=f32)
+        self.x, self.f, self.xs, self.y, self.h = empty(T, H), empty(T, H), empty(M, H), empty(M, H), empty(M, I)
+        self.r2, self.rstd, self.rstd2 = empty(T, H, dt=f32), empty(T, 2, dt=f32), empty(T, 2, dt=f32)
+        self.ids, self.w, self.sig = empty(T, self.k, dt=i32), empty(T, self.k, dt=f32), empty(T, dt=f32)
+        self.counts, self.off = empty(E, dt=i32), empty(E + 1, dt=i32)
+        self.perm, self.inv = empty(M, dt=i32), empty(M, dt=i32)
+        u8 = torch.uint8
+        self.p = empty(M, 2 * I, dt=u8 if keep8 else bf)
+        self.ps = empty(M, 2 * I // 32, dt=u8) if keep8 else None
+        self.xq, self.xsc = empty(T, H, dt=u8), empty(T, H // 32, dt=u8)
+        self.lws, self.ws, self.nws = q.make_workspace(d, T), q.make_grouped_workspace(), q.make_norm_workspace(H)
+        # gradients
+        self.df, self.dy, self.dp, self.dxs, self.dx = empty(T, H), empty(M, H), empty(M, 2 * I), empty(M, H), empty(T, H)
+        self.h2, self.dr = empty(M, I), empty(T, H, dt=f32)
+        self.dw = empty(T, self.k, dt=f32)
+        self.dgu, self.ddn = empty(E, 2 * I, H, dt=f32), empty(E, H, I, dt=f32)
+        self.dwpre, self.dwpost = empty(H, dt=f32), empty(H, dt=f32)
+
+    def forward(self):
+        q.moe_norm_residual(self.r, x=self.x, w_pre=self.w_pre, eps=EPS, rstd=self.rstd)
+        q.moe_route(self.dims, self.layer, self.x, self.ids, self.w, self.sig, self.lws)
+        q.moe_permute(self.dims, self.ids, self.counts, self.off, self.perm, self.inv, self.lws)
+        if self.keep8:
+            q.moe_act8_save(self.x, self.xq, self.xsc)
+        q.moe_slots_spread(self.x, self.inv, self.ws, dy=self.xs)
+        q.moe_grouped_swiglu(self.xs, self.wgu, self.off, self.h, self.ws, p=self.p, p_scales=self.ps)
+        q.moe_grouped_mm(self.h, self.wdn, self.off, self.y, self.ws)
+        q.moe_slots_combine(self.y, self.inv, self.f, self.ws, weights=self.w)
+        q.moe_norm_residual(self.r, self.r2, f=self.f, w_post=self.w_post, post_norm=True, alpha=ALPHA, beta=BETA,
+                            eps=EPS, rstd=self.rstd2)
+
+    def backward(self):
+        """From dr2, the gradient by r2."""
+        q.moe_norm_residual_bwd(self.r2, self.rstd2, self.nws, dresid_out=self.dr2, f=self.f, w_post=self.w_post,
+                                post_norm=True, alpha=ALPHA, beta=BETA, df=self.df, dresid=self.dr,
+                                dw_post=self.dwpost)
+        q.moe_slots_spread(self.df, self.inv, self.ws, dy=self.dy, weights=self.w, y=self.y, dweights=self.dw)
+        q.moe_grouped_swiglu_bwd(self.dy, self.wdn, self.p, self.off, self.dp, self.ws, p_scales=self.ps, h=self.h2)
+        q.moe_grouped_mm_dw(self.dy, self.h2, self.off, self.ddn, self.ws)
+        if self.keep8:
+            q.moe_act8_load(self.xq, self.xsc, self.xs, self.ws, perm=self.perm, top_k=self.k)
+        q.moe_grouped_mm_dw(self.dp, self.xs, self.off, self.dgu, self.ws)
+        q.moe_grouped_mm_dx(self.dp, self.wgu, self.off, self.dxs, self.ws)
+        q.moe_slots_combine(self.dxs, self.inv, self.dx, self.ws)
+        q.moe_norm_residual_bwd(self.r, self.rstd, self.nws, dx=self.dx, dresid_out=self.dr, w_pre=self.w_pre,
+                                dresid=self.dr, dw_pre=self.dwpre)
+
+    def reference(self):
+        """(r2, gradients) in 64 bits, the routing (ids and weights) as it was chosen."""
+        names = ("r", "w_pre", "w_post", "wgu", "wdn", "w")
+        v = {n: getattr(self, n).double().clone().requires_grad_() for n in names}
+
+        def n(t):
+            return t * torch.rsqrt(t.square().mean(dim=1, keepdim=True) + EPS)
+        x = n(v["r"]) * v["w_pre"]
+        f = torch.zeros_like(x)
+        for e in range(self.E):
+            t, k = (self.ids == e).nonzero(as_tuple=True)
+            p = x[t] @ v["wgu"][e].T
+            h = p[:, 0::2] * torch.sigmoid(p[:, 0::2]) * p[:, 1::2]
+            f = f.index_add(0, t, v["w"][t, k][:, None] * (h @ v["wdn"][e].T))
+        r2 = ALPHA * v["r"] + BETA * n(f) * v["w_post"]
+        (r2 * self.dr2.double()).sum().backward()
+        return r2.detach(), {n: t.grad for n, t in v.items()}
+
+    def grads(self):
+        return dict(r=self.dr, w_pre=self.dwpre, w_post=self.dwpost, wgu=self.dgu, wdn=self.ddn, w=self.dw)
+
+
+def _rel(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+# A product of bf16 factors, each rounded to 2^-9 of itself (about 0.29 of that in the mean square), and
+# its own rounding: about 1.1e-3 a step.  The longest chain (wgu's gradient: x, p, y, f, df, dy, dp) has
+# seven of them, sqrt(7) 1.1e-3 = 3e-3; twice that is allowed.  In 8 bits a kept value is off by up to
+# 2^-4 of itself, 2^-4 / sqrt(3) in the mean square at most, and p enters dp by both factors:
+# sqrt(2) 3.6e-2, with x's own 3.6e-2 in wgu's gradient 6.3e-2.
+LIMIT = {False: 6e-3, True: 6.5e-2}
+# w's gradient is <df, y>: both factors have such a chain (sqrt(2)), and as df is orthogonal to f = sum w y
+# (the norm after the block), one of the four directions of a token's weights cancels (sqrt(4 / 3)).
+LIMIT_W = {k: v * (8 / 3) ** 0.5 for k, v in LIMIT.items()}
+
+
+def _check(b):
+    r2, want = b.reference()
+    assert _rel(b.r2 - b.r, r2 - b.r.double()) < LIMIT[False]
+    for n, g in b.grads().items():
+        limit = (LIMIT_W if n == "w" else LIMIT)[b.keep8]
+        assert _rel(g, want[n]) < limit, (n, _rel(g, want[n]))
+    for ws in (b.ws, b.lws):
+        assert q.moe_get_device_status(ws) == q.STRATA_OK
+
+
+@pytest.mark.parametrize("keep8", [False, True])
+@pytest.mark.parametrize("T", [1, 7, 40, 300, 2000])
+def test_step_against_automatic_differentiation(T, keep8):
+    b = Block(T, keep8, seed=T)
+    b.forward()
+    b.backward()
+    _check(b)
+
+
+@pytest.mark.parametrize("keep8", [False, True])
+def test_captured_step_with_other_tokens(keep8):
+    """Captured once, replayed with other tokens (so other routing, offsets and slots)."""
+    b = Block(200, keep8, seed=3)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b.forward()
+        b.backward()
+        with torch.cuda.graph(g, stream=s):
+            b.forward()
+            b.backward()
+    torch.cuda.synchronize()
+    gen2 = torch.Generator(device="cuda").manual_seed(99)
+    for _ in range(2):
+        b.r.copy_(2 * torch.randn(b.T, b.H, generator=gen2, device="cuda"))
+        g.replay()
+        torch.cuda.synchronize()
+        _check(b)
+    eager = Block(200, keep8, seed=3)
+    eager.r.copy_(b.r)
+    eager.forward()
+    eager.backward()
+    for n, t in eager.grads().items():
+        assert torch.equal(t, b.grads()[n]), n
+
+
+def test_single_tokens_are_served_alike():
+    """A prompt's tokens one at a time give the block's outputs up to the roundings of two kernels."""
+    b = Block(24, False, seed=5)
+    b.forward()
+    for t in (0, 11, 23):
+        one = Block(1, False, seed=5)
+        for n in ("layer", "wgu", "wdn", "w_pre", "w_post"):
+            setattr(one, n, getattr(b, n))
+        one.r.copy_(b.r[t:t + 1])
+        one.forward()
+        assert torch.equal(one.ids, b.ids[t:t + 1])
+        assert _rel(one.r2 - one.r, (b.r2 - b.r)[t:t + 1].double()) < LIMIT[False]
+    assert np.isfinite(b.r2.cpu().numpy()).all()
