@@ -43,6 +43,7 @@ cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t s) {
     g.E = a.E;
     g.dtype = a.dtype;
     const SwigluKeep k{a.h, a.p, a.scales, a.I, a.dtype == STRATA_BF16};
+    if (grouped_tc_takes(kGmmFwd, g)) return launch_swiglu_tc(g, k, s);
     return swiglu_simt<kGmmFwd>(g, KeepQuad{k}, s);
 }
 
@@ -58,6 +59,7 @@ cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s) {
     g.E = a.E;
     g.dtype = a.dtype;
     const SwigluBack k{a.p, a.scales, a.dp, a.h, a.I, a.dtype == STRATA_BF16};
+    if (grouped_tc_takes(kGmmDx, g)) return launch_swiglu_back_tc(g, k, s);
     return swiglu_simt<kGmmDx>(g, BackQuad{k}, s);
 }
 

@@ -12,6 +12,7 @@
 
 #include "act8.cuh"
 #include "grouped.cuh"
+#include "grouped.h"
 
 namespace strata {
 
@@ -59,6 +60,10 @@ struct SwigluBack {
     void* h;                                 // or NULL
     int I, bf16;
 };
+
+// On the tensor cores (g: the product's sizes and operands).
+cudaError_t launch_swiglu_tc(const GmmArgs& g, const SwigluKeep& k, cudaStream_t s);
+cudaError_t launch_swiglu_back_tc(const GmmArgs& g, const SwigluBack& k, cudaStream_t s);
 
 __device__ __forceinline__ void store_u16(void* p, size_t at, uint32_t v) {
     static_cast<uint16_t*>(p)[at] = uint16_t(v);

@@ -1,0 +1,12 @@
+// swiglu_back_tc.cu -- SwiGLU's gradient on the tensor cores.
+#include "swiglu_tc.cuh"
+
+namespace strata {
+
+cudaError_t launch_swiglu_back_tc(const GmmArgs& g, const SwigluBack& k, cudaStream_t s) {
+    const SwigluBackPiece epi{k, gt_vec(k.p, size_t(2) * k.I * (k.scales ? 1 : 2)),
+                              gt_vec(k.dp, size_t(4) * k.I), k.h ? gt_vec(k.h, size_t(k.I) * 2) : 0};
+    return gt_pick<kGmmDx>(g, epi, s);
+}
+
+}  // namespace strata
