@@ -1,110 +1,143 @@
-// act8.cu -- rows to 8 bits and back.
-#include <type_traits>
-
+// act8.cu -- rows to 8 bits and back.  Bound by memory: 3.03 bytes an element
+// each way in 16 bits.  A lane takes 16 elements (an access of 16 bytes of
+// codes, of 32 in 16 bits), two lanes a block of 32, and has the loads of
+// kA8Ahead such pieces under way.
 #include "act8.cuh"
-#include "grouped.cuh"
 #include "grouped.h"
+#include "rows.cuh"
 
 namespace strata {
 
 namespace {
 
-constexpr int kA8Threads = 256;
+constexpr int kA8Threads = 256, kA8Ahead = 2;
 
-// A lane takes 8 elements, four lanes a block of 32.
 template <typename T>
-__device__ __forceinline__ void a8_load(const T* p, float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-        const T* e = reinterpret_cast<const T*>(&a);
+struct Raw16 {                               // 16 elements
+    static constexpr int kParts = int(sizeof(T)) / 2;
+    Raw<T, 16 / kParts> r[kParts];
+    __device__ __forceinline__ float get(int j) const { return r[j / (16 / kParts)].get(j % (16 / kParts)); }
+};
+template <typename T>
+__device__ __forceinline__ Raw16<T> ld16(const T* p, bool wide) {
+    Raw16<T> v;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = to_f32(e[j]);
-    }
+    for (int i = 0; i < Raw16<T>::kParts; ++i) ld_words(p + i * (16 / Raw16<T>::kParts), wide, v.r[i].w);
+    return v;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kA8Threads) k_act8_save(const T* x, size_t units, uint8_t* q,
-                                                          uint8_t* scales) {
+                                                          uint8_t* scales, bool wide) {
+    pdl_launch();
+    pdl_wait();
     const size_t step = size_t(gridDim.x) * kA8Threads;
-    // units is a multiple of 4: the lanes of a block stay together
-    for (size_t i = size_t(blockIdx.x) * kA8Threads + threadIdx.x; i < units; i += step) {
-        float v[8];
-        a8_load(x + i * 8, v);
-        uint32_t m = 0;
+    // units (of 16 elements) is even: the two lanes of a block stay together
+    for (size_t i0 = size_t(blockIdx.x) * kA8Threads + threadIdx.x; i0 < units; i0 += kA8Ahead * step) {
+        Raw16<T> v[kA8Ahead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-        const uint32_t group = 0xfu << (threadIdx.x & 28);
-        m = max(m, __shfl_xor_sync(group, m, 1));
-        m = max(m, __shfl_xor_sync(group, m, 2));
-        const uint32_t b = act8_byte(m);
-        const float inv = act8_inverse(b);
-        uint2 w = make_uint2(act8_codes(v[0], v[1], v[2], v[3], inv), act8_codes(v[4], v[5], v[6], v[7], inv));
-        if (b == 255u) w = make_uint2(kAct8Nan, kAct8Nan);
-        *reinterpret_cast<uint2*>(q + i * 8) = w;
-        if (i % 4 == 0) scales[i / 4] = uint8_t(b);
+        for (int n = 0; n < kA8Ahead; ++n)
+            if (i0 + n * step < units) v[n] = ld16(x + (i0 + n * step) * 16, wide);
+#pragma unroll
+        for (int n = 0; n < kA8Ahead; ++n) {
+            const size_t i = i0 + n * step;
+            if (i >= units) break;
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[n].get(j)) & 0x7fffffffu);
+            m = max(m, __shfl_xor_sync(0x3u << (threadIdx.x & 30), m, 1));
+            const uint32_t b = act8_byte(m);
+            const float inv = act8_inverse(b);
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = b == 255u ? kAct8Nan
+                                 : act8_codes(v[n].get(4 * j), v[n].get(4 * j + 1), v[n].get(4 * j + 2),
+                                              v[n].get(4 * j + 3), inv);
+            st_words(q + i * 16, false, w);
+            if (i % 2 == 0) scales[i / 2] = uint8_t(b);
+        }
     }
 }
 
 // A value that fp16 cannot hold reads as its largest.
 template <typename T>
 __device__ __forceinline__ float a8_fit(float v) {
-    if constexpr (sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value)
+    if constexpr (std::is_same<T, __half>::value)
         if (fabsf(v) > 65504.0f) return copysignf(65504.0f, v);       // (not a NaN)
     return v;
 }
 
-// Destination row r from source row perm[r] / top_k (perm NULL: r).
+// Block (bx, by): bx lanes along a row, by rows at a time.  Destination row r
+// from source row perm[r] / top_k (perm NULL: r).
 template <typename T>
-__global__ void __launch_bounds__(kA8Threads) k_act8_load(Act8LoadArgs a) {
-    const int per = a.cols / 8;                       // units of a row
-    const size_t units = size_t(a.rows) * per, step = size_t(gridDim.x) * kA8Threads;
-    T* out = static_cast<T*>(a.out);
-    for (size_t i = size_t(blockIdx.x) * kA8Threads + threadIdx.x; i < units; i += step) {
-        const size_t r = i / per;
-        const int c = int(i % per);
-        long long src = (long long)r;
-        if (a.perm != nullptr) {
-            const int p = __ldg(a.perm + r);
-            src = p < 0 ? -1 : p / a.top_k;
-        }
-        float v[8] = {};
-        if (src < 0 || src >= a.q_rows) {
-            if (c == 0) latch(a.err, STRATA_EBADROUTE);
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.q + size_t(src) * a.cols) + c);
-            const float s = act8_scale(__ldg(a.scales + size_t(src) * (a.cols / kAct8Block) + c / 4));
-            act8_values(w.x, s, v);
-            act8_values(w.y, s, v + 4);
-        }
-        T o[8];
+__global__ void __launch_bounds__(kA8Threads) k_act8_load(Act8LoadArgs a, bool wide) {
+    pdl_launch();
+    pdl_wait();
+    const int c = int(blockIdx.y * blockDim.x + threadIdx.x) * 16;
+    if (c >= a.cols) return;
+    const size_t step = size_t(gridDim.x) * blockDim.y;
+    T* out = static_cast<T*>(a.out) + c;
+    for (size_t r0 = size_t(blockIdx.x) * blockDim.y + threadIdx.y; r0 < size_t(a.rows); r0 += kA8Ahead * step) {
+        uint32_t w[kA8Ahead][4], b[kA8Ahead];
+        bool there[kA8Ahead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = from_f32<T>(a8_fit<T>(v[j]));
+        for (int n = 0; n < kA8Ahead; ++n) {
+            const size_t r = r0 + n * step;
+            there[n] = false;
+            if (r >= size_t(a.rows)) continue;
+            int src = int(r);
+            if (a.perm != nullptr) {
+                const int p = __ldg(a.perm + r);
+                src = p < 0 ? -1 : p / a.top_k;
+            }
+            there[n] = src >= 0 && src < a.q_rows;
+            if (there[n]) {
+                ld_words(a.q + size_t(src) * a.cols + c, false, w[n]);
+                b[n] = __ldg(a.scales + size_t(src) * (a.cols / kAct8Block) + c / kAct8Block);
+            } else if (c == 0) {
+                latch(a.err, STRATA_EBADROUTE);
+            }
+        }
 #pragma unroll
-        for (int j = 0; j < int(sizeof(T)) / 2; ++j)
-            reinterpret_cast<uint4*>(out + i * 8)[j] = reinterpret_cast<const uint4*>(o)[j];
+        for (int n = 0; n < kA8Ahead; ++n) {
+            const size_t r = r0 + n * step;
+            if (r >= size_t(a.rows)) break;
+            float v[16] = {};
+            if (there[n]) {
+                const float s = act8_scale(b[n]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) act8_values(w[n][j], s, v + 4 * j);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = a8_fit<T>(v[j]);
+            T* o = out + r * a.cols;
+            if constexpr (sizeof(T) == 4) {
+                st_row<T, 8>(o, reinterpret_cast<const float(&)[8]>(v[0]), wide);
+                st_row<T, 8>(o + 8, reinterpret_cast<const float(&)[8]>(v[8]), wide);
+            } else {
+                st_row<T, 16>(o, v, wide);
+            }
+        }
     }
-}
-
-int a8_grid(size_t units) {
-    const size_t want = (units + kA8Threads - 1) / kA8Threads, most = size_t(device_info().sms) * 8;
-    return int(want < most ? want : most);
 }
 
 template <typename T>
 cudaError_t run_save(const Act8SaveArgs& a, cudaStream_t s) {
-    const size_t units = size_t(a.rows) * a.cols / 8;
-    k_act8_save<T><<<a8_grid(units), kA8Threads, 0, s>>>(static_cast<const T*>(a.x), units, a.q, a.scales);
-    return cudaGetLastError();
+    const size_t units = size_t(a.rows) * a.cols / 16, per = kA8Threads * kA8Ahead;
+    const size_t want = (units + per - 1) / per, most = size_t(device_info().sms) * 16;
+    return row_launch(k_act8_save<T>, dim3(unsigned(want < most ? want : most)), dim3(kA8Threads), s,
+                      static_cast<const T*>(a.x), units, a.q, a.scales, aligned32(a.x, 0));
 }
 template <typename T>
 cudaError_t run_load(const Act8LoadArgs& a, cudaStream_t s) {
-    k_act8_load<T><<<a8_grid(size_t(a.rows) * a.cols / 8), kA8Threads, 0, s>>>(a);
-    return cudaGetLastError();
+    const int units = a.cols / 16;
+    int bx = 2;
+    while (bx < units && bx < kA8Threads) bx *= 2;
+    const int by = kA8Threads / bx, pieces = (units + bx - 1) / bx, per = by * kA8Ahead;
+    const int want = (a.rows + per - 1) / per, most = (device_info().sms * 32 + pieces - 1) / pieces;
+    return row_launch(k_act8_load<T>, dim3(want < most ? want : most, pieces), dim3(bx, by), s, a,
+                      aligned32(a.out, size_t(a.cols) * sizeof(T)));
 }
 
 }  // namespace

@@ -2,88 +2,193 @@
 // that: its row's gradient spread over its slots, the weights' as dot products.
 //   combine  out[t] = sum_k w[t][k] y[slot(t, k)]
 //   spread   dy[slot(t, k)] = w[t][k] dout[t],  dw[t][k] = <dout[t], y[slot(t, k)]>
-#include "grouped.cuh"
+// Both are bound by memory: each row of y, dy, dout and out moves once.  A
+// thread has V columns of one token (V the most that the rows' alignment lets
+// one access take), so a token's row is read and written once however many
+// slots it has, and the loads of kSlAhead slots are under way together.
 #include "grouped.h"
+#include "rows.cuh"
 
 namespace strata {
 
 namespace {
 
-constexpr int kSlThreads = 128;
+constexpr int kSlAhead = 8;
+constexpr int kSlThreads = 128;              // of a block with several tokens
+constexpr int kSlRow = 256;                  // most threads of a token
 
-// The slots of a token; -1 for one outside [0, M).
-__device__ __forceinline__ int slot_of(const SlotsArgs& a, size_t t, int k) {
-    const int s = __ldg(a.inv + t * a.top_k + k);
-    return s < 0 || s >= a.M ? -1 : s;
+// The slots k0 .. of a token and their weights (-1, 0 where there is none).
+__device__ __forceinline__ void slots_of(const SlotsArgs& a, size_t t, int k0, bool report,
+                                         int (&slot)[kSlAhead], float (&w)[kSlAhead]) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kSlAhead; ++i) {
+        const int k = k0 + i;
+        slot[i] = -1;
+        w[i] = 0.0f;
+        if (k >= a.top_k) continue;
+        const int s = __ldg(a.inv + t * a.top_k + k);
+        w[i] = a.weights ? __ldg(a.weights + t * a.top_k + k) : 1.0f;
+        if (s < 0 || s >= a.M) bad = true;
+        else slot[i] = s;
+    }
+    if (bad && report) latch(a.err, STRATA_EBADROUTE);
+}
+
+// Block (bx, by): by tokens, bx threads along a row; grid.y pieces of a row.
+template <typename T, typename TO, int V>
+__global__ void __launch_bounds__(kSlRow) k_slots_combine(SlotsArgs a, bool wide_out) {
+    pdl_launch();
+    pdl_wait();
+    const size_t t = size_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int c = int(blockIdx.y * blockDim.x + threadIdx.x) * V;
+    if (t >= size_t(a.T) || c >= a.H) return;
+    const T* y = static_cast<const T*>(a.y) + c;
+    float sum[V] = {};
+    for (int k0 = 0; k0 < a.top_k; k0 += kSlAhead) {
+        int slot[kSlAhead];
+        float w[kSlAhead];
+        slots_of(a, t, k0, c == 0, slot, w);
+        Raw<T, V> r[kSlAhead];
+#pragma unroll
+        for (int i = 0; i < kSlAhead; ++i)
+            if (slot[i] >= 0) r[i] = ld_row<T, V>(y + size_t(slot[i]) * a.H);
+#pragma unroll
+        for (int i = 0; i < kSlAhead; ++i)
+            if (slot[i] >= 0) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) sum[j] = fmaf(w[i], r[i].get(j), sum[j]);
+            }
+    }
+    st_row<TO, V>(static_cast<TO*>(a.out) + t * a.H + c, sum, wide_out);
+}
+
+// Block (bx, by) as above, but the threads of a token take its whole row: bx
+// up to 32 for several tokens a block, by = 1 above.  DW: dweights too.
+template <typename T, int V, bool DW>
+__global__ void __launch_bounds__(kSlRow) k_slots_spread(SlotsArgs a) {
+    __shared__ float part[kSlRow / 32][kSlAhead];
+    pdl_launch();
+    pdl_wait();
+    const size_t t = size_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = t < size_t(a.T);
+    const T* dout = static_cast<const T*>(a.dout) + (live ? t : 0) * a.H;
+    const T* y = static_cast<const T*>(a.y);
+    T* dy = static_cast<T*>(a.dy);
+    for (int k0 = 0; k0 < a.top_k; k0 += kSlAhead) {
+        int slot[kSlAhead];
+        float w[kSlAhead], dot[kSlAhead] = {};
+        slots_of(a, live ? t : 0, k0, live && threadIdx.x == 0, slot, w);
+        for (int c = int(threadIdx.x) * V; live && c < a.H; c += int(blockDim.x) * V) {
+            const Raw<T, V> rd = ld_row<T, V>(dout + c);
+            Raw<T, V> r[kSlAhead];
+            if (DW) {
+#pragma unroll
+                for (int i = 0; i < kSlAhead; ++i)
+                    if (slot[i] >= 0) r[i] = ld_row<T, V>(y + size_t(slot[i]) * a.H + c);
+            }
+            float d[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] = rd.get(j);
+#pragma unroll
+            for (int i = 0; i < kSlAhead; ++i) {
+                if (slot[i] < 0) continue;
+                if (dy) {
+                    T* p = dy + size_t(slot[i]) * a.H + c;
+                    if (a.weights) {
+                        float o[V];
+#pragma unroll
+                        for (int j = 0; j < V; ++j) o[j] = w[i] * d[j];
+                        st_row<T, V>(p, o);
+                    } else if constexpr (Raw<T, V>::kBytes == 2) {
+                        *reinterpret_cast<uint16_t*>(p) = uint16_t(rd.w[0]);
+                    } else {
+                        st_words(p, false, rd.w);
+                    }
+                }
+                if (DW) {
+                    // a row's thread sums V columns at a time
+                    float s = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) s = fmaf(d[j], r[i].get(j), s);
+                    dot[i] += s;
+                }
+            }
+        }
+        if (!DW) continue;
+#pragma unroll
+        for (int i = 0; i < kSlAhead; ++i) dot[i] = group_sum(dot[i], min(32, int(blockDim.x)));
+        float* out = a.dweights + t * a.top_k + k0;
+        if (blockDim.x <= 32) {
+#pragma unroll
+            for (int i = 0; i < kSlAhead; ++i)
+                if (live && threadIdx.x == 0 && k0 + i < a.top_k) out[i] = dot[i];
+            continue;
+        }
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < kSlAhead; ++i) part[warp][i] = dot[i];
+        }
+        __syncthreads();
+        if (threadIdx.x < kSlAhead && k0 + int(threadIdx.x) < a.top_k) {
+            float s = 0.0f;
+            for (int i = 0; i < int(blockDim.x) >> 5; ++i) s += part[i][threadIdx.x];
+            out[threadIdx.x] = s;
+        }
+        __syncthreads();
+    }
+}
+
+// Threads along a row of `units` accesses: a power of two.
+int threads_along(int units, int most) {
+    int n = 1;
+    while (n < units && n < most) n *= 2;
+    return n;
+}
+
+template <typename T, typename TO, int V>
+cudaError_t run_combine(const SlotsArgs& a, cudaStream_t s) {
+    const int units = (a.H + V - 1) / V, bx = threads_along(units, kSlThreads), by = kSlThreads / bx;
+    const dim3 grid((a.T + by - 1) / by, (units + bx - 1) / bx);
+    return row_launch(k_slots_combine<T, TO, V>, grid, dim3(bx, by), s, a,
+                      aligned32(a.out, size_t(a.H) * sizeof(TO)));
+}
+template <typename T, int V>
+cudaError_t run_spread(const SlotsArgs& a, cudaStream_t s) {
+    const int units = (a.H + V - 1) / V, bx = threads_along(units, kSlRow);
+    const int by = bx <= 32 ? kSlThreads / bx : 1;
+    const dim3 grid((a.T + by - 1) / by);
+    return a.dweights ? row_launch(k_slots_spread<T, V, true>, grid, dim3(bx, by), s, a)
+                      : row_launch(k_slots_spread<T, V, false>, grid, dim3(bx, by), s, a);
 }
 
 template <typename T, typename TO>
-__global__ void __launch_bounds__(kSlThreads) k_slots_combine(SlotsArgs a) {
-    const size_t t = blockIdx.x;
-    const T* y = static_cast<const T*>(a.y);
-    TO* out = static_cast<TO*>(a.out);
-    for (int c = threadIdx.x; c < a.H; c += kSlThreads) {
-        float sum = 0.0f;
-        for (int k = 0; k < a.top_k; ++k) {
-            const int s = slot_of(a, t, k);
-            if (s < 0) {
-                if (c == 0) latch(a.err, STRATA_EBADROUTE);
-                continue;
-            }
-            const float w = a.weights ? __ldg(a.weights + t * a.top_k + k) : 1.0f;
-            sum = fmaf(w, to_f32(y[size_t(s) * a.H + c]), sum);
-        }
-        out[t * a.H + c] = from_f32<TO>(sum);
-    }
+cudaError_t pick_combine(const SlotsArgs& a, cudaStream_t s) {
+    return a.H % 8 == 0   ? run_combine<T, TO, 8>(a, s)
+           : a.H % 4 == 0 ? run_combine<T, TO, 4>(a, s)
+           : a.H % 2 == 0 ? run_combine<T, TO, 2>(a, s)
+                          : run_combine<T, TO, 1>(a, s);
 }
-
 template <typename T>
-__global__ void __launch_bounds__(kSlThreads) k_slots_spread(SlotsArgs a) {
-    __shared__ float part[kSlThreads / 32];
-    const size_t t = blockIdx.x;
-    const T* dout = static_cast<const T*>(a.dout) + t * a.H;
-    for (int k = 0; k < a.top_k; ++k) {
-        const int s = slot_of(a, t, k);
-        if (s < 0 && threadIdx.x == 0) latch(a.err, STRATA_EBADROUTE);
-        const float w = a.weights ? __ldg(a.weights + t * a.top_k + k) : 1.0f;
-        float dot = 0.0f;
-        if (s >= 0)
-            for (int c = threadIdx.x; c < a.H; c += kSlThreads) {
-                const float d = to_f32(dout[c]);
-                const size_t at = size_t(s) * a.H + c;
-                if (a.dy) static_cast<T*>(a.dy)[at] = from_f32<T>(w * d);
-                if (a.dweights) dot = fmaf(d, to_f32(static_cast<const T*>(a.y)[at]), dot);
-            }
-        if (a.dweights) {
-            dot = warp_sum(dot);
-            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                for (int i = 1; i < kSlThreads / 32; ++i) dot += part[i];
-                a.dweights[t * a.top_k + k] = dot;
-            }
-            __syncthreads();
-        }
-    }
+cudaError_t pick_spread(const SlotsArgs& a, cudaStream_t s) {
+    return a.H % 8 == 0   ? run_spread<T, 8>(a, s)
+           : a.H % 4 == 0 ? run_spread<T, 4>(a, s)
+           : a.H % 2 == 0 ? run_spread<T, 2>(a, s)
+                          : run_spread<T, 1>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_slots_combine(const SlotsArgs& a, cudaStream_t s) {
-    if (a.dtype == STRATA_BF16) {
-        if (a.out_dtype == STRATA_F32) k_slots_combine<__nv_bfloat16, float><<<a.T, kSlThreads, 0, s>>>(a);
-        else k_slots_combine<__nv_bfloat16, __nv_bfloat16><<<a.T, kSlThreads, 0, s>>>(a);
-    } else {
-        if (a.out_dtype == STRATA_F32) k_slots_combine<__half, float><<<a.T, kSlThreads, 0, s>>>(a);
-        else k_slots_combine<__half, __half><<<a.T, kSlThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    if (a.dtype == STRATA_BF16)
+        return a.out_dtype == STRATA_F32 ? pick_combine<__nv_bfloat16, float>(a, s)
+                                         : pick_combine<__nv_bfloat16, __nv_bfloat16>(a, s);
+    return a.out_dtype == STRATA_F32 ? pick_combine<__half, float>(a, s) : pick_combine<__half, __half>(a, s);
 }
 
 cudaError_t launch_slots_spread(const SlotsArgs& a, cudaStream_t s) {
-    if (a.dtype == STRATA_BF16) k_slots_spread<__nv_bfloat16><<<a.T, kSlThreads, 0, s>>>(a);
-    else k_slots_spread<__half><<<a.T, kSlThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return a.dtype == STRATA_BF16 ? pick_spread<__nv_bfloat16>(a, s) : pick_spread<__half>(a, s);
 }
 
 }  // namespace strata
