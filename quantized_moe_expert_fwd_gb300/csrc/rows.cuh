@@ -26,26 +26,39 @@ struct Raw {
 };
 
 // `wide`: the address is a multiple of 32 bytes (only asked where V elements
-// have that many); otherwise of their size, or of 16 bytes.
-template <int WORDS>
+// have that many); otherwise of their size, or of 16 bytes.  NC: nobody writes
+// there while the kernel runs.
+template <bool NC = true, int WORDS>
 __device__ __forceinline__ void ld_words(const void* p, bool wide, uint32_t (&w)[WORDS]) {
-    if constexpr (WORDS == 1) w[0] = __ldg(static_cast<const uint32_t*>(p));
-    else if constexpr (WORDS == 2) {
-        const uint2 v = __ldg(static_cast<const uint2*>(p));
+    if constexpr (WORDS == 1) {
+        const uint32_t* q = static_cast<const uint32_t*>(p);
+        w[0] = NC ? __ldg(q) : *q;
+    } else if constexpr (WORDS == 2) {
+        const uint2* q = static_cast<const uint2*>(p);
+        const uint2 v = NC ? __ldg(q) : *q;
         w[0] = v.x;
         w[1] = v.y;
     } else if constexpr (WORDS == 4) {
-        const uint4 v = __ldg(static_cast<const uint4*>(p));
+        const uint4* q = static_cast<const uint4*>(p);
+        const uint4 v = NC ? __ldg(q) : *q;
         w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     } else {
         static_assert(WORDS == 8, "words of an access");
         if (wide) {
-            asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                           "=r"(w[6]), "=r"(w[7])
-                         : "l"(p));
+            if (NC)
+                asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                               "=r"(w[6]), "=r"(w[7])
+                             : "l"(p));
+            else
+                asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                               "=r"(w[6]), "=r"(w[7])
+                             : "l"(p)
+                             : "memory");
         } else {
-            const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+            const uint4* q = static_cast<const uint4*>(p);
+            const uint4 a = NC ? __ldg(q) : q[0], b = NC ? __ldg(q + 1) : q[1];
             w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
             w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
         }
@@ -68,11 +81,15 @@ __device__ __forceinline__ void st_words(void* p, bool wide, const uint32_t (&w)
         }
     }
 }
-template <typename T, int V>
+template <typename T, int V, bool NC = true>
 __device__ __forceinline__ Raw<T, V> ld_row(const T* p, bool wide = false) {
     Raw<T, V> r;
-    if constexpr (Raw<T, V>::kBytes == 2) r.w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
-    else ld_words(p, wide, r.w);
+    if constexpr (Raw<T, V>::kBytes == 2) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+        r.w[0] = NC ? __ldg(q) : *q;
+    } else {
+        ld_words<NC>(p, wide, r.w);
+    }
     return r;
 }
 // One rounding, to nearest even, into T.

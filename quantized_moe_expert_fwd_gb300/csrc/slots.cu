@@ -13,13 +13,18 @@ namespace strata {
 
 namespace {
 
-constexpr int kSlAhead = 8;
-constexpr int kSlThreads = 128;              // of a block with several tokens
-constexpr int kSlRow = 256;                  // most threads of a token
+// Slots whose loads are under way together, and most threads along a token's
+// row (2048 tokens of 8 slots and 2048 columns, spread with weights' gradients;
+// 16384 tokens gathered into 65536 slots; us): 256 threads and 8 slots 36, 65;
+// 256 and 4 33, 62; 128 and 8 29.5, 55; 128 and 4 28.9, 51 (at the copy's rate
+// 21, 49).
+constexpr int kSlAhead = 4;
+constexpr int kSlThreads = 128;
 
 // The slots k0 .. of a token and their weights (-1, 0 where there is none).
-__device__ __forceinline__ void slots_of(const SlotsArgs& a, size_t t, int k0, bool report,
-                                         int (&slot)[kSlAhead], float (&w)[kSlAhead]) {
+// Returns whether one lies outside [0, M).
+__device__ __forceinline__ bool slots_of(const SlotsArgs& a, size_t t, int k0, int (&slot)[kSlAhead],
+                                         float (&w)[kSlAhead]) {
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kSlAhead; ++i) {
@@ -32,12 +37,12 @@ __device__ __forceinline__ void slots_of(const SlotsArgs& a, size_t t, int k0, b
         if (s < 0 || s >= a.M) bad = true;
         else slot[i] = s;
     }
-    if (bad && report) latch(a.err, STRATA_EBADROUTE);
+    return bad;
 }
 
 // Block (bx, by): by tokens, bx threads along a row; grid.y pieces of a row.
 template <typename T, typename TO, int V>
-__global__ void __launch_bounds__(kSlRow) k_slots_combine(SlotsArgs a, bool wide_out) {
+__global__ void __launch_bounds__(kSlThreads) k_slots_combine(SlotsArgs a, bool wide_out) {
     pdl_launch();
     pdl_wait();
     const size_t t = size_t(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -48,7 +53,7 @@ __global__ void __launch_bounds__(kSlRow) k_slots_combine(SlotsArgs a, bool wide
     for (int k0 = 0; k0 < a.top_k; k0 += kSlAhead) {
         int slot[kSlAhead];
         float w[kSlAhead];
-        slots_of(a, t, k0, c == 0, slot, w);
+        const bool bad = slots_of(a, t, k0, slot, w);
         Raw<T, V> r[kSlAhead];
 #pragma unroll
         for (int i = 0; i < kSlAhead; ++i)
@@ -59,15 +64,17 @@ __global__ void __launch_bounds__(kSlRow) k_slots_combine(SlotsArgs a, bool wide
 #pragma unroll
                 for (int j = 0; j < V; ++j) sum[j] = fmaf(w[i], r[i].get(j), sum[j]);
             }
+        if (bad && c == 0) latch(a.err, STRATA_EBADROUTE);
     }
     st_row<TO, V>(static_cast<TO*>(a.out) + t * a.H + c, sum, wide_out);
 }
 
 // Block (bx, by) as above, but the threads of a token take its whole row: bx
-// up to 32 for several tokens a block, by = 1 above.  DW: dweights too.
+// up to 32 for several tokens a block, by = 1 above; grid.y pieces of their
+// slots.  DW: dweights too.
 template <typename T, int V, bool DW>
-__global__ void __launch_bounds__(kSlRow) k_slots_spread(SlotsArgs a) {
-    __shared__ float part[kSlRow / 32][kSlAhead];
+__global__ void __launch_bounds__(kSlThreads) k_slots_spread(SlotsArgs a) {
+    __shared__ float part[kSlThreads / 32][kSlAhead];
     pdl_launch();
     pdl_wait();
     const size_t t = size_t(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -75,12 +82,16 @@ __global__ void __launch_bounds__(kSlRow) k_slots_spread(SlotsArgs a) {
     const T* dout = static_cast<const T*>(a.dout) + (live ? t : 0) * a.H;
     const T* y = static_cast<const T*>(a.y);
     T* dy = static_cast<T*>(a.dy);
-    for (int k0 = 0; k0 < a.top_k; k0 += kSlAhead) {
+    const int first = int(threadIdx.x) * V;
+    // under way while the slots' numbers come
+    Raw<T, V> ahead{};
+    if (first < a.H) ahead = ld_row<T, V>(dout + first);
+    for (int k0 = int(blockIdx.y) * kSlAhead; k0 < a.top_k; k0 += int(gridDim.y) * kSlAhead) {
         int slot[kSlAhead];
         float w[kSlAhead], dot[kSlAhead] = {};
-        slots_of(a, live ? t : 0, k0, live && threadIdx.x == 0, slot, w);
-        for (int c = int(threadIdx.x) * V; live && c < a.H; c += int(blockDim.x) * V) {
-            const Raw<T, V> rd = ld_row<T, V>(dout + c);
+        const bool bad = slots_of(a, live ? t : 0, k0, slot, w);
+        for (int c = first; live && c < a.H; c += int(blockDim.x) * V) {
+            const Raw<T, V> rd = c == first ? ahead : ld_row<T, V>(dout + c);
             Raw<T, V> r[kSlAhead];
             if (DW) {
 #pragma unroll
@@ -115,6 +126,7 @@ __global__ void __launch_bounds__(kSlRow) k_slots_spread(SlotsArgs a) {
                 }
             }
         }
+        if (bad && live && threadIdx.x == 0) latch(a.err, STRATA_EBADROUTE);
         if (!DW) continue;
 #pragma unroll
         for (int i = 0; i < kSlAhead; ++i) dot[i] = group_sum(dot[i], min(32, int(blockDim.x)));
@@ -156,9 +168,11 @@ cudaError_t run_combine(const SlotsArgs& a, cudaStream_t s) {
 }
 template <typename T, int V>
 cudaError_t run_spread(const SlotsArgs& a, cudaStream_t s) {
-    const int units = (a.H + V - 1) / V, bx = threads_along(units, kSlRow);
+    const int units = (a.H + V - 1) / V, bx = threads_along(units, kSlThreads);
     const int by = bx <= 32 ? kSlThreads / bx : 1;
-    const dim3 grid((a.T + by - 1) / by);
+    // few tokens: their slots in pieces side by side (16 tokens of ten slots: 6.4 us in a row)
+    const int pieces = a.T <= device_info().sms * 2 ? (a.top_k + kSlAhead - 1) / kSlAhead : 1;
+    const dim3 grid((a.T + by - 1) / by, pieces);
     return a.dweights ? row_launch(k_slots_spread<T, V, true>, grid, dim3(bx, by), s, a)
                       : row_launch(k_slots_spread<T, V, false>, grid, dim3(bx, by), s, a);
 }
