@@ -6,9 +6,9 @@ namespace strata {
 namespace {
 
 template <typename T, typename TR, int W, int C, bool VEC>
-__global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a, bool wide) {
+__global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a) {
     using R = NormRow<W, C, VEC>;
-    __shared__ float buf[2][R::kGroups][W][1];
+    __shared__ NormSums<1> buf[2][R::kGroups][W];
     const R row;
     pdl_launch();
     pdl_wait();
@@ -20,9 +20,9 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a,
     Raw<TR, 8> rr[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        if (a.f) rf[c] = row.template load<true>(static_cast<const T*>(a.f) + at, c, H, false);
+        if (a.f) rf[c] = row.template load<true>(static_cast<const T*>(a.f) + at, c, H);
         // r' may take r's place
-        rr[c] = row.template load<false>(static_cast<const TR*>(a.resid) + at, c, H, wide);
+        rr[c] = row.template load<false>(static_cast<const TR*>(a.resid) + at, c, H);
     }
     const float g = a.beta * (a.gate ? __ldg(a.gate + t) : 1.0f);
     const float inv = 1.0f / float(H);
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a,
         for (int j = 0; j < 8; ++j) v[c][j] = a.alpha * rr[c].get(j);
         if (a.f) {
             Raw<float, 8> w{};
-            if (a.w_post) w = row.template load<true>(a.w_post, c, H, wide);
+            if (a.w_post) w = row.template load<true>(a.w_post, c, H);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float n = rf[c].get(j) * s0;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a,
             v[c][j] = to_f32(from_f32<TR>(v[c][j]));
             q[0] = fmaf(v[c][j], v[c][j], q[0]);
         }
-        if (a.resid_out) row.store(static_cast<TR*>(a.resid_out) + at, c, H, v[c], wide);
+        if (a.resid_out) row.store(static_cast<TR*>(a.resid_out) + at, c, H, v[c]);
     }
     if (a.x) {
         row.sum(q, &buf[1]);
@@ -66,11 +66,11 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a,
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             Raw<float, 8> w{};
-            if (a.w_pre) w = row.template load<true>(a.w_pre, c, H, wide);
+            if (a.w_pre) w = row.template load<true>(a.w_pre, c, H);
             float o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = a.w_pre ? v[c][j] * s1 * w.get(j) : v[c][j] * s1;
-            row.store(static_cast<T*>(a.x) + at, c, H, o, false);
+            row.store(static_cast<T*>(a.x) + at, c, H, o);
         }
     }
     if (a.rstd && row.id == 0) {
@@ -128,11 +128,7 @@ __global__ void __launch_bounds__(kNmThreads) k_norm_any(NormArgs a) {
 template <typename T, typename TR, int W, int C, bool VEC>
 cudaError_t run_rows(const NormArgs& a, cudaStream_t s) {
     using R = NormRow<W, C, VEC>;
-    const size_t pitch = size_t(a.H) * sizeof(TR);
-    const bool wide = aligned32(a.resid, pitch) && aligned32(a.resid_out, pitch) && aligned32(a.w_post, 0) &&
-                      aligned32(a.w_pre, size_t(a.H) * 4);
-    return row_launch(k_norm<T, TR, W, C, VEC>, dim3((a.T + R::kGroups - 1) / R::kGroups), dim3(R::kBlock), s, a,
-                      wide);
+    return row_launch(k_norm<T, TR, W, C, VEC>, dim3((a.T + R::kGroups - 1) / R::kGroups), dim3(R::kBlock), s, a);
 }
 
 template <typename T, typename TR, bool VEC>
@@ -149,7 +145,7 @@ cudaError_t run_norm(const NormArgs& a, cudaStream_t s) {
 }
 template <typename T, typename TR>
 cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
-    return a.H % 8 == 0 ? run_norm<T, TR, true>(a, s) : run_norm<T, TR, false>(a, s);
+    return a.H % 4 == 0 ? run_norm<T, TR, true>(a, s) : run_norm<T, TR, false>(a, s);
 }
 
 }  // namespace

@@ -12,15 +12,23 @@
 // pass did.
 //
 // Both are bound by memory: every tensor moves once.  W warps have a row in
-// their registers, 8 C columns a thread: 8 neighbouring ones where rows are
-// whole numbers of 8 columns (VEC), strided ones otherwise.  Longer rows take a
-// kernel that reads them once a pass.
+// their registers, 8 C columns a thread: fours of neighbouring ones where rows
+// are whole numbers of 4 columns (VEC), strided ones otherwise.  (Neighbouring
+// lanes have neighbouring fours, so that an access of a warp covers whole
+// sectors in fp32 and in 16 bits.)  Longer rows take a kernel that reads them
+// once a pass.
 #pragma once
 
 #include "grouped.h"
 #include "rows.cuh"
 
 namespace strata {
+
+// A warp's sums: one access.
+template <int N>
+struct __align__(N == 1 ? 4 : 16) NormSums {
+    float v[N == 1 ? 1 : (N + 3) / 4 * 4];
+};
 
 // A thread's place among the W warps of a row, and their sums.
 template <int W, int C, bool VEC>
@@ -30,14 +38,21 @@ struct NormRow {
     int group, id;                           // row of the block, thread of the row
     __device__ __forceinline__ NormRow() : group(int(threadIdx.x) / kThreads), id(int(threadIdx.x) % kThreads) {}
     __device__ __forceinline__ int column(int c, int j) const {
-        return VEC ? (c * kThreads + id) * 8 + j : (c * 8 + j) * kThreads + id;
+        return VEC ? ((2 * c + j / 4) * kThreads + id) * 4 + j % 4 : (c * 8 + j) * kThreads + id;
     }
     // Eight columns; zeros past the row's end.
     template <bool NC, typename T>
-    __device__ __forceinline__ Raw<T, 8> load(const T* row, int c, int H, bool wide) const {
+    __device__ __forceinline__ Raw<T, 8> load(const T* row, int c, int H) const {
         Raw<T, 8> r{};
         if constexpr (VEC) {
-            if (column(c, 0) < H) r = ld_row<T, 8, NC>(row + column(c, 0), wide);
+            constexpr int N = Raw<T, 4>::kWords;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (column(c, 4 * h) >= H) continue;
+                const Raw<T, 4> p = ld_row<T, 4, NC>(row + column(c, 4 * h));
+#pragma unroll
+                for (int i = 0; i < N; ++i) r.w[h * N + i] = p.w[i];
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -50,34 +65,39 @@ struct NormRow {
         return r;
     }
     template <typename T>
-    __device__ __forceinline__ void store(T* row, int c, int H, const float (&v)[8], bool wide) const {
+    __device__ __forceinline__ void store(T* row, int c, int H, const float (&v)[8]) const {
         if constexpr (VEC) {
-            if (column(c, 0) < H) st_row<T, 8>(row + column(c, 0), v, wide);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (column(c, 4 * h) < H)
+                    st_row<T, 4>(row + column(c, 4 * h), reinterpret_cast<const float(&)[4]>(v[4 * h]));
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (column(c, j) < H) row[column(c, j)] = from_f32<T>(v[j]);
         }
     }
-    // N sums over the row's threads, in all of them; buf is used by every other
-    // call (a thread past the barrier of the next has read this one's).
+    // N sums over the row's threads, in all of them; buf is used by
+    // every other call (a thread past the barrier of the next has read this one's).
     template <int N>
-    __device__ __forceinline__ void sum(float (&v)[N], float (*buf)[kGroups][W][N]) const {
+    __device__ __forceinline__ void sum(float (&v)[N], NormSums<N> (*buf)[kGroups][W]) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
         if constexpr (W > 1) {
             if ((id & 31) == 0) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) (*buf)[group][id >> 5][i] = v[i];
+                for (int i = 0; i < N; ++i) (*buf)[group][id >> 5].v[i] = v[i];
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kThreads) : "memory");
+            NormSums<N> s = (*buf)[group][0];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float s = 0.0f;
+            for (int k = 1; k < W; ++k) {
+                const NormSums<N> o = (*buf)[group][k];
 #pragma unroll
-                for (int k = 0; k < W; ++k) s += (*buf)[group][k][i];
-                v[i] = s;
+                for (int i = 0; i < N; ++i) s.v[i] += o.v[i];
             }
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = s.v[i];
         }
     }
 };

@@ -7,6 +7,7 @@
 // summed in the threads' registers over the rows of a CTA, set aside in shared
 // memory every kNbPiece rows (equal terms round one way within a binade), and
 // the CTAs' sums joined in their order by a second kernel.
+#include "grouped_tc.cuh"
 #include "norm.cuh"
 
 namespace strata {
@@ -15,128 +16,290 @@ namespace {
 
 constexpr int kNbPiece = 256;
 
-template <typename T, typename TR, int C>
-struct NormIn {                              // what a thread reads of a row
-    Raw<T, 8> dx[C], f[C];
-    Raw<TR, 8> v[C], dr2[C];
-    float s0, s1, g;
+// Two columns at once (packed fp32, each half rounded as alone).
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pk(v, v); }
+__device__ __forceinline__ float halves(uint64_t v) {
+    const float2 f = upk(v);
+    return f.x + f.y;
+}
+template <typename T>
+__device__ __forceinline__ uint64_t pair(const Raw<T, 8>& r, int i) { return pk(r.get(2 * i), r.get(2 * i + 1)); }
+
+template <typename T, typename TR>
+struct NormCols {                            // eight columns of a row
+    Raw<T, 8> dx, f;
+    Raw<TR, 8> v, dr2;
+};
+struct NormScalars {
+    float s0, s1, gate;
 };
 
-template <typename T, typename TR, int W, int C, bool VEC>
-__global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_norm_bwd(NormBwdArgs a, bool wide) {
+// Rows on their way (VEC): each thread copies its own columns of the next rows
+// to its own places in shared memory (fours of columns, no barrier), and reads
+// them there when their turn comes; what does not exist is filled with zeros.
+// kNbSteps steps of ROWS rows.
+constexpr int kNbSteps = 2;
+template <typename T, typename TR, int W, int C, int ROWS>
+struct NormRing {
+    static constexpr int kBlock = NormRow<W, C, true>::kBlock;
+    static constexpr uint32_t kT = uint32_t(kBlock) * 4 * sizeof(T), kTR = uint32_t(kBlock) * 4 * sizeof(TR);
+    static constexpr uint32_t kChunk = 4 * kT + 4 * kTR;     // dx, f; r', dr': twice four columns
+    static constexpr uint32_t kBytes = kNbSteps * ROWS * C * kChunk;
+    uint8_t* base;
+    // Piece k (0 dx, 1 f, 2 r', 3 dr') of chunk c, half h; slot: a row's place.
+    template <typename E>
+    __device__ __forceinline__ uint8_t* at(int slot, int c, int k, int h) const {
+        return base + (slot * C + c) * kChunk +
+               (k < 2 ? (2 * k + h) * kT : 4 * kT + (2 * (k - 2) + h) * kTR) + threadIdx.x * (4 * sizeof(E));
+    }
+    template <typename E>
+    __device__ __forceinline__ void copy(const E* src, size_t at_, bool live, int slot, int c, int k, int h) const {
+        const uint32_t dst = smem_u32(at<E>(slot, c, k, h)), bytes = live && src != nullptr ? 4 * sizeof(E) : 0;
+        if (bytes) src += at_;
+        if constexpr (sizeof(E) == 4)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    }
+    template <typename E>
+    __device__ __forceinline__ void take(Raw<E, 8>& r, int slot, int c, int k) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (sizeof(E) == 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(at<E>(slot, c, k, h));
+                r.w[4 * h] = v.x; r.w[4 * h + 1] = v.y; r.w[4 * h + 2] = v.z; r.w[4 * h + 3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(at<E>(slot, c, k, h));
+                r.w[2 * h] = v.x; r.w[2 * h + 1] = v.y;
+            }
+        }
+    }
+};
+
+// Where the weights' gradients are put aside: a block of one row at a time keeps
+// them in its own part of the workspace, others in shared memory.
+template <typename R, int C>
+constexpr uint32_t kNbAside = R::kGroups == 1 ? 0 : 16 * C * R::kBlock * sizeof(float);
+
+// ROWS rows a step share a barrier, and hide each other's latencies.
+template <typename T, typename TR, int W, int C, bool VEC, int ROWS>
+__global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_norm_bwd(NormBwdArgs a) {
     using R = NormRow<W, C, VEC>;
-    using In = NormIn<T, TR, C>;
-    constexpr bool AHEAD = C == 1;           // the next row's loads under way, the weights in registers
-    __shared__ float buf[2][R::kGroups][W][3];
-    extern __shared__ float aside[];         // [2 C][8][thread]
+    using Ring = NormRing<T, TR, W, C, ROWS>;
+    using Cols = NormCols<T, TR>;
+    constexpr bool KEEP = C == 1;            // the norms' weights in registers
+    __shared__ NormSums<3 * ROWS> buf[2][R::kGroups][W];
+    extern __shared__ __align__(16) uint8_t nb_dyn[];
+    [[maybe_unused]] float* aside = reinterpret_cast<float*>(nb_dyn);       // [2 C][8][thread]
+    const Ring ring{nb_dyn + kNbAside<R, C>};
     const R row;
     pdl_launch();
     pdl_wait();
     const int H = a.H;
     const float inv = 1.0f / float(H);
     const size_t step = size_t(gridDim.x) * R::kGroups;
-    auto read = [&](In& in, size_t t) {
-        if (t >= size_t(a.T)) return;
+    const T* pdx = static_cast<const T*>(a.dx);
+    const T* pf = static_cast<const T*>(a.f);
+    const TR* pv = a.dx ? static_cast<const TR*>(a.resid_out) : nullptr;
+    const TR* pr = static_cast<const TR*>(a.dresid_out);
+    // VEC: starts the copies of rows t, t + step ..
+    auto start = [&](size_t t, int at_step) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = row.column(c, 4 * h), slot = at_step * ROWS + r;
+                    const bool live = t + r * step < size_t(a.T) && col < H;
+                    const size_t at = (t + r * step) * H + col;
+                    ring.copy(pdx, at, live, slot, c, 0, h);
+                    ring.copy(pf, at, live, slot, c, 1, h);
+                    ring.copy(pv, at, live, slot, c, 2, h);
+                    ring.copy(pr, at, live, slot, c, 3, h);
+                }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto from_ring = [&](int slot, int c) {
+        Cols o;
+        ring.take(o.dx, slot, c, 0);
+        ring.take(o.f, slot, c, 1);
+        ring.take(o.v, slot, c, 2);
+        ring.take(o.dr2, slot, c, 3);
+        return o;
+    };
+    auto from_memory = [&](size_t t, int c) {
+        Cols o{};
+        if (t >= size_t(a.T)) return o;
         const size_t at = t * H;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (a.dx) {
-                in.dx[c] = row.template load<true>(static_cast<const T*>(a.dx) + at, c, H, false);
-                in.v[c] = row.template load<true>(static_cast<const TR*>(a.resid_out) + at, c, H, wide);
-            }
-            // dr may take its place
-            if (a.dresid_out) in.dr2[c] = row.template load<false>(static_cast<const TR*>(a.dresid_out) + at, c, H, wide);
-            if (a.f) in.f[c] = row.template load<true>(static_cast<const T*>(a.f) + at, c, H, false);
+        if (pdx) {
+            o.dx = row.template load<true>(pdx + at, c, H);
+            o.v = row.template load<true>(pv + at, c, H);
         }
-        in.s0 = __ldg(a.rstd + 2 * t);
-        in.s1 = __ldg(a.rstd + 2 * t + 1);
-        in.g = a.beta * (a.gate ? __ldg(a.gate + t) : 1.0f);
+        if (pr) o.dr2 = row.template load<false>(pr + at, c, H);             // dr may take its place
+        if (pf) o.f = row.template load<true>(pf + at, c, H);
+        return o;
     };
-    auto weight = [&](const float* w, int c, float (&o)[8]) {
+    auto weight = [&](const float* w, int c, uint64_t (&o)[4]) {
         Raw<float, 8> r{};
-        if (w) r = row.template load<true>(w, c, H, wide);
+        if (w) r = row.template load<true>(w, c, H);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = w ? r.get(j) : 1.0f;
+        for (int i = 0; i < 4; ++i) o[i] = w ? pair(r, i) : both(1.0f);
     };
-    float w_pre[8], w_post[8];
-    if (AHEAD) {
+    uint64_t w_pre[4], w_post[4];
+    if (KEEP) {
         weight(a.w_pre, 0, w_pre);
         weight(a.w_post, 0, w_post);
     }
-    float d_pre[C][8] = {}, d_post[C][8] = {};
+    uint64_t d_pre[C][4] = {}, d_post[C][4] = {};
     int rows = 0;
     bool set = false;
+    float* out = a.parts + size_t(blockIdx.x) * 2 * H;
     auto put_aside = [&]() {
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float* p = aside + (2 * c * 8 + j) * R::kBlock + threadIdx.x;
-                float* q = p + 8 * R::kBlock;
-                *p = set ? *p + d_pre[c][j] : d_pre[c][j];
-                *q = set ? *q + d_post[c][j] : d_post[c][j];
-                d_pre[c][j] = d_post[c][j] = 0.0f;
+            for (int k = 0; k < 2; ++k) {
+                uint64_t(&d)[4] = k == 0 ? d_pre[c] : d_post[c];
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = upk(d[i]);
+                    o[2 * i] = v.x;
+                    o[2 * i + 1] = v.y;
+                    d[i] = 0;
+                }
+                if constexpr (R::kGroups == 1) {
+                    if (k == 0 ? a.dw_pre == nullptr : a.dw_post == nullptr) continue;
+                    if (set) {
+                        const Raw<float, 8> had = row.template load<false>(out + k * H, c, H);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] += had.get(j);
+                    }
+                    row.store(out + k * H, c, H, o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float* p = aside + ((2 * c + k) * 8 + j) * R::kBlock + threadIdx.x;
+                        *p = set ? *p + o[j] : o[j];
+                    }
+                }
             }
         set = true;
     };
-    In in{};
+    // read whether there is such a row, a gate, or not, so that nothing waits
+    // for the values before their row's turn
+    const float* pgate = a.gate ? a.gate : a.rstd;
+    auto scalars = [&](size_t t) {
+        t = min(t, size_t(a.T) - 1);
+        return NormScalars{__ldg(a.rstd + 2 * t), __ldg(a.rstd + 2 * t + 1), __ldg(pgate + t)};
+    };
     size_t t = size_t(blockIdx.x) * R::kGroups + row.group;
-    read(in, t);
-    for (int n = 0; t < size_t(a.T); t += step, n ^= 1) {
-        In next{};
-        if (AHEAD) read(next, t + step);
-        const size_t at = t * H;
-        float q[3] = {};
-        float c1 = 0.0f, c0 = 0.0f;
+    NormScalars ahead[ROWS];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (!AHEAD) {
-                weight(a.w_pre, c, w_pre);
-                weight(a.w_post, c, w_post);
-            }
+    for (int r = 0; r < ROWS; ++r) ahead[r] = scalars(t + r * step);
+    Cols next[C];                            // not VEC: the next row in registers
+    if constexpr (VEC) {
+        start(t, 0);
+    } else {
+        static_assert(ROWS == 1, "one row a step");
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float gx = in.dx[c].get(j) * w_pre[j], v = in.v[c].get(j);
-                const float wf = w_post[j] * in.f[c].get(j);
-                q[0] = fmaf(gx, v, q[0]);
-                q[1] = fmaf(fmaf(in.s1, gx, in.dr2[c].get(j)), wf, q[1]);
-                q[2] = fmaf(v, wf, q[2]);
+        for (int c = 0; c < C; ++c) next[c] = from_memory(t, c);
+    }
+    for (int n = 0; t < size_t(a.T); t += ROWS * step, n ^= 1) {
+        Cols cur[C];
+        if constexpr (VEC) {
+            start(t + ROWS * step, n ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                cur[c] = next[c];
+                next[c] = from_memory(t + step, c);
             }
+        }
+        float s0[ROWS], s1[ROWS], g[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const bool live = t + r * step < size_t(a.T);
+            s0[r] = live ? ahead[r].s0 : 0.0f;
+            s1[r] = live ? ahead[r].s1 : 0.0f;
+            g[r] = !live ? 0.0f : a.gate ? a.beta * ahead[r].gate : a.beta;
+            ahead[r] = scalars(t + (ROWS + r) * step);
+        }
+        // dr' + s1 dx wpre, kept for the second pass
+        uint64_t part[ROWS][C][4];
+        float q[3 * ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            uint64_t q0 = 0, q1 = 0, q2 = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (!KEEP) {
+                    weight(a.w_pre, c, w_pre);
+                    weight(a.w_post, c, w_post);
+                }
+                const Cols in = VEC ? from_ring(n * ROWS + r, c) : cur[c];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t gx = mul2(pair(in.dx, i), w_pre[i]), v = pair(in.v, i);
+                    const uint64_t wf = mul2(w_post[i], pair(in.f, i));
+                    part[r][c][i] = ffma2(both(s1[r]), gx, pair(in.dr2, i));
+                    q0 = ffma2(gx, v, q0);
+                    q1 = ffma2(part[r][c][i], wf, q1);
+                    q2 = ffma2(v, wf, q2);
+                }
+            }
+            q[3 * r] = halves(q0);
+            q[3 * r + 1] = halves(q1);
+            q[3 * r + 2] = halves(q2);
         }
         row.sum(q, &buf[n]);
-        c1 = in.s1 * in.s1 * in.s1 * (q[0] * inv);
-        const float df = q[1] - c1 * q[2];
-        if (a.dgate && row.id == 0) a.dgate[t] = a.beta * in.s0 * df;
-        if (a.post) c0 = in.g * in.s0 * in.s0 * in.s0 * (df * inv);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (!AHEAD) {
-                weight(a.w_pre, c, w_pre);
-                weight(a.w_post, c, w_post);
-            }
-            float o[8], r[8];
+        for (int r = 0; r < ROWS; ++r) {
+            const size_t tr = t + r * step, at = tr * H;
+            if (tr >= size_t(a.T)) break;
+            const float c1 = s1[r] * s1[r] * s1[r] * (q[3 * r] * inv);
+            const float dn_f = q[3 * r + 1] - c1 * q[3 * r + 2];             // sum of D wpost f
+            if (a.dgate && row.id == 0) a.dgate[tr] = a.beta * s0[r] * dn_f;
+            const float c0 = a.post ? g[r] * s0[r] * s0[r] * s0[r] * (dn_f * inv) : 0.0f;
+            const uint64_t nc1 = both(-c1), nc0 = both(-c0), gs = both(g[r] * s0[r]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float dx = in.dx[c].get(j), v = in.v[c].get(j), f = in.f[c].get(j);
-                const float d = in.dr2[c].get(j) + fmaf(in.s1, dx * w_pre[j], -c1 * v);
-                const float dn = in.g * d;
-                d_pre[c][j] = fmaf(dx * v, in.s1, d_pre[c][j]);
-                d_post[c][j] = fmaf(dn * f, in.s0, d_post[c][j]);
-                o[j] = a.post ? fmaf(in.s0, dn * w_post[j], -c0 * f) : dn;
-                r[j] = a.alpha * d;
+            for (int c = 0; c < C; ++c) {
+                if (!KEEP) weight(a.w_post, c, w_post);
+                const Cols in = VEC ? from_ring(n * ROWS + r, c) : cur[c];
+                float o[8], p[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t v = pair(in.v, i), f = pair(in.f, i);
+                    const uint64_t d = ffma2(nc1, v, part[r][c][i]);
+                    d_pre[c][i] = ffma2(both(s1[r]), mul2(pair(in.dx, i), v), d_pre[c][i]);
+                    d_post[c][i] = ffma2(gs, mul2(d, f), d_post[c][i]);
+                    const uint64_t dn = mul2(gs, a.post ? mul2(d, w_post[i]) : d);
+                    const float2 x = upk(a.post ? ffma2(nc0, f, dn) : dn);
+                    const float2 y = upk(mul2(both(a.alpha), d));
+                    o[2 * i] = x.x;
+                    o[2 * i + 1] = x.y;
+                    p[2 * i] = y.x;
+                    p[2 * i + 1] = y.y;
+                }
+                if (a.df) row.store(static_cast<T*>(a.df) + at, c, H, o);
+                if (a.dresid) row.store(static_cast<TR*>(a.dresid) + at, c, H, p);
             }
-            if (a.df) row.store(static_cast<T*>(a.df) + at, c, H, o, false);
-            if (a.dresid) row.store(static_cast<TR*>(a.dresid) + at, c, H, r, wide);
         }
-        if (++rows % kNbPiece == 0) put_aside();
-        if (AHEAD) in = next;
-        else read(in, t + step);
+        if (++rows % (kNbPiece / ROWS) == 0) put_aside();
     }
+    if (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
     if (!a.dw_pre && !a.dw_post) return;
     put_aside();
+    if constexpr (R::kGroups == 1) return;
     __syncthreads();
     // the groups of the block in their order
-    float* part = a.parts + size_t(blockIdx.x) * 2 * H;
     if (row.group == 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -146,11 +309,10 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     o[j] = 0.0f;
-                    for (int g = 0; g < R::kGroups; ++g)
-                        o[j] += aside[((2 * c + k) * 8 + j) * R::kBlock + g * R::kThreads + row.id];
+                    for (int i = 0; i < R::kGroups; ++i)
+                        o[j] += aside[((2 * c + k) * 8 + j) * R::kBlock + i * R::kThreads + row.id];
                 }
-                if (k == 0 ? a.dw_pre != nullptr : a.dw_post != nullptr)
-                    row.store(part + k * H, c, H, o, false);
+                if (k == 0 ? a.dw_pre != nullptr : a.dw_post != nullptr) row.store(out + k * H, c, H, o);
             }
     }
 }
@@ -256,25 +418,14 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRows) k_norm_join(const float
 
 template <typename T, typename TR, int W, int C, bool VEC>
 cudaError_t run_rows(const NormBwdArgs& a, int* n, cudaStream_t s) {
+    constexpr int ROWS = VEC && C == 1 && W > 1 ? 2 : 1;
     using R = NormRow<W, C, VEC>;
     const int want = (a.T + R::kGroups - 1) / R::kGroups, most = device_info().sms * (W <= 8 ? 2 : 1);
     *n = want < most ? want : most;
     if (*n > kNormParts) *n = kNormParts;
     if (*n == 0) return cudaSuccess;
-    const size_t pitch = size_t(a.H) * sizeof(TR);
-    const bool wide = aligned32(a.resid_out, pitch) && aligned32(a.dresid_out, pitch) && aligned32(a.dresid, pitch) &&
-                      aligned32(a.w_post, 0) && aligned32(a.w_pre, size_t(a.H) * 4);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(*n);
-    cfg.blockDim = dim3(R::kBlock);
-    cfg.dynamicSmemBytes = size_t(16) * C * R::kBlock * sizeof(float);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_norm_bwd<T, TR, W, C, VEC>, a, wide);
+    const size_t dyn = kNbAside<R, C> + (VEC ? NormRing<T, TR, W, C, ROWS>::kBytes : 0);
+    return gt_launch<k_norm_bwd<T, TR, W, C, VEC, ROWS>>(R::kBlock, 1, *n, dyn, s, a);
 }
 template <typename T, typename TR, bool VEC>
 cudaError_t run_norm_bwd(const NormBwdArgs& a, int* n, cudaStream_t s) {
@@ -283,13 +434,15 @@ cudaError_t run_norm_bwd(const NormBwdArgs& a, int* n, cudaStream_t s) {
     if (a.H <= 1024) return run_rows<T, TR, 4, 1, VEC>(a, n, s);
     if (a.H <= 2048) return run_rows<T, TR, 8, 1, VEC>(a, n, s);
     if (a.H <= 4096) return run_rows<T, TR, 16, 1, VEC>(a, n, s);
+    if constexpr (VEC)
+        if (a.H <= 8192) return run_rows<T, TR, 16, 2, VEC>(a, n, s);
     const int want = (a.T + kNmRows - 1) / kNmRows;
     *n = want < kNormParts ? want : kNormParts;
     return *n == 0 ? cudaSuccess : row_launch(k_norm_bwd_any<T, TR>, dim3(*n), dim3(kNmThreads), s, a);
 }
 template <typename T, typename TR>
 cudaError_t pick_norm_bwd(const NormBwdArgs& a, int* n, cudaStream_t s) {
-    return a.H % 8 == 0 ? run_norm_bwd<T, TR, true>(a, n, s) : run_norm_bwd<T, TR, false>(a, n, s);
+    return a.H % 4 == 0 ? run_norm_bwd<T, TR, true>(a, n, s) : run_norm_bwd<T, TR, false>(a, n, s);
 }
 
 }  // namespace
