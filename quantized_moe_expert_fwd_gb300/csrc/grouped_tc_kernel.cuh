@@ -150,12 +150,17 @@ __device__ __forceinline__ void gt_part(float* p, const float* v) {
 }
 
 // What becomes of the sums: the output as it is (GtPlain), or an epilogue EPI
-// (16-bit outputs of forward and dx) that takes 32 columns of a warp's 32 rows,
-//   piece(first row, rows, first column, columns, values, the warp's staging),
+// (16-bit outputs of forward and dx).  It takes kStep columns of a warp's 32
+// rows at a time,
+//   take(read ahead, first row, rows, first column, end, values, the warp's
+//        staging),
 // or, where a reduction was split, four columns of a row a lane,
 //   quad(row, first column, values, whether they exist),
-// and may look at a tile's place before its sums are there,
-//   ahead(row, whether it exists, first column, columns).
+// and reads ahead of a tile's sums (its type Ahead),
+//   ahead(row, whether it exists, first column, end).
+// Its steps are a loop that is not unrolled, over sums in tensor memory (where
+// pieces were added they go back there first): unrolled, the code of SwiGLU's
+// gradient left the instruction cache (2048-token prompt 201 us).
 struct GtPlain {};
 
 template <int MODE, int BN, int OUT, int CL, typename EPI = GtPlain>
@@ -431,14 +436,6 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             const int c0 = i.c0 + half * (BN / 2);
             const size_t at = (i.orow + r - lane) * size_t(cols) + c0;
             const int live = min(32, i.rows - (r - lane));       // of the warp's rows
-            if constexpr (!PLAIN && !SPLIT) epi.template ahead<CH>(i.orow + r, lane < live, c0);
-            auto out = [&](int c, const float* f) {
-                if constexpr (PLAIN)
-                    gt_store<F32, 32>(a.out, at + c * 32, cols, live, f, cols - c0 - c * 32, a.vec,
-                                      a.bf16, store);
-                else
-                    epi.piece(i.orow + r - lane, live, c0 + c * 32, f, store);
-            };
             auto taken = [&](uint32_t buf) {             // the accumulator is free again
                 tc_fence_before();
                 __syncwarp();
@@ -447,6 +444,52 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     else mbar_arrive(&acc_empty[buf]);
                 }
             };
+            if constexpr (!PLAIN && !SPLIT) {
+                const int last = min(cols, c0 + BN / 2);
+                auto read = epi.ahead(i.orow + r, lane < live, c0, last);
+                uint32_t buf = acc & 1u;
+                gt_wait(&acc_full[buf], (acc >> 1) & 1, waits, 55, buf);
+                tc_fence_after();
+                if (PIECES && i.k1 - i.k0 > PIECE) {
+                    float sum[CH][32];
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
+                    for (int ks = i.k0;; ks += PIECE) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            uint32_t v[32];
+                            tmem_ld32(tl + buf * BN + c * 32, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[c][j] += __uint_as_float(v[j]);
+                        }
+                        if (ks + PIECE >= i.k1) break;
+                        taken(buf);
+                        ++acc;
+                        buf = acc & 1u;
+                        gt_wait(&acc_full[buf], (acc >> 1) & 1, waits, 55, buf);
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        tmem_st32(tl + buf * BN + c * 32, reinterpret_cast<const uint32_t(&)[32]>(sum[c]));
+                    tmem_st_wait();
+                }
+#pragma unroll 1
+                for (int c = 0; c < BN / 2; c += EPI::kStep) {
+                    uint32_t v[EPI::kStep];
+                    if constexpr (EPI::kStep == 32) tmem_ld32(tl + buf * BN + c, v);
+                    else tmem_ld16(tl + buf * BN + c, v);
+                    tmem_ld_wait();
+                    epi.take(read, i.orow + r - lane, live, c0 + c, last, reinterpret_cast<const float*>(v),
+                             store);
+                }
+                taken(buf);
+                ++acc;
+                continue;
+            }
             // Stored as it is read: a reduction of one piece, and dw's tiles of one
             // (8 experts of 4096 x 4096, 400 rows each: 109 us, by way of the sums
             // 112).  A pair's go through the sums, so that the accumulator is free
@@ -478,7 +521,9 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     const float* f = reinterpret_cast<const float*>(v);
                     if (DW1) pack(c, f);
                     else if (SPLIT) gt_part(part + c * 32, f);
-                    else out(c, f);
+                    else if constexpr (PLAIN)
+                        gt_store<false, 32>(a.out, at + c * 32, cols, live, f, cols - c0 - c * 32,
+                                            a.vec, a.bf16, store);
                 }
                 if (i.k1 > i.k0) {
                     taken(buf);
@@ -510,7 +555,9 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                         put(i, c0 + c * 32, reinterpret_cast<const uint32_t(&)[32]>(sum[c]));
                     else if (MODE == kGmmDw) pack(c, sum[c]);
                     else if (SPLIT) gt_part(part + c * 32, sum[c]);
-                    else out(c, sum[c]);
+                    else if constexpr (PLAIN)
+                        gt_store<F32, 32>(a.out, at + c * 32, cols, live, sum[c], cols - c0 - c * 32,
+                                          a.vec, a.bf16, store);
                 }
             }
         }

@@ -1,6 +1,7 @@
 // swiglu.cu -- the gated feed-forward block over grouped rows: gate and up
 // products with SwiGLU, and the down product's input gradient with SwiGLU's
 // gradient, each one kernel.
+#include "grouped_few.cuh"
 #include "grouped_simt.cuh"
 #include "swiglu.cuh"
 
@@ -12,6 +13,22 @@ struct KeepQuad {
     SwigluKeep k;
     __device__ __forceinline__ void operator()(size_t row, int c, const float* v, bool live) const {
         swiglu_quad(k, row, c, v, live);
+    }
+};
+// Few rows: a warp has the sums of two pairs.
+struct KeepFew {
+    SwigluKeep k;
+    __device__ __forceinline__ void operator()(size_t row, int n0, const float (&s)[kFewRows]) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < kFewRows; i += 2) {
+            if (n0 + i >= 2 * k.I || lane != i) continue;
+            store_u16(k.h, row * k.I + (n0 + i) / 2, pack16(swiglu(s[i], s[i + 1]), 0.0f, k.bf16));
+            if (k.p == nullptr) continue;
+            const uint32_t w = pack16(s[i], s[i + 1], k.bf16);
+            store_u16(k.p, row * 2 * k.I + n0 + i, w);
+            store_u16(k.p, row * 2 * k.I + n0 + i + 1, w >> 16);
+        }
     }
 };
 struct BackQuad {
@@ -43,6 +60,9 @@ cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t s) {
     g.E = a.E;
     g.dtype = a.dtype;
     const SwigluKeep k{a.h, a.p, a.scales, a.I, a.dtype == STRATA_BF16};
+    // (8-bit blocks span the columns of several warps of the few-row kernel)
+    if (g.M <= kFewRowsMax && g.K % 8 == 0 && a.scales == nullptr)
+        return k.bf16 ? run_few<true>(g, KeepFew{k}, s) : run_few<false>(g, KeepFew{k}, s);
     if (grouped_tc_takes(kGmmFwd, g)) return launch_swiglu_tc(g, k, s);
     return swiglu_simt<kGmmFwd>(g, KeepQuad{k}, s);
 }
