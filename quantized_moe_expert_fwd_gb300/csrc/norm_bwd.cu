@@ -16,12 +16,7 @@ namespace {
 
 constexpr int kNbPiece = 256;
 
-// Two columns at once (packed fp32, each half rounded as alone).
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
+// Two columns at once (packed fp32).
 __device__ __forceinline__ uint64_t both(float v) { return pk(v, v); }
 __device__ __forceinline__ float halves(uint64_t v) {
     const float2 f = upk(v);

@@ -3,10 +3,17 @@
 
 namespace strata {
 
-cudaError_t launch_swiglu_back_tc(const GmmArgs& g, const SwigluBack& k, cudaStream_t s) {
-    const SwigluBackPiece epi{k, gt_vec(k.p, size_t(2) * k.I * (k.scales ? 1 : 2)),
-                              gt_vec(k.dp, size_t(4) * k.I), k.h ? gt_vec(k.h, size_t(k.I) * 2) : 0};
+namespace {
+template <bool BF16>
+cudaError_t run(const GmmArgs& g, const SwigluBack& k, cudaStream_t s) {
+    const SwigluBackPiece<BF16> epi{k, gt_vec(k.p, size_t(2) * k.I * (k.scales ? 1 : 2)),
+                                    gt_vec(k.dp, size_t(4) * k.I), k.h ? gt_vec(k.h, size_t(k.I) * 2) : 0};
     return gt_pick<kGmmDx>(g, epi, s);
+}
+}  // namespace
+
+cudaError_t launch_swiglu_back_tc(const GmmArgs& g, const SwigluBack& k, cudaStream_t s) {
+    return k.bf16 ? run<true>(g, k, s) : run<false>(g, k, s);
 }
 
 }  // namespace strata

@@ -49,6 +49,8 @@ __device__ __forceinline__ void put_rows(void* out, size_t at, size_t pitch, int
     gt_store_staged<WORDS>(reinterpret_cast<uint8_t*>(p), pitch * 2, rows, stage, nv * 2);
 }
 
+// BF16: the operands' type, or fp16.
+template <bool BF16>
 struct SwigluPiece {
     SwigluKeep k;
     int vec_h, vec_p;                        // bytes that every row is aligned to: 32, 16, 0
@@ -62,7 +64,7 @@ struct SwigluPiece {
         const int cols = 2 * k.I, nv = cols - c, lane = threadIdx.x & 31;
         if (rows <= 0 || nv <= 0) return;
         if (k.p != nullptr && k.scales == nullptr)
-            gt_store<false, 32>(k.p, row0 * cols + c, cols, rows, v, nv, vec_p, k.bf16, stage);
+            gt_store<false, 32>(k.p, row0 * cols + c, cols, rows, v, nv, vec_p, BF16, stage);
         if (k.scales != nullptr && lane < rows) {            // whole blocks
             uint32_t m = 0;
 #pragma unroll
@@ -76,15 +78,18 @@ struct SwigluPiece {
             put32(static_cast<uint8_t*>(k.p) + (row0 + lane) * cols + c, vec_p == 32, w);
             k.scales[(row0 + lane) * (cols / kAct8Block) + c / kAct8Block] = uint8_t(b);
         }
-        // rows that do not exist may hold anything: the slow paths of their
-        // quotients are not taken
         float h[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) h[j] = lane < rows ? swiglu(v[2 * j], v[2 * j + 1]) : 0.0f;
-        gt_store<false, 16>(k.h, row0 * k.I + c / 2, k.I, rows, h, nv / 2, vec_h, k.bf16, stage);
+        for (int j = 0; j < 16; j += 2) {
+            const float2 o = swiglu2(v[2 * j], v[2 * j + 1], v[2 * j + 2], v[2 * j + 3]);
+            h[j] = o.x;
+            h[j + 1] = o.y;
+        }
+        gt_store<false, 16>(k.h, row0 * k.I + c / 2, k.I, rows, h, nv / 2, vec_h, BF16, stage);
     }
 };
 
+template <bool BF16>
 struct SwigluBackPiece {
     SwigluBack k;
     int vec_p, vec_dp, vec_h;
@@ -127,29 +132,32 @@ struct SwigluBackPiece {
         if (rows <= 0 || nv <= 0) return;
         const Ahead now = a;
         if (c + 16 < end) read(a, row0 + lane, lane < rows, c + 16);
+        float g[16], u[16];
+        if (k.scales != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                float q[4];
+                act8_values(now.lo[j / 2], now.scale, q);
+                g[j] = q[0];
+                u[j] = q[1];
+                g[j + 1] = q[2];
+                u[j + 1] = q[3];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t w = j < 8 ? now.lo[j & 7] : now.hi[j & 7];
+                g[j] = unpack16(w & 0xffffu, BF16);
+                u[j] = BF16 ? bf16_hi(w) : unpack16(w >> 16, BF16);
+            }
+        }
         uint32_t d[16], h[8];
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-            float g[2], u[2];
-            if (k.scales != nullptr) {
-                float q[4];
-                act8_values(now.lo[j / 2], now.scale, q);
-                g[0] = q[0]; u[0] = q[1]; g[1] = q[2]; u[1] = q[3];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t w = j < 8 ? now.lo[(j + i) & 7] : now.hi[(j + i) & 7];
-                    g[i] = unpack16(w & 0xffffu, k.bf16);
-                    u[i] = unpack16(w >> 16, k.bf16);
-                }
-            }
-            SwigluGrads o[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                o[i] = swiglu_grads(g[i], u[i], v[j + i]);
-                d[j + i] = pack16(o[i].dg, o[i].du, k.bf16);
-            }
-            h[j / 2] = pack16(o[0].h, o[1].h, k.bf16);
+            const SwigluGrads2 o = swiglu_grads2(g + j, u + j, v + j);
+            d[j] = pack16(o.dg.x, o.du.x, BF16);
+            d[j + 1] = pack16(o.dg.y, o.du.y, BF16);
+            h[j / 2] = pack16(o.h.x, o.h.y, BF16);
         }
         put_rows<16>(k.dp, row0 * 2 * k.I + 2 * c, size_t(2) * k.I, rows, d, 2 * nv, vec_dp, stage);
         if (k.h != nullptr) put_rows<8>(k.h, row0 * k.I + c, k.I, rows, h, nv, vec_h, stage);
