@@ -65,13 +65,13 @@ constexpr int kGtPair = 1, kGtSplit = 2;        // what the CTAs of a cluster sh
 // A kernel's geometry.  CL = kGtPair: two CTAs make one tile of 256 rows by
 // BN columns; each loads its 128 rows and half of the columns.  CL =
 // kGtSplit: the CTAs of a cluster take a part of one tile's reduction each.
-template <int MODE, int BN, int CL>
+template <int MODE, int BN, int CL, uint32_t STAGING = kGtStoreBytes>
 struct Gt {
     static constexpr bool PAIR = CL == kGtPair;
     static constexpr int kCols = PAIR ? BN / 2 : BN;             // B columns a CTA loads
     static constexpr uint32_t kBBytes = uint32_t(kCols) * 128u;
     static constexpr uint32_t kStage = kGtABytes + kBBytes;
-    static constexpr uint32_t kStagingBytes = MODE == kGmmDw ? kGtEpiWarps * kGtPiece : kGtStoreBytes;
+    static constexpr uint32_t kStagingBytes = MODE == kGmmDw ? kGtEpiWarps * kGtPiece : STAGING;
     static constexpr int kStages = int((214016u - kStagingBytes) / kStage);
     static constexpr size_t kDyn = size_t(kStages) * kStage + kStagingBytes + 1024;
     static constexpr int kBlock = PAIR ? 2 * kGtRows : kGtRows;  // rows of a tile
@@ -156,18 +156,21 @@ __device__ __forceinline__ void gt_part(float* p, const float* v) {
 //        staging),
 // or, where a reduction was split, four columns of a row a lane,
 //   quad(row, first column, values, whether they exist),
-// and reads ahead of a tile's sums (its type Ahead),
-//   ahead(row, whether it exists, first column, end).
+// and reads ahead of a tile's sums,
+//   ahead(first row, rows, first column, end, the warp's staging),
+// which has kWarpStaging bytes.
 // Its steps are a loop that is not unrolled, over sums in tensor memory (where
 // pieces were added they go back there first): unrolled, the code of SwiGLU's
 // gradient left the instruction cache (2048-token prompt 201 us).
-struct GtPlain {};
+struct GtPlain {
+    static constexpr uint32_t kWarpStaging = kGtStoreWords * 4;
+};
 
 template <int MODE, int BN, int OUT, int CL, typename EPI = GtPlain>
 __global__ void __launch_bounds__(kGtThreads, 1)
     k_gmm_tc(const __grid_constant__ GtMaps maps, GtArgs a, EPI epi) {
     constexpr bool PLAIN = std::is_same<EPI, GtPlain>::value;
-    using G = Gt<MODE, BN, CL>;
+    using G = Gt<MODE, BN, CL, kGtEpiWarps * EPI::kWarpStaging>;
     constexpr bool PAIR = CL == kGtPair, SPLIT = CL == kGtSplit;
     constexpr int STAGES = G::kStages;
     constexpr bool F32 = OUT == kGt32, PIECES = OUT != kGt16;
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
         const uint32_t tl = tmem + (uint32_t((wid & 3) * 32) << 16) + uint32_t(half * (BN / 2));
         uint8_t* stage = base + STAGES * STAGE + wid * kGtPiece;            // dw
         uint32_t* store =                                                   // forward, dx
-            reinterpret_cast<uint32_t*>(base + STAGES * STAGE) + wid * kGtStoreWords;
+            reinterpret_cast<uint32_t*>(base + STAGES * STAGE + wid * EPI::kWarpStaging);
         // split: this CTA's partial sums, in the stages (all consumed by then)
         float* part = reinterpret_cast<float*>(base) + r * kGtPartPitch + half * (BN / 2);
         uint32_t acc = 0;
@@ -446,7 +449,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
             };
             if constexpr (!PLAIN && !SPLIT) {
                 const int last = min(cols, c0 + BN / 2);
-                auto read = epi.ahead(i.orow + r, lane < live, c0, last);
+                auto read = epi.ahead(i.orow + r - lane, live, c0, last, store);
                 uint32_t buf = acc & 1u;
                 gt_wait(&acc_full[buf], (acc >> 1) & 1, waits, 55, buf);
                 tc_fence_after();
@@ -628,6 +631,7 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 // ------------------------------------------------------------------- host
 template <int MODE, int BN, int OUT, int CL, typename EPI>
 cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, const EPI& epi, cudaStream_t s) {
+    using G = Gt<MODE, BN, CL, kGtEpiWarps * EPI::kWarpStaging>;
     constexpr bool F32 = OUT == kGt32;
     GtMaps m;
     bool ok = true;
@@ -642,7 +646,7 @@ cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, const EPI& epi, cuda
     } else {
         const int red = MODE == kGmmFwd ? g.K : g.N;
         ok = gt_map16(&m.a.part, g.a, red, rows, 0, kGtBox) &&
-             gt_map16(&m.a.whole, g.a, red, rows, 0, kGtRows) && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? Gt<MODE, BN, CL>::kCols : 64);
+             gt_map16(&m.a.whole, g.a, red, rows, 0, kGtRows) && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? G::kCols : 64);
         m.out = m.b;
     }
     if (!ok) return cudaErrorInvalidValue;
@@ -657,8 +661,7 @@ cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, const EPI& epi, cuda
     a.bf16 = g.dtype == STRATA_BF16;
     const size_t pitch = size_t(MODE == kGmmFwd ? g.N : g.K) * (F32 ? 4 : 2);
     a.vec = gt_vec(g.out, pitch);
-    return gt_launch<k_gmm_tc<MODE, BN, OUT, CL, EPI>>(kGtThreads, cluster, grid,
-                                                       Gt<MODE, BN, CL>::kDyn, s, m, a, epi);
+    return gt_launch<k_gmm_tc<MODE, BN, OUT, CL, EPI>>(kGtThreads, cluster, grid, G::kDyn, s, m, a, epi);
 }
 
 template <int MODE, int BN, int CL, typename EPI>

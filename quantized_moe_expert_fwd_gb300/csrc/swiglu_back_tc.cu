@@ -6,8 +6,7 @@ namespace strata {
 namespace {
 template <bool BF16>
 cudaError_t run(const GmmArgs& g, const SwigluBack& k, cudaStream_t s) {
-    const SwigluBackPiece<BF16> epi{k, gt_vec(k.p, size_t(2) * k.I * (k.scales ? 1 : 2)),
-                                    gt_vec(k.dp, size_t(4) * k.I), k.h ? gt_vec(k.h, size_t(k.I) * 2) : 0};
+    const SwigluBackPiece<BF16> epi{k};
     return gt_pick<kGmmDx>(g, epi, s);
 }
 }  // namespace

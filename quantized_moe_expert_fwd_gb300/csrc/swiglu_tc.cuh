@@ -17,45 +17,14 @@ __device__ __forceinline__ void put32(uint8_t* p, bool wide, const uint32_t (&w)
         reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
-__device__ __forceinline__ void get32(const uint8_t* p, bool wide, uint32_t (&w)[8]) {
-    if (wide) {
-        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                       "=r"(w[6]), "=r"(w[7])
-                     : "l"(p));
-    } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    }
-}
-
-// gt_store of values that are packed already: 2 WORDS columns (nv of them
-// exist, a multiple of 8) of a warp's rows.
-template <int WORDS>
-__device__ __forceinline__ void put_rows(void* out, size_t at, size_t pitch, int rows, const uint32_t (&w)[WORDS],
-                                         int nv, int vec, uint32_t* stage) {
-    const int lane = threadIdx.x & 31;
-    uint16_t* p = static_cast<uint16_t*>(out) + at;
-    if (vec == 32) {
-        if (lane < rows) gt_store_words(reinterpret_cast<uint8_t*>(p + lane * pitch), w, nv * 2);
-        return;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < WORDS; ++j) stage[lane * 17 + j] = w[j];
-    __syncwarp();
-    gt_store_staged<WORDS>(reinterpret_cast<uint8_t*>(p), pitch * 2, rows, stage, nv * 2);
-}
-
 // BF16: the operands' type, or fp16.
 template <bool BF16>
 struct SwigluPiece {
     SwigluKeep k;
     int vec_h, vec_p;                        // bytes that every row is aligned to: 32, 16, 0
     static constexpr int kStep = 32;
-    __device__ __forceinline__ int ahead(size_t, bool, int, int) const { return 0; }
+    static constexpr uint32_t kWarpStaging = kGtStoreWords * 4;
+    __device__ __forceinline__ int ahead(size_t, int, int, int, uint32_t*) const { return 0; }
     __device__ __forceinline__ void quad(size_t row, int c, const float* v, bool live) const {
         swiglu_quad(k, row, c, v, live);
     }
@@ -89,78 +58,129 @@ struct SwigluPiece {
     }
 };
 
+// The gradient reads as much as it writes, 10 bytes a column and row.  A lane a
+// row, 32 bytes at a time, both took two shared-memory cycles a lane and access
+// and bound the kernel (8192 rows, 2048 to 4096 columns: 125 us, now 112, against
+// 72 of the plain product, which moves a fifth of the bytes).  So 32 columns of the warp's 32 rows go through
+// its staging, 128 bytes a row: p comes there by asynchronous copies of
+// neighbouring 16 bytes, the next columns' while these are worked on; a lane
+// reads its row's and leaves dp in its place; and 8 lanes store a row's line.
+// h follows the same way.  16-byte pieces are spread over the banks by the row.
 template <bool BF16>
 struct SwigluBackPiece {
     SwigluBack k;
-    int vec_p, vec_dp, vec_h;
-    // Sixteen columns' part of p, read while what is before it is worked on (one
-    // after the other, 8192 rows of 4096 columns, a dense block: 156 us; DENSE).
+    static constexpr int kStep = 32;
+    static constexpr uint32_t kBuffer = 32 * 128, kWarpStaging = 2 * kBuffer;
     struct Ahead {
-        uint32_t lo[8], hi[8];
-        float scale;
+        int buf;                             // the buffer that holds the next columns
+        uint32_t scales;                     // and their two scale bytes (of the lane's row)
     };
-    __device__ __forceinline__ void read(Ahead& a, size_t row, bool live, int c) const {
-        if (!live || c >= k.I) return;
-        const size_t at = row * 2 * k.I + 2 * c;
-        const uint8_t* p = static_cast<const uint8_t*>(k.p);
-        if (k.scales != nullptr) {                           // whole blocks
-            get32(p + at, vec_p == 32, a.lo);
-            a.scale = act8_scale(__ldg(k.scales + at / kAct8Block));
-        } else {
-            get32(p + at * 2, vec_p == 32, a.lo);
-            if (c + 8 < k.I) get32(p + (at + 16) * 2, vec_p == 32, a.hi);
+    static __device__ __forceinline__ uint32_t place(int r, int chunk) {
+        return uint32_t(r) * 128 + uint32_t((chunk ^ (r & 7)) * 16);
+    }
+    // Starts the copies of p's columns c .. of rows row0 ..
+    __device__ __forceinline__ void fetch(Ahead& a, size_t row0, int rows, int c, uint32_t* stage) const {
+        const int lane = threadIdx.x & 31, n = min(32, k.I - c);
+        const uint32_t to = smem_u32(stage) + a.buf * kBuffer;
+        const bool small = k.scales != nullptr;              // 64 bytes a row, else 128
+        const int per = small ? 4 : 8, have = small ? n / 8 : n / 4;
+        const size_t pitch = size_t(2) * k.I * (small ? 1 : 2);
+        const uint8_t* p = static_cast<const uint8_t*>(k.p) + row0 * pitch + size_t(c) * (small ? 2 : 4);
+        const int q = lane & (per - 1);
+        if (q < have)
+            for (int r = lane / per; r < rows; r += 32 / per)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + place(r, q)),
+                             "l"(p + r * pitch + q * 16)
+                             : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (small && lane < rows) {
+            const uint8_t* s = k.scales + (row0 + lane) * (2 * k.I / kAct8Block) + 2 * c / kAct8Block;
+            a.scales = __ldg(s) | (n > 16 ? uint32_t(__ldg(s + 1)) << 8 : 0u);
         }
     }
-    // The first of them, and the others' lines into the L2, while the products run.
-    __device__ __forceinline__ Ahead ahead(size_t row, bool live, int c0, int end) const {
+    __device__ __forceinline__ Ahead ahead(size_t row0, int rows, int c0, int end, uint32_t* stage) const {
         Ahead a{};
-        read(a, row, live, c0);
-        const int bytes = k.scales != nullptr ? 2 : 4;       // of a column
-        for (int c = c0; c < end; c += 128 / bytes)
-            if (live)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(k.p) +
-                                                              (row * k.I + c) * bytes));
+        if (rows > 0 && c0 < end) fetch(a, row0, rows, c0, stage);
         return a;
     }
     __device__ __forceinline__ void quad(size_t row, int c, const float* v, bool live) const {
         swiglu_back_quad(k, row, c, v, live);
     }
-    static constexpr int kStep = 16;
+    // `chunks` pieces of 16 bytes a row, out of a buffer into rows of `pitch` bytes.
+    template <int PER>
+    static __device__ __forceinline__ void put(uint8_t* out, size_t pitch, int rows, int chunks, const uint8_t* buf) {
+        const int lane = threadIdx.x & 31, q = lane % PER;
+        __syncwarp();
+        if (q < chunks) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int r = i * (32 / PER) + lane / PER;
+                if (r < rows)
+                    *reinterpret_cast<uint4*>(out + r * pitch + q * 16) =
+                        *reinterpret_cast<const uint4*>(buf + place(r, q));
+            }
+        }
+        __syncwarp();
+    }
     __device__ __forceinline__ void take(Ahead& a, size_t row0, int rows, int c, int end, const float* v,
                                          uint32_t* stage) const {
-        const int lane = threadIdx.x & 31, nv = k.I - c;     // nv is a multiple of 8
+        const int lane = threadIdx.x & 31, nv = min(32, k.I - c);            // a multiple of 8
         if (rows <= 0 || nv <= 0) return;
-        const Ahead now = a;
-        if (c + 16 < end) read(a, row0 + lane, lane < rows, c + 16);
-        float g[16], u[16];
+        uint8_t* buf = reinterpret_cast<uint8_t*>(stage) + a.buf * kBuffer;
+        const uint32_t scales = a.scales;
+        a.buf ^= 1;
+        if (c + 32 < end) {
+            fetch(a, row0, rows, c + 32, stage);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
+        // what does not exist is worked on like the rest and not stored
+        uint4 small[4];
         if (k.scales != nullptr) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                float q[4];
-                act8_values(now.lo[j / 2], now.scale, q);
-                g[j] = q[0];
-                u[j] = q[1];
-                g[j + 1] = q[2];
-                u[j + 1] = q[3];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t w = j < 8 ? now.lo[j & 7] : now.hi[j & 7];
-                g[j] = unpack16(w & 0xffffu, BF16);
-                u[j] = BF16 ? bf16_hi(w) : unpack16(w >> 16, BF16);
-            }
+            for (int q = 0; q < 4; ++q) small[q] = *reinterpret_cast<const uint4*>(buf + place(lane, q));
         }
-        uint32_t d[16], h[8];
+        uint32_t h[16];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const SwigluGrads2 o = swiglu_grads2(g + j, u + j, v + j);
-            d[j] = pack16(o.dg.x, o.du.x, BF16);
-            d[j + 1] = pack16(o.dg.y, o.du.y, BF16);
-            h[j / 2] = pack16(o.h.x, o.h.y, BF16);
+        for (int q = 0; q < 8; ++q) {                        // four columns
+            float g[4], u[4];
+            if (k.scales != nullptr) {
+                const float s = act8_scale((scales >> (q < 4 ? 0 : 8)) & 0xffu);
+                const uint4& w = small[q / 2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float t[4];
+                    act8_values(q & 1 ? (j ? w.w : w.z) : (j ? w.y : w.x), s, t);
+                    g[2 * j] = t[0];
+                    u[2 * j] = t[1];
+                    g[2 * j + 1] = t[2];
+                    u[2 * j + 1] = t[3];
+                }
+            } else {
+                const uint4 w = *reinterpret_cast<const uint4*>(buf + place(lane, q));
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    g[j] = unpack16(x[j] & 0xffffu, BF16);
+                    u[j] = BF16 ? bf16_hi(x[j]) : unpack16(x[j] >> 16, BF16);
+                }
+            }
+            const SwigluGrads2 o = swiglu_grads2(g, u, v + 4 * q), p = swiglu_grads2(g + 2, u + 2, v + 4 * q + 2);
+            *reinterpret_cast<uint4*>(buf + place(lane, q)) =
+                make_uint4(pack16(o.dg.x, o.du.x, BF16), pack16(o.dg.y, o.du.y, BF16),
+                           pack16(p.dg.x, p.du.x, BF16), pack16(p.dg.y, p.du.y, BF16));
+            h[2 * q] = pack16(o.h.x, o.h.y, BF16);
+            h[2 * q + 1] = pack16(p.h.x, p.h.y, BF16);
         }
-        put_rows<16>(k.dp, row0 * 2 * k.I + 2 * c, size_t(2) * k.I, rows, d, 2 * nv, vec_dp, stage);
-        if (k.h != nullptr) put_rows<8>(k.h, row0 * k.I + c, k.I, rows, h, nv, vec_h, stage);
+        put<8>(static_cast<uint8_t*>(k.dp) + (row0 * 2 * k.I + 2 * c) * 2, size_t(4) * k.I, rows, nv / 4, buf);
+        if (k.h == nullptr) return;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(buf + place(lane, q)) =
+                make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+        put<4>(static_cast<uint8_t*>(k.h) + (row0 * k.I + c) * 2, size_t(2) * k.I, rows, nv / 8, buf);
     }
 };
 
