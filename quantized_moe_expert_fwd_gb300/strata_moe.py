@@ -617,33 +617,48 @@ def moe_grouped_mm_fp4(xq, xs, wq, wsc, offsets, y, fmt: int, ws, alpha=None,
 
 
 # ------------------------------------------- a tuning step around the experts
-def _on_device(dev, stream, tensors):
-    """As _grouped, for calls without a workspace of their own: `dev` is their first tensor's."""
+# As above, the checks look at each tensor once and name what they refuse only
+# when they refuse (a decode step's norms 8.4 -> 7.8 us a call, 3.3 of them the
+# library's and the launch's).
+_MOST = 0x7fffffff
+
+
+def _current(dev, stream):
+    """The stream handle of the device of a call's tensors, which must be the current one."""
     if dev < 0 or dev != _get_device():
         raise ValueError("the tensors must be on the current CUDA device")
-    for t in tensors:
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("tensors must be on one device" if t.get_device() != dev
-                             else "tensors passed to strata_moe must be contiguous")
     return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _with_ws(ws, stream):
+    if ws.dtype is not _U8 or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous uint8 tensor")
+    dev = ws.get_device()
+    return dev, _current(dev, stream)
+
+
+def _refuse(dev, *wanted):
+    """Raises what is wrong with the first of (name, tensor, type, shape or number of elements)."""
+    for what, t, dtype, shape in wanted:
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"tensors must be on one device: {what} is not")
+        if not t.is_contiguous():
+            raise ValueError(f"tensors passed to strata_moe must be contiguous: {what} is not")
+        if isinstance(shape, int):
+            if t.dtype is not dtype or t.numel() != shape:
+                raise ValueError(f"{what} must be a {dtype} tensor of {shape} entries")
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError("tensors must be contiguous, of their types and shapes, and on one device")
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
-
-
-def _kept(p, p_scales, M, cols, dtype):
-    """Checks p as moe_grouped_swiglu keeps it."""
-    _shape(p, (M, cols), "p")
-    if p_scales is None:
-        if p.dtype is not dtype:
-            raise TypeError(f"p must be {dtype} (or uint8 with p_scales), not {p.dtype}")
-        return
-    if p.dtype is not _U8 or p_scales.dtype is not _U8:
-        raise TypeError("p kept in 8 bits and its scales must be uint8")
-    if cols % 32:
-        raise ValueError("p is kept in 8 bits where its width is a multiple of 32")
-    _shape(p_scales, (M, cols // 32), "p_scales")
 
 
 def moe_grouped_swiglu(x, w, offsets, h, ws, p=None, p_scales=None, stream=None):
@@ -653,25 +668,49 @@ def moe_grouped_swiglu(x, w, offsets, h, ws, p=None, p_scales=None, stream=None)
     (uint8, with p_scales uint8 [M][2I / 32])."""
     E, N, K = w.shape
     M = x.shape[0]
-    _int32(M, K, N, E)
-    st = _grouped(ws, stream, [t for t in (x, w, offsets, h, p, p_scales) if t is not None])
-    dt = _dtype(x, "x", _DTYPES16)
-    if w.dtype is not x.dtype or h.dtype is not x.dtype:
-        raise TypeError(f"x, w and h must have one type, not {x.dtype}, {w.dtype} and {h.dtype}")
-    if N % 2:
+    if M > _MOST or K > _MOST or N > _MOST or E > _MOST:
+        _int32(M, K, N, E)
+    dev, st = _with_ws(ws, stream)
+    t = x.dtype
+    dt = _DTYPES16.get(t)
+    if dt is None:
+        _dtype(x, "x", _DTYPES16)
+    if w.dtype is not t or h.dtype is not t:
+        raise TypeError(f"x, w and h must have one type, not {t}, {w.dtype} and {h.dtype}")
+    if N & 1:
         raise ValueError("w must have a gate and an up row for each column of h")
-    _shape(x, (M, K), "x")
-    _shape(h, (M, N // 2), "h")
+    if (x.shape != (M, K) or h.shape != (M, N >> 1) or not x.is_contiguous() or not h.is_contiguous()
+            or not w.is_contiguous() or not offsets.is_contiguous()
+            or not x.get_device() == h.get_device() == w.get_device() == offsets.get_device() == dev):
+        _refuse(dev, ("x", x, t, (M, K)), ("h", h, t, (M, N >> 1)), ("w", w, t, w.shape),
+                ("offsets", offsets, offsets.dtype, offsets.shape))
     if p is not None:
-        _kept(p, p_scales, M, N, x.dtype)
+        _kept(p, p_scales, M, N, t, dev)
     elif p_scales is not None:
         raise ValueError("p_scales without p")
     _offsets(offsets, E)
     status = (_lib or load()).moe_grouped_swiglu(
-        dt, x.data_ptr(), w.data_ptr(), M, K, N // 2, E, offsets.data_ptr(), h.data_ptr(), _at(p),
+        dt, x.data_ptr(), w.data_ptr(), M, K, N >> 1, E, offsets.data_ptr(), h.data_ptr(), _at(p),
         _at(p_scales), ws.data_ptr(), ws.numel(), st)
     if status:
         _check("moe_grouped_swiglu", status)
+
+
+def _kept(p, p_scales, M, cols, dtype, dev):
+    """Checks p as moe_grouped_swiglu keeps it."""
+    if p_scales is None:
+        if p.dtype is not dtype:
+            raise TypeError(f"p must be {dtype} (or uint8 with p_scales), not {p.dtype}")
+        if p.shape != (M, cols) or p.get_device() != dev or not p.is_contiguous():
+            _refuse(dev, ("p", p, dtype, (M, cols)))
+        return
+    if p.dtype is not _U8 or p_scales.dtype is not _U8:
+        raise TypeError("p kept in 8 bits and its scales must be uint8")
+    if cols % 32:
+        raise ValueError("p is kept in 8 bits where its width is a multiple of 32")
+    if (p.shape != (M, cols) or p_scales.shape != (M, cols // 32) or not p.is_contiguous()
+            or not p_scales.is_contiguous() or not p.get_device() == p_scales.get_device() == dev):
+        _refuse(dev, ("p", p, _U8, (M, cols)), ("p_scales", p_scales, _U8, (M, cols // 32)))
 
 
 def moe_grouped_swiglu_bwd(dy, w, p, offsets, dp, ws, p_scales=None, h=None, stream=None):
@@ -680,16 +719,22 @@ def moe_grouped_swiglu_bwd(dy, w, p, offsets, dp, ws, p_scales=None, h=None, str
     where it is given."""
     E, N, I = w.shape
     M = dy.shape[0]
-    _int32(M, N, 2 * I, E)
-    st = _grouped(ws, stream, [t for t in (dy, w, p, offsets, dp, p_scales, h) if t is not None])
-    dt = _dtype(dy, "dy", _DTYPES16)
-    if w.dtype is not dy.dtype or dp.dtype is not dy.dtype or (h is not None and h.dtype is not dy.dtype):
+    if M > _MOST or N > _MOST or 2 * I > _MOST or E > _MOST:
+        _int32(M, N, 2 * I, E)
+    dev, st = _with_ws(ws, stream)
+    t = dy.dtype
+    dt = _DTYPES16.get(t)
+    if dt is None:
+        _dtype(dy, "dy", _DTYPES16)
+    if w.dtype is not t or dp.dtype is not t or (h is not None and h.dtype is not t):
         raise TypeError("dy, w, dp and h must have one type")
-    _shape(dy, (M, N), "dy")
-    _shape(dp, (M, 2 * I), "dp")
-    if h is not None:
-        _shape(h, (M, I), "h")
-    _kept(p, p_scales, M, 2 * I, dy.dtype)
+    if (dy.shape != (M, N) or dp.shape != (M, 2 * I) or not dy.is_contiguous() or not dp.is_contiguous()
+            or not w.is_contiguous() or not offsets.is_contiguous()
+            or not dy.get_device() == dp.get_device() == w.get_device() == offsets.get_device() == dev
+            or (h is not None and (h.shape != (M, I) or not h.is_contiguous() or h.get_device() != dev))):
+        _refuse(dev, ("dy", dy, t, (M, N)), ("dp", dp, t, (M, 2 * I)), ("h", h, t, (M, I)), ("w", w, t, w.shape),
+                ("offsets", offsets, offsets.dtype, offsets.shape))
+    _kept(p, p_scales, M, 2 * I, t, dev)
     _offsets(offsets, E)
     status = (_lib or load()).moe_grouped_swiglu_bwd(
         dt, dy.data_ptr(), w.data_ptr(), p.data_ptr(), _at(p_scales), M, N, I, E, offsets.data_ptr(),
@@ -698,21 +743,26 @@ def moe_grouped_swiglu_bwd(dy, w, p, offsets, dp, ws, p_scales=None, h=None, str
         _check("moe_grouped_swiglu_bwd", status)
 
 
-def _act8(q, scales, rows, cols):
+def _act8(q, scales, rows, cols, dev):
     if q.dtype is not _U8 or scales.dtype is not _U8:
         raise TypeError("codes and scales must be uint8")
-    _shape(q, (rows, cols), "q")
-    _shape(scales, (rows, cols // 32), "scales")
+    if (q.shape != (rows, cols) or scales.shape != (rows, cols // 32) or not q.is_contiguous()
+            or not scales.is_contiguous() or not q.get_device() == scales.get_device() == dev):
+        _refuse(dev, ("q", q, _U8, (rows, cols)), ("scales", scales, _U8, (rows, cols // 32)))
 
 
 def moe_act8_save(x, q, scales, stream=None):
     """Rows of x [R][C] (bf16, fp16 or fp32; C a multiple of 32) kept in 8 bits:
     q uint8 [R][C] and scales uint8 [R][C / 32]."""
     R, C = x.shape
-    _int32(R, C)
-    st = _on_device(x.get_device(), stream, (x, q, scales))
+    if R > _MOST or C > _MOST:
+        _int32(R, C)
+    dev = x.get_device()
+    st = _current(dev, stream)
     dt = _dtype(x, "x")
-    _act8(q, scales, R, C)
+    _act8(q, scales, R, C, dev)
+    if not x.is_contiguous():
+        _refuse(dev, ("x", x, x.dtype, x.shape))
     status = (_lib or load()).moe_act8_save(dt, x.data_ptr(), R, C, q.data_ptr(), scales.data_ptr(), st)
     if status:
         _check("moe_act8_save", status)
@@ -724,15 +774,20 @@ def moe_act8_load(q, scales, out, ws, perm=None, top_k: int = 1, stream=None):
     than out: the rows behind it stay as they are."""
     R, C = q.shape
     rows = out.shape[0]
-    _int32(R, C, rows, top_k)
-    st = _grouped(ws, stream, (q, scales, out) if perm is None else (q, scales, out, perm))
+    if R > _MOST or C > _MOST or rows > _MOST or not -_MOST <= top_k <= _MOST:
+        _int32(R, C, rows, top_k)
+    dev, st = _with_ws(ws, stream)
     od = _dtype(out, "out")
-    _act8(q, scales, R, C)
-    _shape(out, (rows, C), "out")
+    _act8(q, scales, R, C, dev)
+    if out.shape != (rows, C) or not out.is_contiguous() or out.get_device() != dev:
+        _refuse(dev, ("out", out, out.dtype, (rows, C)))
     if perm is not None:
-        if perm.dtype is not _I32 or perm.dim() != 1 or perm.numel() > rows:
+        n = perm.numel()
+        if perm.dtype is not _I32 or perm.dim() != 1 or n > rows:
             raise ValueError("perm must be an int32 vector of at most out's rows")
-        rows = perm.numel()
+        if not perm.is_contiguous() or perm.get_device() != dev:
+            _refuse(dev, ("perm", perm, _I32, n))
+        rows = n
         perm = perm.data_ptr()
     status = (_lib or load()).moe_act8_load(q.data_ptr(), scales.data_ptr(), R, C, perm, top_k, rows, od,
                                             out.data_ptr(), ws.data_ptr(), ws.numel(), st)
@@ -740,15 +795,17 @@ def moe_act8_load(q, scales, out, ws, perm=None, top_k: int = 1, stream=None):
         _check("moe_act8_load", status)
 
 
-def _slots(inv_perm, T, weights):
+def _slots(inv_perm, T, weights, dev):
     """Slots a token, of inv_perm as moe_permute writes it (or [T][top_k])."""
     n = inv_perm.numel()
     if inv_perm.dtype is not _I32 or (n % T if T else n):
         raise ValueError("inv_perm must be an int32 tensor of tokens x top_k entries")
-    top_k = n // T if T else 1
-    if weights is not None and (weights.dtype is not _F32 or weights.numel() != n):
-        raise ValueError(f"weights must be an fp32 tensor of {n} entries")
-    return top_k
+    if not inv_perm.is_contiguous() or inv_perm.get_device() != dev:
+        _refuse(dev, ("inv_perm", inv_perm, _I32, n))
+    if weights is not None and (weights.dtype is not _F32 or weights.numel() != n
+                                or not weights.is_contiguous() or weights.get_device() != dev):
+        _refuse(dev, ("weights", weights, _F32, n))
+    return n // T if T else 1
 
 
 def moe_slots_combine(y, inv_perm, out, ws, weights=None, stream=None):
@@ -756,15 +813,20 @@ def moe_slots_combine(y, inv_perm, out, ws, weights=None, stream=None):
     [T][H] in y's type or fp32; weights fp32 [T][top_k], None for ones)."""
     M, H = y.shape
     T = out.shape[0]
-    _int32(M, H, T)
-    st = _grouped(ws, stream, (y, inv_perm, out) if weights is None else (y, inv_perm, out, weights))
-    dt, od = _dtype(y, "y", _DTYPES16), _dtype(out, "out")
-    if od != dt and od != 2:
+    if M > _MOST or H > _MOST or T > _MOST:
+        _int32(M, H, T)
+    dev, st = _with_ws(ws, stream)
+    dt, od = _DTYPES16.get(y.dtype), _DTYPES.get(out.dtype)
+    if dt is None or (od != dt and od != 2):
+        _dtype(y, "y", _DTYPES16)
         raise TypeError(f"out must be {y.dtype} or fp32, not {out.dtype}")
-    _shape(out, (T, H), "out")
+    if (out.shape != (T, H) or not y.is_contiguous() or not out.is_contiguous()
+            or not y.get_device() == out.get_device() == dev):
+        _refuse(dev, ("y", y, y.dtype, (M, H)), ("out", out, out.dtype, (T, H)))
+    top_k = _slots(inv_perm, T, weights, dev)
     status = (_lib or load()).moe_slots_combine(
-        dt, y.data_ptr(), M, H, inv_perm.data_ptr(), _at(weights), T, _slots(inv_perm, T, weights), od,
-        out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+        dt, y.data_ptr(), M, H, inv_perm.data_ptr(), _at(weights), T, top_k, od, out.data_ptr(),
+        ws.data_ptr(), ws.numel(), st)
     if status:
         _check("moe_slots_combine", status)
 
@@ -778,18 +840,24 @@ def moe_slots_spread(dout, inv_perm, ws, dy=None, weights=None, y=None, dweights
     if slots is None:
         raise ValueError("nothing to compute: give dy, or y and dweights")
     M = slots.shape[0]
-    _int32(M, H, T)
-    st = _grouped(ws, stream,
-                  [t for t in (dout, inv_perm, dy, weights, y, dweights) if t is not None])
-    dt = _dtype(dout, "dout", _DTYPES16)
-    for t, what in ((dy, "dy"), (y, "y")):
-        if t is not None:
-            _shape(t, (M, H), what)
-            if t.dtype is not dout.dtype:
-                raise TypeError(f"{what} must be {dout.dtype}, not {t.dtype}")
-    top_k = _slots(inv_perm, T, weights)
-    if dweights is not None and (dweights.dtype is not _F32 or dweights.numel() != T * top_k):
-        raise ValueError(f"dweights must be an fp32 tensor of {T * top_k} entries")
+    if M > _MOST or H > _MOST or T > _MOST:
+        _int32(M, H, T)
+    dev, st = _with_ws(ws, stream)
+    t = dout.dtype
+    dt = _DTYPES16.get(t)
+    if dt is None:
+        _dtype(dout, "dout", _DTYPES16)
+    shape = (M, H)
+    if (not dout.is_contiguous() or dout.get_device() != dev
+            or (dy is not None and (dy.dtype is not t or dy.shape != shape or not dy.is_contiguous()
+                                    or dy.get_device() != dev))
+            or (y is not None and (y.dtype is not t or y.shape != shape or not y.is_contiguous()
+                                   or y.get_device() != dev))):
+        _refuse(dev, ("dout", dout, t, dout.shape), ("dy", dy, t, shape), ("y", y, t, shape))
+    top_k = _slots(inv_perm, T, weights, dev)
+    if dweights is not None and (dweights.dtype is not _F32 or dweights.numel() != T * top_k
+                                 or not dweights.is_contiguous() or dweights.get_device() != dev):
+        _refuse(dev, ("dweights", dweights, _F32, T * top_k))
     status = (_lib or load()).moe_slots_spread(
         dt, dout.data_ptr(), inv_perm.data_ptr(), _at(weights), _at(y), T, top_k, M, H, _at(dy),
         _at(dweights), ws.data_ptr(), ws.numel(), st)
@@ -799,7 +867,7 @@ def moe_slots_spread(dout, inv_perm, ws, dy=None, weights=None, y=None, dweights
 
 def moe_norm_workspace_bytes(H: int) -> int:
     H = int(H)
-    return 0 if H > 0x7fffffff or H < 0 else int(load().moe_norm_workspace_bytes(H))
+    return 0 if H > _MOST or H < 0 else int(load().moe_norm_workspace_bytes(H))
 
 
 def make_norm_workspace(H: int, device="cuda") -> torch.Tensor:
@@ -810,18 +878,24 @@ def make_norm_workspace(H: int, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _norm_types(act, resid, rows, vectors, T, H):
-    """dtype and resid_dtype numbers; rows: (tensor, its type, name) of [T][H] tensors; vectors:
-    (fp32 tensor, length, name)."""
-    for t, dtype, what in rows:
-        if t is not None:
-            if t.dtype is not dtype:
-                raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-            if t.shape != (T, H):
-                raise ValueError(f"{what} must have shape {(T, H)}, not {tuple(t.shape)}")
-    for t, n, what in vectors:
-        if t is not None and (t.dtype is not _F32 or t.numel() != n):
-            raise ValueError(f"{what} must be an fp32 tensor of {n} entries")
+def _norm_rows(tensors, dtype, shape, dev):
+    """Whether all of them (None aside) are rows of that type and shape."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                              or t.get_device() != dev):
+            return False
+    return True
+
+
+def _norm_vectors(tensors, n, dev):
+    for t in tensors:
+        if t is not None and (t.dtype is not _F32 or t.numel() != n or not t.is_contiguous()
+                              or t.get_device() != dev):
+            return False
+    return True
+
+
+def _norm_types(act, resid):
     dt, rt = _DTYPES16.get(act), _DTYPES.get(resid)
     if dt is None or (rt != dt and rt != 2):
         raise TypeError(f"f and x must be bf16 or fp16 and the residual of that type or fp32, not {act} "
@@ -836,16 +910,22 @@ def moe_norm_residual(resid, resid_out=None, f=None, x=None, w_pre=None, w_post=
     norms after a block (post_norm) and before the next one with their weights
     (fp32 [H]); resid fp32 or f's type, resid_out may be resid; rstd fp32 [T][2]
     keeps what the backward pass needs."""
-    T, H = resid.shape
-    _int32(T, H)
-    st = _on_device(resid.get_device(), stream,
-                    [t for t in (resid, resid_out, f, x, w_pre, w_post, gate, rstd) if t is not None])
-    act = f.dtype if f is not None else x.dtype if x is not None else None
-    if act is None:                      # a residual alone: its own type, or any
-        act = resid.dtype if resid.dtype in _DTYPES16 else torch.bfloat16
-    dt, rt = _norm_types(act, resid.dtype, ((f, act, "f"), (x, act, "x"), (resid_out, resid.dtype, "resid_out")),
-                         ((w_pre, H, "w_pre"), (w_post, H, "w_post"), (gate, T, "gate"),
-                          (rstd, 2 * T, "rstd")), T, H)
+    shape = resid.shape
+    T, H = shape
+    if T > _MOST or H > _MOST:
+        _int32(T, H)
+    dev, rd = resid.get_device(), resid.dtype
+    st = _current(dev, stream)
+    # (a residual alone: its own type, or any)
+    act = f.dtype if f is not None else x.dtype if x is not None else rd if rd in _DTYPES16 else torch.bfloat16
+    dt, rt = _norm_types(act, rd)
+    if not (_norm_rows((f, x), act, shape, dev) and _norm_rows((resid, resid_out), rd, shape, dev)
+            and _norm_vectors((w_pre, w_post), H, dev)
+            and (gate is None or _norm_vectors((gate,), T, dev))
+            and (rstd is None or _norm_vectors((rstd,), 2 * T, dev))):
+        _refuse(dev, ("f", f, act, shape), ("x", x, act, shape), ("resid", resid, rd, shape),
+                ("resid_out", resid_out, rd, shape), ("w_pre", w_pre, _F32, H), ("w_post", w_post, _F32, H),
+                ("gate", gate, _F32, T), ("rstd", rstd, _F32, 2 * T))
     status = (_lib or load()).moe_norm_residual(
         dt, rt, _at(f), resid.data_ptr(), _at(w_post), _at(w_pre), _at(gate), T, H, 1 if post_norm else 0,
         alpha, beta, eps, _at(resid_out), _at(x), _at(rstd), st)
@@ -861,22 +941,26 @@ def moe_norm_residual_bwd(resid_out, rstd, ws=None, dx=None, dresid_out=None, f=
     with the resid_out and rstd that it wrote: dresid (may be dresid_out), df,
     dgate fp32 [T], dw_pre and dw_post fp32 [H], each where given (the last two
     need ws, make_norm_workspace(H))."""
-    T, H = resid_out.shape
-    _int32(T, H)
-    st = _on_device(resid_out.get_device(), stream,
-                    [t for t in (resid_out, rstd, ws, dx, dresid_out, f, w_pre, w_post, gate, dresid, df,
-                                 dgate, dw_pre, dw_post) if t is not None])
-    act = next((t.dtype for t in (dx, f, df) if t is not None), None)
-    if act is None:
-        act = resid_out.dtype if resid_out.dtype in _DTYPES16 else torch.bfloat16
-    rd = resid_out.dtype
-    dt, rt = _norm_types(act, rd, ((dx, act, "dx"), (f, act, "f"), (df, act, "df"),
-                                   (dresid_out, rd, "dresid_out"), (dresid, rd, "dresid")),
-                         ((w_pre, H, "w_pre"), (w_post, H, "w_post"), (gate, T, "gate"),
-                          (rstd, 2 * T, "rstd"), (dgate, T, "dgate"), (dw_pre, H, "dw_pre"),
-                          (dw_post, H, "dw_post")), T, H)
-    if ws is not None and ws.dtype is not _U8:
-        raise ValueError("the workspace must be a contiguous uint8 tensor")
+    shape = resid_out.shape
+    T, H = shape
+    if T > _MOST or H > _MOST:
+        _int32(T, H)
+    dev, rd = resid_out.get_device(), resid_out.dtype
+    st = _current(dev, stream)
+    act = dx.dtype if dx is not None else f.dtype if f is not None else df.dtype if df is not None \
+        else rd if rd in _DTYPES16 else torch.bfloat16
+    dt, rt = _norm_types(act, rd)
+    if not (_norm_rows((dx, f, df), act, shape, dev)
+            and _norm_rows((resid_out, dresid_out, dresid), rd, shape, dev)
+            and _norm_vectors((w_pre, w_post, dw_pre, dw_post), H, dev)
+            and _norm_vectors((gate, dgate), T, dev) and _norm_vectors((rstd,), 2 * T, dev)):
+        _refuse(dev, ("dx", dx, act, shape), ("f", f, act, shape), ("df", df, act, shape),
+                ("resid_out", resid_out, rd, shape), ("dresid_out", dresid_out, rd, shape),
+                ("dresid", dresid, rd, shape), ("w_pre", w_pre, _F32, H), ("w_post", w_post, _F32, H),
+                ("dw_pre", dw_pre, _F32, H), ("dw_post", dw_post, _F32, H), ("gate", gate, _F32, T),
+                ("dgate", dgate, _F32, T), ("rstd", rstd, _F32, 2 * T))
+    if ws is not None and (ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("the workspace must be a contiguous uint8 tensor on the tensors' device")
     status = (_lib or load()).moe_norm_residual_bwd(
         dt, rt, _at(dx), _at(dresid_out), _at(f), resid_out.data_ptr(), _at(w_post), _at(w_pre), _at(gate),
         _at(rstd), T, H, 1 if post_norm else 0, alpha, beta, _at(df), _at(dresid), _at(dgate),
