@@ -24,6 +24,10 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a)
         // r' may take r's place
         rr[c] = row.template load<false>(static_cast<const TR*>(a.resid) + at, c, H);
     }
+    Raw<float, 8> wpost[VEC ? C : 1];
+#pragma unroll
+    for (int c = 0; VEC && c < C; ++c)
+        if (a.w_post) wpost[c] = row.template load<true>(a.w_post, c, H);
     const float g = a.beta * (a.gate ? __ldg(a.gate + t) : 1.0f);
     const float inv = 1.0f / float(H);
     float s0 = 1.0f, s1 = 1.0f;
@@ -44,7 +48,8 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock) k_norm(NormArgs a)
         for (int j = 0; j < 8; ++j) v[c][j] = a.alpha * rr[c].get(j);
         if (a.f) {
             Raw<float, 8> w{};
-            if (a.w_post) w = row.template load<true>(a.w_post, c, H);
+            if (VEC) w = wpost[VEC ? c : 0];
+            else if (a.w_post) w = row.template load<true>(a.w_post, c, H);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float n = rf[c].get(j) * s0;
@@ -131,13 +136,17 @@ cudaError_t run_rows(const NormArgs& a, cudaStream_t s) {
     return row_launch(k_norm<T, TR, W, C, VEC>, dim3((a.T + R::kGroups - 1) / R::kGroups), dim3(R::kBlock), s, a);
 }
 
+// Sixteen columns a thread (us, 32768 rows of 512 columns, 16384 of 2048, 8192 of
+// 4096; at the copy's rate 30, 59, 59): 8 a thread 36.9, 71.2, 66.3; 16 32.5,
+// 61.0, 60.9; 32 32.4, 63.2, 63.7; 16 and the weights read with the row 31.1,
+// 59.3, 59.3 (columns one by one, 16384 x 1031: 54.8, with them 62.0).
 template <typename T, typename TR, bool VEC>
 cudaError_t run_norm(const NormArgs& a, cudaStream_t s) {
     if (a.H <= 256) return run_rows<T, TR, 1, 1, VEC>(a, s);
-    if (a.H <= 512) return run_rows<T, TR, 2, 1, VEC>(a, s);
-    if (a.H <= 1024) return run_rows<T, TR, 4, 1, VEC>(a, s);
-    if (a.H <= 2048) return run_rows<T, TR, 8, 1, VEC>(a, s);
-    if (a.H <= 4096) return run_rows<T, TR, 16, 1, VEC>(a, s);
+    if (a.H <= 512) return run_rows<T, TR, 1, 2, VEC>(a, s);
+    if (a.H <= 1024) return run_rows<T, TR, 2, 2, VEC>(a, s);
+    if (a.H <= 2048) return run_rows<T, TR, 4, 2, VEC>(a, s);
+    if (a.H <= 4096) return run_rows<T, TR, 8, 2, VEC>(a, s);
     if (a.H <= 8192) return run_rows<T, TR, 16, 2, VEC>(a, s);
     if (a.H <= 16384) return run_rows<T, TR, 32, 2, VEC>(a, s);
     const int most = device_info().sms * 8;
