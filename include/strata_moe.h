@@ -610,7 +610,8 @@ STRATA_API strata_status moe_slots_spread(int32_t dtype, const void* dout_dev,
                                           void* ws_dev, size_t ws_bytes, void* stream);
 
 /* Workspace of moe_norm_residual_bwd's weight gradients for rows of H columns
- * (0 for an H that is refused); 256-byte aligned, any contents. */
+ * (0 for an H that is refused); 256-byte aligned, any contents, not shared by
+ * calls that may run at the same time. */
 STRATA_API size_t moe_norm_workspace_bytes(int32_t H);
 
 /* The norm after a block, its gate, the residual, and the norm before the next

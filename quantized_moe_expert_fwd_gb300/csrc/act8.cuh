@@ -47,10 +47,13 @@ __device__ __forceinline__ void act8_values(uint32_t codes, float scale, float* 
         "  cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
         : "=r"(lo), "=r"(hi)
         : "r"(codes));
-    v[0] = f16_to_f32(uint16_t(lo)) * scale;
-    v[1] = f16_to_f32(uint16_t(lo >> 16)) * scale;
-    v[2] = f16_to_f32(uint16_t(hi)) * scale;
-    v[3] = f16_to_f32(uint16_t(hi >> 16)) * scale;
+    const uint64_t s = pk(scale, scale);
+    const float2 a = upk(mul2(pk(f16_to_f32(uint16_t(lo)), f16_to_f32(uint16_t(lo >> 16))), s));
+    const float2 b = upk(mul2(pk(f16_to_f32(uint16_t(hi)), f16_to_f32(uint16_t(hi >> 16))), s));
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
 }
 
 }  // namespace strata

@@ -28,6 +28,9 @@ SHAPES = {
     "one_by_one": ([2, 30], 1, 1),
     "long": ([40, 300, 7], 2560, 136),
     "longer": ([3, 140], 4168, 272),
+    # reductions of several pieces in long groups, and in many groups of one tile
+    "long_wide": ([900, 1200, 40], 2184, 520),
+    "long_each": ([100 + e % 7 for e in range(60)], 2184, 520),
     "many": ([(7 * e) % 11 for e in range(300)], 128, 40),
     "long_groups": ([1500, 0, 777, 2048, 1], 320, 136),
     "long_even": ([1024, 512], 512, 512),
