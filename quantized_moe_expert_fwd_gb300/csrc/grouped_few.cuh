@@ -1,5 +1,5 @@
 // grouped_few.cuh -- the forward product for a handful of rows (the slots of
-// one token) or of columns.  Rows: every touched expert's W is streamed through the CUDA cores.
+// one token): every touched expert's W is streamed through the CUDA cores.
 // The tensor-core kernel takes a reduction of 2048 as 32 pipeline stages in a
 // row, each a quarter of a microsecond however few rows there are; here all of
 // a warp's loads are in flight at once.

@@ -16,7 +16,8 @@
 // are whole numbers of 4 columns (VEC), strided ones otherwise.  (Neighbouring
 // lanes have neighbouring fours, so that an access of a warp covers whole
 // sectors in fp32 and in 16 bits.)  Longer rows take a kernel that reads them
-// once a pass.
+// once a pass.  (16384 rows of 1031 columns: strided 55 us forward and 138
+// back; aligned fours with the rows' ends one by one 81 and 158.)
 #pragma once
 
 #include "grouped.h"

@@ -1,6 +1,10 @@
 // swiglu.cu -- the gated feed-forward block over grouped rows: gate and up
 // products with SwiGLU, and the down product's input gradient with SwiGLU's
-// gradient, each one kernel.
+// gradient, each one kernel: the grouped products' own, with another epilogue
+// (tensor cores; few rows forward; any width).  A pass over p in memory, or over
+// dh, is what the epilogue saves: 2048-token prompt of 256 experts of 1024 x 2048
+// (bf16, us) 186 forward with p kept where the plain product alone takes 182;
+// 113 back where its product alone takes 94 (at the copy's rate 175 and 101).
 #include "grouped_few.cuh"
 #include "grouped_simt.cuh"
 #include "swiglu.cuh"
@@ -15,7 +19,8 @@ struct KeepQuad {
         swiglu_quad(k, row, c, v, live);
     }
 };
-// Few rows: a warp has the sums of two pairs.
+// Few rows: a warp has the sums of two pairs.  (8 rows of 8 such experts: 7.5 us
+// against 11.2 on the tensor cores, the plain product 7.2.)
 struct KeepFew {
     SwigluKeep k;
     __device__ __forceinline__ void operator()(size_t row, int n0, const float (&s)[kFewRows]) const {
