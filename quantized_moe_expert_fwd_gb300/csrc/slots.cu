@@ -7,7 +7,7 @@
 // one access take), so a token's row is read and written once however many
 // slots it has, and the loads of kSlAhead slots are under way together.
 // 2048 tokens of 8 slots, 2048 columns, bf16: combine 14.4 us (5.2 TB/s), spread
-// with the weights' gradients 28.5 (5.0); the gather of 16384 tokens into 65536
+// with the weights' gradients 26.5 (5.4); the gather of 16384 tokens into 65536
 // slots 51 (6.6).  1031 columns, V = 1: 23 and 34.
 #include "grouped.h"
 #include "rows.cuh"
@@ -19,7 +19,7 @@ namespace {
 // Slots whose loads are under way together, and most threads along a token's
 // row (2048 tokens of 8 slots and 2048 columns, spread with weights' gradients;
 // 16384 tokens gathered into 65536 slots; us): 256 threads and 8 slots 36, 65;
-// 256 and 4 33, 62; 128 and 8 29.5, 55; 128 and 4 28.9, 51 (at the copy's rate
+// 256 and 4 33, 62; 128 and 8 29.5, 55; 128 and 4 28.6, 51 (at the copy's rate
 // 21, 49).
 constexpr int kSlAhead = 4;
 constexpr int kSlThreads = 128;
@@ -75,8 +75,10 @@ __global__ void __launch_bounds__(kSlThreads) k_slots_combine(SlotsArgs a, bool 
 // Block (bx, by) as above, but the threads of a token take its whole row: bx
 // up to 32 for several tokens a block, by = 1 above; grid.y pieces of their
 // slots.  DW: dweights too.
+// (Eight blocks an SM, 64 registers, where an access has eight columns: 26.5 us
+// instead of 28.6 above; where it has one: 35 instead of 34.)
 template <typename T, int V, bool DW>
-__global__ void __launch_bounds__(kSlThreads) k_slots_spread(SlotsArgs a) {
+__global__ void __launch_bounds__(kSlThreads, V == 8 ? 8 : 0) k_slots_spread(SlotsArgs a) {
     __shared__ float part[kSlThreads / 32][kSlAhead];
     pdl_launch();
     pdl_wait();
