@@ -646,7 +646,8 @@ cudaError_t gt_run(const GmmArgs& g, int cluster, int grid, const EPI& epi, cuda
     } else {
         const int red = MODE == kGmmFwd ? g.K : g.N;
         ok = gt_map16(&m.a.part, g.a, red, rows, 0, kGtBox) &&
-             gt_map16(&m.a.whole, g.a, red, rows, 0, kGtRows) && gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? G::kCols : 64);
+             gt_map16(&m.a.whole, g.a, red, rows, 0, kGtRows) &&
+             gt_map16(&m.b, g.b, g.K, g.N, g.E, MODE == kGmmFwd ? G::kCols : 64);
         m.out = m.b;
     }
     if (!ok) return cudaErrorInvalidValue;

@@ -96,7 +96,10 @@ __global__ void __launch_bounds__(kNmThreads) k_norm_any(NormArgs a) {
         const TR* r = static_cast<const TR*>(a.resid) + t * H;
         float s0 = 1.0f;
         if (a.post) {
-            const float q = cta_sum(column_sum(H, [&](int c) { const float v = to_f32(f[c]); return v * v; }), buf);
+            const float q = cta_sum(column_sum(H, [&](int c) {
+                const float v = to_f32(f[c]);
+                return v * v;
+            }), buf);
             s0 = 1.0f / sqrtf(q / float(H) + a.eps);
         }
         const float g = a.beta * (a.gate ? a.gate[t] : 1.0f);
@@ -111,7 +114,10 @@ __global__ void __launch_bounds__(kNmThreads) k_norm_any(NormArgs a) {
         };
         float s1 = 1.0f;
         if (a.x) {
-            const float q = cta_sum(column_sum(H, [&](int c) { const float v = to_f32(stored(c)); return v * v; }), buf);
+            const float q = cta_sum(column_sum(H, [&](int c) {
+                const float v = to_f32(stored(c));
+                return v * v;
+            }), buf);
             s1 = 1.0f / sqrtf(q / float(H) + a.eps);
         }
         // r' may take r's place: a column is read once more and then written, by one thread

@@ -22,7 +22,7 @@ namespace strata {
 
 namespace {
 
-constexpr int kNbPiece = 256;
+constexpr int kNbPiece = 256;                  // rows
 
 // Two columns at once (packed fp32).
 __device__ __forceinline__ uint64_t both(float v) { return pk(v, v); }
@@ -61,13 +61,17 @@ struct NormRing {
                (k < 2 ? (2 * k + h) * kT : 4 * kT + (2 * (k - 2) + h) * kTR) + threadIdx.x * (4 * sizeof(E));
     }
     template <typename E>
-    __device__ __forceinline__ void copy(const E* src, size_t at_, bool live, int slot, int c, int k, int h) const {
-        const uint32_t dst = smem_u32(at<E>(slot, c, k, h)), bytes = live && src != nullptr ? 4 * sizeof(E) : 0;
-        if (bytes) src += at_;
+    __device__ __forceinline__ void copy(const E* src, size_t from, bool live, int slot, int c, int k,
+                                         int h) const {
+        const uint32_t dst = smem_u32(at<E>(slot, c, k, h));
+        const uint32_t bytes = live && src != nullptr ? 4 * sizeof(E) : 0;
+        if (bytes) src += from;
         if constexpr (sizeof(E) == 4)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                         : "memory");
         else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                         : "memory");
     }
     template <typename E>
     __device__ __forceinline__ void take(Raw<E, 8>& r, int slot, int c, int k) const {
@@ -397,8 +401,8 @@ __global__ void __launch_bounds__(kNmThreads) k_norm_bwd_any(NormBwdArgs a) {
 
 // The CTAs' sums of a column: kJoinRows runs of them, then the runs, in order.
 constexpr int kJoinCols = 32, kJoinRows = 8;
-__global__ void __launch_bounds__(kJoinCols * kJoinRows) k_norm_join(const float* parts, int n, int H, float* dw_pre,
-                                                                     float* dw_post) {
+__global__ void __launch_bounds__(kJoinCols * kJoinRows)
+    k_norm_join(const float* parts, int n, int H, float* dw_pre, float* dw_post) {
     __shared__ float run[kJoinRows][kJoinCols];
     pdl_launch();
     pdl_wait();

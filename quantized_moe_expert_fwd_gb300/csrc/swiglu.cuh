@@ -10,8 +10,9 @@
 // where e is not.  The outputs have 16 bits: the approximate exponential (2
 // steps of 2^-23, twice) and reciprocal (1 step) and the argument's rounding
 // leave s within 7 + 1.2 |g| steps of 2^-23, next to roundings of 2^-9 or 2^-12.
-// Two columns at a time in packed fp32: 13 instructions a column of the
-// gradient where the fast exponential and quotient took 37.
+// Two columns at a time in packed fp32 (with the fast exponential and quotient,
+// column by column: 2048-token prompt of 256 experts 190 us forward and 117 back,
+// so 183 and 114).
 #pragma once
 
 #include "act8.cuh"

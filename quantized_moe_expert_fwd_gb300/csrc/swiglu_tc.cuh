@@ -17,6 +17,7 @@ __device__ __forceinline__ void put32(uint8_t* p, bool wide, const uint32_t (&w)
         reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
+
 // BF16: the operands' type, or fp16.
 template <bool BF16>
 struct SwigluPiece {
@@ -24,6 +25,7 @@ struct SwigluPiece {
     int vec_h, vec_p;                        // bytes that every row is aligned to: 32, 16, 0
     static constexpr int kStep = 32;
     static constexpr uint32_t kWarpStaging = kGtStoreWords * 4;
+    // reads nothing
     __device__ __forceinline__ int ahead(size_t, int, int, int, uint32_t*) const { return 0; }
     __device__ __forceinline__ void quad(size_t row, int c, const float* v, bool live) const {
         swiglu_quad(k, row, c, v, live);
@@ -61,11 +63,13 @@ struct SwigluPiece {
 // The gradient reads as much as it writes, 10 bytes a column and row.  A lane a
 // row, 32 bytes at a time, both took two shared-memory cycles a lane and access
 // and bound the kernel (8192 rows, 2048 to 4096 columns: 125 us, now 112, against
-// 72 of the plain product, which moves a fifth of the bytes).  So 32 columns of the warp's 32 rows go through
-// its staging, 128 bytes a row: p comes there by asynchronous copies of
-// neighbouring 16 bytes, the next columns' while these are worked on; a lane
-// reads its row's and leaves dp in its place; and 8 lanes store a row's line.
-// h follows the same way.  16-byte pieces are spread over the banks by the row.
+// 72 of the plain product, which moves a fifth of the bytes).  So 32 columns of
+// the warp's 32 rows go through its staging, 128 bytes a row: p comes there by
+// asynchronous copies of neighbouring 16 bytes, the next columns' while these
+// are worked on; a lane reads its row's and leaves dp in its place; and 8 lanes
+// store a row's line.  h follows the same way.  16-byte pieces are spread over
+// the banks by the row.  (Of the 112: stores 28, reads 12, arithmetic 3; dp by
+// TMA from the same place gains 1.)
 template <bool BF16>
 struct SwigluBackPiece {
     SwigluBack k;
@@ -108,7 +112,8 @@ struct SwigluBackPiece {
     }
     // `chunks` pieces of 16 bytes a row, out of a buffer into rows of `pitch` bytes.
     template <int PER>
-    static __device__ __forceinline__ void put(uint8_t* out, size_t pitch, int rows, int chunks, const uint8_t* buf) {
+    static __device__ __forceinline__ void put(uint8_t* out, size_t pitch, int rows, int chunks,
+                                               const uint8_t* buf) {
         const int lane = threadIdx.x & 31, q = lane % PER;
         __syncwarp();
         if (q < chunks) {
