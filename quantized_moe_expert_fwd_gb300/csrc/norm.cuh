@@ -13,11 +13,11 @@
 //
 // Both are bound by memory: every tensor moves once.  W warps have a row in
 // their registers, 8 C columns a thread: fours of neighbouring ones where rows
-// are whole numbers of 4 columns (VEC), strided ones otherwise.  (Neighbouring
-// lanes have neighbouring fours, so that an access of a warp covers whole
-// sectors in fp32 and in 16 bits.)  Longer rows take a kernel that reads them
-// once a pass.  (16384 rows of 1031 columns: strided 55 us forward and 138
-// back; aligned fours with the rows' ends one by one 81 and 158.)
+// are whole numbers of 4 columns (VEC).  Neighbouring lanes have neighbouring
+// fours, so that an access of a warp covers whole sectors in fp32 and in 16
+// bits.  Other rows: strided columns forward (16384 rows of 1031 columns 55 us;
+// aligned fours with the rows' ends one by one 81), the fours that the row lies
+// in backward.  Longer rows take a kernel that reads them once a pass.
 #pragma once
 
 #include "grouped.h"

@@ -33,6 +33,12 @@ __device__ __forceinline__ float halves(uint64_t v) {
 template <typename T>
 __device__ __forceinline__ uint64_t pair(const Raw<T, 8>& r, int i) { return pk(r.get(2 * i), r.get(2 * i + 1)); }
 
+template <typename T>
+__device__ __forceinline__ void clear(Raw<T, 8>& r, int j) {
+    if constexpr (sizeof(T) == 4) r.w[j] = 0;
+    else r.w[j >> 1] &= j & 1 ? 0xffffu : 0xffff0000u;
+}
+
 template <typename T, typename TR>
 struct NormCols {                            // eight columns of a row
     Raw<T, 8> dx, f;
@@ -42,9 +48,9 @@ struct NormScalars {
     float s0, s1, gate;
 };
 
-// Rows on their way (VEC): each thread copies its own columns of the next rows
-// to its own places in shared memory (fours of columns, no barrier), and reads
-// them there when their turn comes; what does not exist is filled with zeros.
+// Rows on their way: each thread copies its own columns of the next rows to its
+// own places in shared memory (fours of columns, no barrier), and reads them
+// there when their turn comes; what does not exist is filled with zeros.
 // kNbSteps steps of ROWS rows.
 constexpr int kNbSteps = 2;
 template <typename T, typename TR, int W, int C, int ROWS>
@@ -60,11 +66,11 @@ struct NormRing {
         return base + (slot * C + c) * kChunk +
                (k < 2 ? (2 * k + h) * kT : 4 * kT + (2 * (k - 2) + h) * kTR) + threadIdx.x * (4 * sizeof(E));
     }
+    // n of four elements from src + from on.
     template <typename E>
-    __device__ __forceinline__ void copy(const E* src, size_t from, bool live, int slot, int c, int k,
-                                         int h) const {
+    __device__ __forceinline__ void copy(const E* src, size_t from, int n, int slot, int c, int k, int h) const {
         const uint32_t dst = smem_u32(at<E>(slot, c, k, h));
-        const uint32_t bytes = live && src != nullptr ? 4 * sizeof(E) : 0;
+        const uint32_t bytes = src != nullptr ? n * sizeof(E) : 0;
         if (bytes) src += from;
         if constexpr (sizeof(E) == 4)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -89,32 +95,53 @@ struct NormRing {
 };
 
 // Where the weights' gradients are put aside: a block of one row at a time keeps
-// them in its own part of the workspace, others in shared memory.
+// them in its own part of the workspace, others in shared memory, [row of the
+// block][2][columns].
 template <typename R, int C>
 constexpr uint32_t kNbAside = R::kGroups == 1 ? 0 : 16 * C * R::kBlock * sizeof(float);
 
-// ROWS rows a step share a barrier, and hide each other's latencies.
+// ROWS rows a step share a barrier, and hide each other's latencies.  VEC: rows
+// of whole fours.  Others start and end within one; the copies take those
+// fours whole, and the columns of the rows beside are set to zero where a warp
+// has such (one column an access instead: 16384 x 1031 138 us, now 89; 8192 x
+// 2045 85, 60; 6000 x 3999 141, 88; at the copy's rate 45, 44, 64).
 template <typename T, typename TR, int W, int C, bool VEC, int ROWS>
-__global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_norm_bwd(NormBwdArgs a) {
-    using R = NormRow<W, C, VEC>;
+__global__ void __launch_bounds__(NormRow<W, C, true>::kBlock, W <= 8 ? 2 : 1) k_norm_bwd(NormBwdArgs a) {
+    using R = NormRow<W, C, true>;
     using Ring = NormRing<T, TR, W, C, ROWS>;
     using Cols = NormCols<T, TR>;
     constexpr bool KEEP = C == 1;            // the norms' weights in registers
     __shared__ NormSums<3 * ROWS> buf[2][R::kGroups][W];
     extern __shared__ __align__(16) uint8_t nb_dyn[];
-    [[maybe_unused]] float* aside = reinterpret_cast<float*>(nb_dyn);       // [2 C][8][thread]
     const Ring ring{nb_dyn + kNbAside<R, C>};
     const R row;
     pdl_launch();
     pdl_wait();
     const int H = a.H;
     const float inv = 1.0f / float(H);
-    const size_t step = size_t(gridDim.x) * R::kGroups;
+    const size_t step = size_t(gridDim.x) * R::kGroups, total = size_t(a.T) * H;
     const T* pdx = static_cast<const T*>(a.dx);
     const T* pf = static_cast<const T*>(a.f);
     const TR* pv = a.dx ? static_cast<const TR*>(a.resid_out) : nullptr;
     const TR* pr = static_cast<const TR*>(a.dresid_out);
-    // VEC: starts the copies of rows t, t + step ..
+    size_t t = size_t(blockIdx.x) * R::kGroups + row.group;
+    // columns of a row's first four that belong to the row before: the same for all
+    // of a thread's rows, as the grid is a whole number of fours of rows
+    const int off = VEC ? 0 : int((t * H) & 3);
+    auto column = [&](int c, int h) { return row.column(c, 4 * h) - off; };
+    auto live = [&](int col) { return col >= 0 && col < H; };
+    bool ends = false;                       // whether a four of the warp reaches past its row
+    if (!VEC) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = column(c, h);
+                ends |= col < 0 || (col < H && col + 4 > H);
+            }
+        ends = __any_sync(0xffffffffu, ends);
+    }
+    // starts the copies of rows t, t + step ..
     auto start = [&](size_t t, int at_step) {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
@@ -122,13 +149,14 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int col = row.column(c, 4 * h), slot = at_step * ROWS + r;
-                    const bool live = t + r * step < size_t(a.T) && col < H;
+                    const int col = column(c, h), slot = at_step * ROWS + r;
                     const size_t at = (t + r * step) * H + col;
-                    ring.copy(pdx, at, live, slot, c, 0, h);
-                    ring.copy(pf, at, live, slot, c, 1, h);
-                    ring.copy(pv, at, live, slot, c, 2, h);
-                    ring.copy(pr, at, live, slot, c, 3, h);
+                    int n = t + r * step < size_t(a.T) && col < H ? 4 : 0;
+                    if (!VEC && n && total - at < 4) n = int(total - at);     // the tensor's end
+                    ring.copy(pdx, at, n, slot, c, 0, h);
+                    ring.copy(pf, at, n, slot, c, 1, h);
+                    ring.copy(pv, at, n, slot, c, 2, h);
+                    ring.copy(pr, at, n, slot, c, 3, h);
                 }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -138,23 +166,49 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
         ring.take(o.f, slot, c, 1);
         ring.take(o.v, slot, c, 2);
         ring.take(o.dr2, slot, c, 3);
+        if (!VEC && ends) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (!live(column(c, j / 4) + j % 4)) {
+                    clear(o.dx, j);
+                    clear(o.f, j);
+                    clear(o.v, j);
+                    clear(o.dr2, j);
+                }
+        }
         return o;
     };
-    auto from_memory = [&](size_t t, int c) {
-        Cols o{};
-        if (t >= size_t(a.T)) return o;
-        const size_t at = t * H;
-        if (pdx) {
-            o.dx = row.template load<true>(pdx + at, c, H);
-            o.v = row.template load<true>(pv + at, c, H);
+    auto store = [&](auto* p, int c, const float (&v)[8], bool fours) {
+        using E = typename std::remove_pointer<decltype(p)>::type;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int col = column(c, h);
+            if (fours) {
+                if (col < H) st_row<E, 4>(p + col, reinterpret_cast<const float(&)[4]>(v[4 * h]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (live(col + j)) p[col + j] = from_f32<E>(v[4 * h + j]);
+            }
         }
-        if (pr) o.dr2 = row.template load<false>(pr + at, c, H);             // dr may take its place
-        if (pf) o.f = row.template load<true>(pf + at, c, H);
-        return o;
+    };
+    // eight columns of a vector [H]
+    auto values = [&](const float* w, int c) {
+        Raw<float, 8> r{};
+        if constexpr (VEC) {
+            r = row.template load<false>(w, c, H);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = column(c, j / 4) + j % 4;
+                if (live(col)) r.w[j] = __float_as_uint(w[col]);
+            }
+        }
+        return r;
     };
     auto weight = [&](const float* w, int c, uint64_t (&o)[4]) {
         Raw<float, 8> r{};
-        if (w) r = row.template load<true>(w, c, H);
+        if (w) r = values(w, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = w ? pair(r, i) : both(1.0f);
     };
@@ -181,21 +235,14 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
                     o[2 * i + 1] = v.y;
                     d[i] = 0;
                 }
-                if constexpr (R::kGroups == 1) {
-                    if (k == 0 ? a.dw_pre == nullptr : a.dw_post == nullptr) continue;
-                    if (set) {
-                        const Raw<float, 8> had = row.template load<false>(out + k * H, c, H);
+                if (R::kGroups == 1 && (k == 0 ? a.dw_pre == nullptr : a.dw_post == nullptr)) continue;
+                float* to = (R::kGroups == 1 ? out : reinterpret_cast<float*>(nb_dyn) + row.group * 2 * H) + k * H;
+                if (set) {
+                    const Raw<float, 8> had = values(to, c);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] += had.get(j);
-                    }
-                    row.store(out + k * H, c, H, o);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float* p = aside + ((2 * c + k) * 8 + j) * R::kBlock + threadIdx.x;
-                        *p = set ? *p + o[j] : o[j];
-                    }
+                    for (int j = 0; j < 8; ++j) o[j] += had.get(j);
                 }
+                store(to, c, o, VEC);
             }
         set = true;
     };
@@ -206,37 +253,20 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
         t = min(t, size_t(a.T) - 1);
         return NormScalars{__ldg(a.rstd + 2 * t), __ldg(a.rstd + 2 * t + 1), __ldg(pgate + t)};
     };
-    size_t t = size_t(blockIdx.x) * R::kGroups + row.group;
     NormScalars ahead[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) ahead[r] = scalars(t + r * step);
-    Cols next[C];                            // not VEC: the next row in registers
-    if constexpr (VEC) {
-        start(t, 0);
-    } else {
-        static_assert(ROWS == 1, "one row a step");
-#pragma unroll
-        for (int c = 0; c < C; ++c) next[c] = from_memory(t, c);
-    }
+    start(t, 0);
     for (int n = 0; t < size_t(a.T); t += ROWS * step, n ^= 1) {
-        Cols cur[C];
-        if constexpr (VEC) {
-            start(t + ROWS * step, n ^ 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                cur[c] = next[c];
-                next[c] = from_memory(t + step, c);
-            }
-        }
+        start(t + ROWS * step, n ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         float s0[ROWS], s1[ROWS], g[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const bool live = t + r * step < size_t(a.T);
-            s0[r] = live ? ahead[r].s0 : 0.0f;
-            s1[r] = live ? ahead[r].s1 : 0.0f;
-            g[r] = !live ? 0.0f : a.gate ? a.beta * ahead[r].gate : a.beta;
+            const bool there = t + r * step < size_t(a.T);
+            s0[r] = there ? ahead[r].s0 : 0.0f;
+            s1[r] = there ? ahead[r].s1 : 0.0f;
+            g[r] = !there ? 0.0f : a.gate ? a.beta * ahead[r].gate : a.beta;
             ahead[r] = scalars(t + (ROWS + r) * step);
         }
         // dr' + s1 dx wpre, kept for the second pass
@@ -251,7 +281,7 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
                     weight(a.w_pre, c, w_pre);
                     weight(a.w_post, c, w_post);
                 }
-                const Cols in = VEC ? from_ring(n * ROWS + r, c) : cur[c];
+                const Cols in = from_ring(n * ROWS + r, c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint64_t gx = mul2(pair(in.dx, i), w_pre[i]), v = pair(in.v, i);
@@ -279,7 +309,7 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 if (!KEEP) weight(a.w_post, c, w_post);
-                const Cols in = VEC ? from_ring(n * ROWS + r, c) : cur[c];
+                const Cols in = from_ring(n * ROWS + r, c);
                 float o[8], p[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -295,32 +325,24 @@ __global__ void __launch_bounds__(NormRow<W, C, VEC>::kBlock, W <= 8 ? 2 : 1) k_
                     p[2 * i] = y.x;
                     p[2 * i + 1] = y.y;
                 }
-                if (a.df) row.store(static_cast<T*>(a.df) + at, c, H, o);
-                if (a.dresid) row.store(static_cast<TR*>(a.dresid) + at, c, H, p);
+                if (a.df) store(static_cast<T*>(a.df) + at, c, o, !ends);
+                if (a.dresid) store(static_cast<TR*>(a.dresid) + at, c, p, !ends);
             }
         }
         if (++rows % (kNbPiece / ROWS) == 0) put_aside();
     }
-    if (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!a.dw_pre && !a.dw_post) return;
     put_aside();
     if constexpr (R::kGroups == 1) return;
     __syncthreads();
     // the groups of the block in their order
-    if (row.group == 0) {
+    for (int c = int(threadIdx.x); c < 2 * H; c += R::kBlock) {
+        if (c < H ? a.dw_pre == nullptr : a.dw_post == nullptr) continue;
+        float sum = 0.0f;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    o[j] = 0.0f;
-                    for (int i = 0; i < R::kGroups; ++i)
-                        o[j] += aside[((2 * c + k) * 8 + j) * R::kBlock + i * R::kThreads + row.id];
-                }
-                if (k == 0 ? a.dw_pre != nullptr : a.dw_post != nullptr) row.store(out + k * H, c, H, o);
-            }
+        for (int i = 0; i < R::kGroups; ++i) sum += reinterpret_cast<const float*>(nb_dyn)[i * 2 * H + c];
+        out[c] = sum;
     }
 }
 
@@ -424,27 +446,30 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRows)
 }
 
 // (8192 rows of 4096 columns: 16 warps and two rows a step 106 us, one row 142,
-// 8 warps of 16 columns a thread 120; 4096 of 8192: 144, read once a pass 390.)
+// 8 warps of 16 columns a thread 120; 4096 of 8192: 144, read once a pass 390;
+// 4096 of 6521, which is no whole number of fours: 176 and 327.)
 template <typename T, typename TR, int W, int C, bool VEC>
 cudaError_t run_rows(const NormBwdArgs& a, int* n, cudaStream_t s) {
-    constexpr int ROWS = VEC && C == 1 && W > 1 ? 2 : 1;
-    using R = NormRow<W, C, VEC>;
+    constexpr int ROWS = C == 1 && W > 1 ? 2 : 1;
+    using R = NormRow<W, C, true>;
     const int want = (a.T + R::kGroups - 1) / R::kGroups, most = device_info().sms * (W <= 8 ? 2 : 1);
     *n = want < most ? want : most;
     if (*n > kNormParts) *n = kNormParts;
     if (*n == 0) return cudaSuccess;
-    const size_t dyn = kNbAside<R, C> + (VEC ? NormRing<T, TR, W, C, ROWS>::kBytes : 0);
+    // a whole number of fours of rows in the grid (one that has fewer takes one row a thread)
+    if (!VEC && *n * R::kGroups >= 4) *n -= *n * R::kGroups % 4 / R::kGroups;
+    const size_t dyn = kNbAside<R, C> + NormRing<T, TR, W, C, ROWS>::kBytes;
     return gt_launch<k_norm_bwd<T, TR, W, C, VEC, ROWS>>(R::kBlock, 1, *n, dyn, s, a);
 }
 template <typename T, typename TR, bool VEC>
 cudaError_t run_norm_bwd(const NormBwdArgs& a, int* n, cudaStream_t s) {
-    if (a.H <= 256) return run_rows<T, TR, 1, 1, VEC>(a, n, s);
-    if (a.H <= 512) return run_rows<T, TR, 2, 1, VEC>(a, n, s);
-    if (a.H <= 1024) return run_rows<T, TR, 4, 1, VEC>(a, n, s);
-    if (a.H <= 2048) return run_rows<T, TR, 8, 1, VEC>(a, n, s);
-    if (a.H <= 4096) return run_rows<T, TR, 16, 1, VEC>(a, n, s);
-    if constexpr (VEC)
-        if (a.H <= 8192) return run_rows<T, TR, 16, 2, VEC>(a, n, s);
+    const int wide = VEC ? a.H : a.H + 3;    // a row that starts within a four has one more
+    if (wide <= 256) return run_rows<T, TR, 1, 1, VEC>(a, n, s);
+    if (wide <= 512) return run_rows<T, TR, 2, 1, VEC>(a, n, s);
+    if (wide <= 1024) return run_rows<T, TR, 4, 1, VEC>(a, n, s);
+    if (wide <= 2048) return run_rows<T, TR, 8, 1, VEC>(a, n, s);
+    if (wide <= 4096) return run_rows<T, TR, 16, 1, VEC>(a, n, s);
+    if (wide <= 8192) return run_rows<T, TR, 16, 2, VEC>(a, n, s);
     const int want = (a.T + kNmRows - 1) / kNmRows;
     *n = want < kNormParts ? want : kNormParts;
     return *n == 0 ? cudaSuccess : row_launch(k_norm_bwd_any<T, TR>, dim3(*n), dim3(kNmThreads), s, a);
