@@ -456,8 +456,9 @@ cudaError_t run_rows(const NormBwdArgs& a, int* n, cudaStream_t s) {
     *n = want < most ? want : most;
     if (*n > kNormParts) *n = kNormParts;
     if (*n == 0) return cudaSuccess;
-    // a whole number of fours of rows in the grid (one that has fewer takes one row a thread)
-    if (!VEC && *n * R::kGroups >= 4) *n -= *n * R::kGroups % 4 / R::kGroups;
+    // where a thread has several rows: a whole number of fours of rows in the grid
+    constexpr int FOURS = R::kGroups >= 4 ? 1 : 4 / R::kGroups;
+    if (!VEC && *n < want) *n = *n < FOURS ? FOURS : *n - *n % FOURS;
     const size_t dyn = kNbAside<R, C> + NormRing<T, TR, W, C, ROWS>::kBytes;
     return gt_launch<k_norm_bwd<T, TR, W, C, VEC, ROWS>>(R::kBlock, 1, *n, dyn, s, a);
 }

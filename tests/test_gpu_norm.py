@@ -235,3 +235,13 @@ def test_binding_refuses():
         q.moe_norm_residual(c["resid"], x=x, f=c["f"], w_post=c["w_post"])      # a weight of no norm
     with pytest.raises(q.StrataError):
         q.moe_norm_residual_bwd(c["resid"], torch.empty(4, 2, device="cuda"), dx=x, dw_pre=c["w_pre"])  # no workspace
+
+
+@pytest.mark.parametrize("T", [150, 151, 152, 153, 303, 304, 305, 608, 611, 1217])
+@pytest.mark.parametrize("H", [1029, 2501, 4099])
+def test_backward_of_rows_that_start_within_a_four(T, H):
+    """Around one row a thread and more, in grids that are cut to whole fours of rows."""
+    c = _case(T, H, "bf16", "bf16", True, True)
+    r2, _, rstd = _forward(c, True, "bf16", "bf16")
+    got = _backward(c, True, r2, rstd, q.make_norm_workspace(H))
+    _check_backward(c, True, r2, rstd, got, f"{T}x{H}")
