@@ -178,3 +178,32 @@ def test_single_tokens_are_served_alike():
         assert torch.equal(one.ids, b.ids[t:t + 1])
         assert _rel(one.r2 - one.r, (b.r2 - b.r)[t:t + 1].double()) < LIMIT[False]
     assert np.isfinite(b.r2.cpu().numpy()).all()
+
+
+def test_calls_on_a_named_stream():
+    """Each call takes the stream that it is given, not the current one: work queued before it there is
+    seen, and the other streams do not wait."""
+    a, b = Block(300, True, seed=7), Block(300, True, seed=7)
+    a.forward()
+    a.backward()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    real = {n: getattr(q, n) for n in dir(q) if n.startswith("moe_") and n != "moe_get_device_status"
+            and not n.endswith("_bytes")}
+    r = b.r.clone()
+    b.r.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)            # about ten milliseconds
+        b.r.copy_(r)
+    try:
+        for n, f in real.items():
+            setattr(q, n, lambda *args, _f=f, **kw: _f(*args, stream=s, **kw))
+        b.forward()
+        b.backward()
+    finally:
+        for n, f in real.items():
+            setattr(q, n, f)
+    s.synchronize()
+    for n, t in a.grads().items():
+        assert torch.equal(t, b.grads()[n]), n
