@@ -3,7 +3,12 @@
 //
 // A row's three sums come from one pass over it, as s0 and s1 are known:
 //   m = sum dx wpre r',   A = sum (dr' + s1 dx wpre) wpost f,   B = sum r' wpost f
-// give c = s1^3 m / H and sum D wpost f = A - c B.  The weights' gradients are
+// give D = dr' + s1 dx wpre - e (s1 r') and sum D wpost f = A - e (s1 B) with
+// e = s1 (s1 m / H).  The factors are multiplied so that none leaves fp32 before
+// the gradient does: s1^3 would for rows of root mean square 1e13 (its digits go;
+// at 1e15 the whole term) or, where eps lets them be, 1e-13 (infinite).
+//
+// The weights' gradients are
 // summed in the threads' registers over the rows of a CTA, set aside in shared
 // memory every kNbPiece rows (equal terms round one way within a binade), and
 // the CTAs' sums joined in their order by a second kernel.
@@ -301,11 +306,11 @@ __global__ void __launch_bounds__(NormRow<W, C, true>::kBlock, W <= 8 ? 2 : 1) k
         for (int r = 0; r < ROWS; ++r) {
             const size_t tr = t + r * step, at = tr * H;
             if (tr >= size_t(a.T)) break;
-            const float c1 = s1[r] * s1[r] * s1[r] * (q[3 * r] * inv);
-            const float dn_f = q[3 * r + 1] - c1 * q[3 * r + 2];             // sum of D wpost f
-            if (a.dgate && row.id == 0) a.dgate[tr] = a.beta * s0[r] * dn_f;
-            const float c0 = a.post ? g[r] * s0[r] * s0[r] * s0[r] * (dn_f * inv) : 0.0f;
-            const uint64_t nc1 = both(-c1), nc0 = both(-c0), gs = both(g[r] * s0[r]);
+            const float e = s1[r] * (s1[r] * (q[3 * r] * inv));
+            const float dn_f = q[3 * r + 1] - e * (s1[r] * q[3 * r + 2]);    // sum of D wpost f
+            if (a.dgate && row.id == 0) a.dgate[tr] = a.beta * (s0[r] * dn_f);
+            const float m0 = s0[r] * (s0[r] * (dn_f * inv));
+            const uint64_t ne = both(-e), nm0 = both(-m0), gs = both(g[r] * s0[r]);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 if (!KEEP) weight(a.w_post, c, w_post);
@@ -313,12 +318,12 @@ __global__ void __launch_bounds__(NormRow<W, C, true>::kBlock, W <= 8 ? 2 : 1) k
                 float o[8], p[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint64_t v = pair(in.v, i), f = pair(in.f, i);
-                    const uint64_t d = ffma2(nc1, v, part[r][c][i]);
-                    d_pre[c][i] = ffma2(both(s1[r]), mul2(pair(in.dx, i), v), d_pre[c][i]);
+                    const uint64_t v = mul2(both(s1[r]), pair(in.v, i)), f = pair(in.f, i);
+                    const uint64_t d = ffma2(ne, v, part[r][c][i]);
+                    // (with s1 r' from above: 4096 x 8192 150 us, now 145)
+                    d_pre[c][i] = ffma2(both(s1[r]), mul2(pair(in.dx, i), pair(in.v, i)), d_pre[c][i]);
                     d_post[c][i] = ffma2(gs, mul2(d, f), d_post[c][i]);
-                    const uint64_t dn = mul2(gs, a.post ? mul2(d, w_post[i]) : d);
-                    const float2 x = upk(a.post ? ffma2(nc0, f, dn) : dn);
+                    const float2 x = upk(mul2(gs, a.post ? ffma2(nm0, f, mul2(d, w_post[i])) : d));
                     const float2 y = upk(mul2(both(a.alpha), d));
                     o[2 * i] = x.x;
                     o[2 * i + 1] = x.y;
@@ -354,7 +359,7 @@ constexpr int kNmRows = 8;               // rows whose weight gradients are adde
 template <typename T, typename TR>
 __global__ void __launch_bounds__(kNmThreads) k_norm_bwd_any(NormBwdArgs a) {
     __shared__ float buf[kNmThreads / 32];
-    __shared__ float c1s[kNmRows], c0s[kNmRows];
+    __shared__ float es[kNmRows], m0s[kNmRows];
     const int H = a.H;
     pdl_launch();
     pdl_wait();
@@ -368,33 +373,33 @@ __global__ void __launch_bounds__(kNmThreads) k_norm_bwd_any(NormBwdArgs a) {
     bool first = true;
     for (size_t t0 = size_t(blockIdx.x) * kNmRows; t0 < size_t(a.T); t0 += size_t(gridDim.x) * kNmRows) {
         const int rows = int(min(size_t(kNmRows), size_t(a.T) - t0));
-        // D of one element; c1 = s1^3 mean(dx wpre r')
-        auto grad = [&](size_t at, int c, float s1, float c1) {
+        // D of one element; e = s1^2 mean(dx wpre r')
+        auto grad = [&](size_t at, int c, float s1, float e) {
             float d = dr2 ? to_f32(dr2[at]) : 0.0f;
-            if (dx) d += fmaf(s1, to_f32(dx[at]) * (a.w_pre ? a.w_pre[c] : 1.0f), -c1 * to_f32(v[at]));
+            if (dx) d += fmaf(s1, to_f32(dx[at]) * (a.w_pre ? a.w_pre[c] : 1.0f), -e * (s1 * to_f32(v[at])));
             return d;
         };
         __syncthreads();
         for (int i = 0; i < rows; ++i) {
             const size_t t = t0 + i, row = t * H;
             const float s0 = a.rstd[2 * t], s1 = a.rstd[2 * t + 1];
-            float c1 = 0.0f, c0 = 0.0f;
+            float e = 0.0f, m0 = 0.0f;
             if (dx) {
                 const float q = cta_sum(column_sum(H, [&](int c) {
                     return to_f32(dx[row + c]) * (a.w_pre ? a.w_pre[c] : 1.0f) * to_f32(v[row + c]);
                 }), buf);
-                c1 = s1 * s1 * s1 * (q * inv);
+                e = s1 * (s1 * (q * inv));
             }
             if (a.post || a.dgate) {
                 const float q = cta_sum(column_sum(H, [&](int c) {
-                    return grad(row + c, c, s1, c1) * (a.w_post ? a.w_post[c] : 1.0f) * to_f32(f[row + c]);
+                    return grad(row + c, c, s1, e) * (a.w_post ? a.w_post[c] : 1.0f) * to_f32(f[row + c]);
                 }), buf);
-                if (a.dgate && threadIdx.x == 0) a.dgate[t] = a.beta * s0 * q;
-                if (a.post) c0 = a.beta * (a.gate ? a.gate[t] : 1.0f) * s0 * s0 * s0 * (q * inv);
+                if (a.dgate && threadIdx.x == 0) a.dgate[t] = a.beta * (s0 * q);
+                m0 = s0 * (s0 * (q * inv));
             }
             if (threadIdx.x == 0) {
-                c1s[i] = c1;
-                c0s[i] = c0;
+                es[i] = e;
+                m0s[i] = m0;
             }
         }
         __syncthreads();
@@ -403,13 +408,14 @@ __global__ void __launch_bounds__(kNmThreads) k_norm_bwd_any(NormBwdArgs a) {
             for (int i = 0; i < rows; ++i) {
                 const size_t t = t0 + i, at = t * H + c;
                 const float s0 = a.rstd[2 * t], s1 = a.rstd[2 * t + 1];
-                const float d = grad(at, c, s1, c1s[i]);
-                const float dn = a.beta * (a.gate ? a.gate[t] : 1.0f) * d;
+                const float d = grad(at, c, s1, es[i]);
+                const float g = a.beta * (a.gate ? a.gate[t] : 1.0f), dn = g * d;
                 if (a.dw_pre) dw_pre += to_f32(dx[at]) * to_f32(v[at]) * s1;
                 if (a.dw_post) dw_post += dn * to_f32(f[at]) * s0;
                 if (a.df) {
                     float o = dn;
-                    if (a.post) o = fmaf(s0, dn * (a.w_post ? a.w_post[c] : 1.0f), -c0s[i] * to_f32(f[at]));
+                    if (a.post)
+                        o = g * s0 * fmaf(-m0s[i], to_f32(f[at]), d * (a.w_post ? a.w_post[c] : 1.0f));
                     static_cast<T*>(a.df)[at] = from_f32<T>(o);
                 }
                 if (a.dresid) static_cast<TR*>(a.dresid)[at] = from_f32<TR>(a.alpha * d);
