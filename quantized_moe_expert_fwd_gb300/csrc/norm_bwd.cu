@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(NormRow<W, C, true>::kBlock, W <= 8 ? 2 : 1) k
         for (int r = 0; r < ROWS; ++r) {
             const bool there = t + r * step < size_t(a.T);
             s0[r] = there ? ahead[r].s0 : 0.0f;
-            s1[r] = there ? ahead[r].s1 : 0.0f;
+            s1[r] = there && a.dx ? ahead[r].s1 : 0.0f;      // (infinite times no dx is no number)
             g[r] = !there ? 0.0f : a.gate ? a.beta * ahead[r].gate : a.beta;
             ahead[r] = scalars(t + (ROWS + r) * step);
         }
