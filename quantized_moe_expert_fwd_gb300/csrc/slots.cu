@@ -23,6 +23,12 @@ namespace {
 // 21, 49).
 constexpr int kSlAhead = 4;
 constexpr int kSlThreads = 128;
+// Accesses of a row whose products a thread adds before it sets the sum aside:
+// within a binade equal terms all round one way, and 8192 one after the other
+// came out 1.2e-4 off.  The kernels of longer rows, which have a block each, are
+// their own (LONG): the checks cost them up to 8 % (200 tokens of 2 slots, 40001
+// columns: 201 us, now 215), and others 4 to 10 % (2048 tokens of 8 slots: 28.2).
+constexpr int kSlPiece = 64;
 
 // The slots k0 .. of a token and their weights (-1, 0 where there is none).
 // Returns whether one lies outside [0, M).
@@ -77,9 +83,10 @@ __global__ void __launch_bounds__(kSlThreads) k_slots_combine(SlotsArgs a, bool 
 // slots.  DW: dweights too.
 // (Eight blocks an SM, 64 registers, where an access has eight columns: 26.5 us
 // instead of 28.6 above; where it has one: 35 instead of 34.)
-template <typename T, int V, bool DW>
+template <typename T, int V, bool DW, bool LONG>
 __global__ void __launch_bounds__(kSlThreads, V == 8 ? 8 : 0) k_slots_spread(SlotsArgs a) {
     __shared__ float part[kSlThreads / 32][kSlAhead];
+    __shared__ float aside[LONG ? kSlAhead : 1][LONG ? kSlThreads : 1];
     pdl_launch();
     pdl_wait();
     const size_t t = size_t(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -95,7 +102,20 @@ __global__ void __launch_bounds__(kSlThreads, V == 8 ? 8 : 0) k_slots_spread(Slo
         int slot[kSlAhead];
         float w[kSlAhead], dot[kSlAhead] = {};
         const bool bad = slots_of(a, live ? t : 0, k0, slot, w);
+        int next = first + kSlPiece * kSlThreads * V;        // the next piece (LONG)
+        if (LONG) {
+#pragma unroll
+            for (int i = 0; i < kSlAhead; ++i) aside[i][threadIdx.x] = 0.0f;
+        }
         for (int c = first; live && c < a.H; c += int(blockDim.x) * V) {
+            if (LONG && c == next) {
+                next += kSlPiece * kSlThreads * V;
+#pragma unroll
+                for (int i = 0; i < kSlAhead; ++i) {
+                    aside[i][threadIdx.x] += dot[i];
+                    dot[i] = 0.0f;
+                }
+            }
             const Raw<T, V> rd = c == first ? ahead : ld_row<T, V>(dout + c);
             Raw<T, V> r[kSlAhead];
             if (DW) {
@@ -134,7 +154,10 @@ __global__ void __launch_bounds__(kSlThreads, V == 8 ? 8 : 0) k_slots_spread(Slo
         if (bad && live && threadIdx.x == 0) latch(a.err, STRATA_EBADROUTE);
         if (!DW) continue;
 #pragma unroll
-        for (int i = 0; i < kSlAhead; ++i) dot[i] = group_sum(dot[i], min(32, int(blockDim.x)));
+        for (int i = 0; i < kSlAhead; ++i) {
+            if (LONG) dot[i] += aside[i][threadIdx.x];       // its own
+            dot[i] = group_sum(dot[i], min(32, int(blockDim.x)));
+        }
         float* out = a.dweights + t * a.top_k + k0;
         if (blockDim.x <= 32) {
 #pragma unroll
@@ -178,8 +201,9 @@ cudaError_t run_spread(const SlotsArgs& a, cudaStream_t s) {
     // few tokens: their slots in pieces side by side (16 tokens of ten slots: 6.4 us in a row)
     const int pieces = a.T <= device_info().sms * 2 ? (a.top_k + kSlAhead - 1) / kSlAhead : 1;
     const dim3 grid((a.T + by - 1) / by, pieces);
-    return a.dweights ? row_launch(k_slots_spread<T, V, true>, grid, dim3(bx, by), s, a)
-                      : row_launch(k_slots_spread<T, V, false>, grid, dim3(bx, by), s, a);
+    if (!a.dweights) return row_launch(k_slots_spread<T, V, false, false>, grid, dim3(bx, by), s, a);
+    return a.H > kSlPiece * kSlThreads * V ? row_launch(k_slots_spread<T, V, true, true>, grid, dim3(bx, by), s, a)
+                                           : row_launch(k_slots_spread<T, V, true, false>, grid, dim3(bx, by), s, a);
 }
 
 template <typename T, typename TO>
