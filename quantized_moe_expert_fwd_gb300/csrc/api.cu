@@ -1355,7 +1355,9 @@ strata_status moe_slots_spread(int32_t dtype, const void* dout_dev, const int32_
                                float* dweights_dev, void* ws_dev, size_t ws_bytes, void* stream) {
     if (!slots_shape_ok(dtype, M, H, T, top_k)) return STRATA_EINVAL;
     if (T == 0) return STRATA_OK;
-    if ((dy_dev == nullptr && dweights_dev == nullptr) || (dweights_dev == nullptr) != (y_dev == nullptr))
+    // (no slots: nothing to point at, and every one named is out of range)
+    if (M > 0 &&
+        ((dy_dev == nullptr && dweights_dev == nullptr) || (dweights_dev == nullptr) != (y_dev == nullptr)))
         return STRATA_EINVAL;
     if (!al16(dout_dev) || !al4(inv_perm_dev) || !opt4(weights_dev) || !opt16(y_dev) || !opt16(dy_dev) ||
         !opt4(dweights_dev) || !grouped_ws_ok(ws_dev, ws_bytes))
