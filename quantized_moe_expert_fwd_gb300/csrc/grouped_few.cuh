@@ -133,8 +133,12 @@ __device__ __forceinline__ void few_unit(const GmmArgs& g, const EPI& epi, int e
     }
 }
 
-template <bool BF16, bool LONG, typename EPI>
-__global__ void __launch_bounds__(kFewThreads, 2) k_gmm_few(GmmArgs g, EPI epi) {
+// CTAS: blocks an SM.  Two leave a thread 128 registers and spill a few; a grid
+// that has no more than one an SM keeps them all (us, bf16 and fp16, two and one:
+// 8 rows of 2 experts, 512 x 1032, 6.8 7.3 and 5.7 5.8; of 8 experts, 512 x 2048,
+// 6.0 6.2 and 5.8 5.9; but 1024 x 2048, whose grid is larger, 7.7 7.9 and 9.3 9.5).
+template <bool BF16, bool LONG, int CTAS, typename EPI>
+__global__ void __launch_bounds__(kFewThreads, CTAS) k_gmm_few(GmmArgs g, EPI epi) {
     __shared__ FewTable t;
     __shared__ float aside[LONG ? kFewThreads / 32 : 1][LONG ? kFewX * kFewRows * 32 : 1];
     pdl_launch();
@@ -172,8 +176,11 @@ cudaError_t few_launch(void (*kernel)(P...), int units, int per_sm, cudaStream_t
 template <bool BF16, typename EPI>
 cudaError_t run_few(const GmmArgs& g, const EPI& epi, cudaStream_t s) {
     const int units = (g.M < g.E ? g.M : g.E) * ((g.N + kFewRows - 1) / kFewRows);
-    return few_long(g) ? few_launch(k_gmm_few<BF16, true, EPI>, units, 2, s, g, epi)
-                       : few_launch(k_gmm_few<BF16, false, EPI>, units, 2, s, g, epi);
+    if (units <= device_info().sms * (kFewThreads / 32))
+        return few_long(g) ? few_launch(k_gmm_few<BF16, true, 1, EPI>, units, 1, s, g, epi)
+                           : few_launch(k_gmm_few<BF16, false, 1, EPI>, units, 1, s, g, epi);
+    return few_long(g) ? few_launch(k_gmm_few<BF16, true, 2, EPI>, units, 2, s, g, epi)
+                       : few_launch(k_gmm_few<BF16, false, 2, EPI>, units, 2, s, g, epi);
 }
 
 }  // namespace
