@@ -150,7 +150,7 @@ __device__ __forceinline__ void gt_part(float* p, const float* v) {
 }
 
 // What becomes of the sums: the output as it is (GtPlain), or an epilogue EPI
-// (16-bit outputs of forward and dx).  It takes kStep columns of a warp's 32
+// (16-bit outputs of forward and dx).  It takes 32 columns of a warp's 32
 // rows at a time,
 //   take(read ahead, first row, rows, first column, end, values, the warp's
 //        staging),
@@ -481,10 +481,9 @@ __global__ void __launch_bounds__(kGtThreads, 1)
                     tmem_st_wait();
                 }
 #pragma unroll 1
-                for (int c = 0; c < BN / 2; c += EPI::kStep) {
-                    uint32_t v[EPI::kStep];
-                    if constexpr (EPI::kStep == 32) tmem_ld32(tl + buf * BN + c, v);
-                    else tmem_ld16(tl + buf * BN + c, v);
+                for (int c = 0; c < BN / 2; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tl + buf * BN + c, v);
                     tmem_ld_wait();
                     epi.take(read, i.orow + r - lane, live, c0 + c, last, reinterpret_cast<const float*>(v),
                              store);

@@ -23,7 +23,6 @@ template <bool BF16>
 struct SwigluPiece {
     SwigluKeep k;
     int vec_h, vec_p;                        // bytes that every row is aligned to: 32, 16, 0
-    static constexpr int kStep = 32;
     static constexpr uint32_t kWarpStaging = kGtStoreWords * 4;
     // reads nothing
     __device__ __forceinline__ int ahead(size_t, int, int, int, uint32_t*) const { return 0; }
@@ -73,7 +72,6 @@ struct SwigluPiece {
 template <bool BF16>
 struct SwigluBackPiece {
     SwigluBack k;
-    static constexpr int kStep = 32;
     static constexpr uint32_t kBuffer = 32 * 128, kWarpStaging = 2 * kBuffer;
     struct Ahead {
         int buf;                             // the buffer that holds the next columns
