@@ -4,9 +4,11 @@
 // row, each a quarter of a microsecond however few rows there are; here all of
 // a warp's loads are in flight at once.
 //
-// Measured (1024 x 2048 experts, bf16, 8 rows of 8 experts, 33.5 MB): 6.5 us
-// (5.1 TB/s) against 11.1 on the tensor cores; 16 rows: 13.8 against 14.0;
-// 32 rows of 4 experts: 11.6 against 10.3.  Hence at most 8 rows.
+// Measured (1024 x 2048 experts, bf16, 8 rows of 8 experts, 33.5 MB, another
+// eight every call so that they come from HBM): 7.6 us (4.4 TB/s; 5.3 where the
+// L2 holds them) against 11.4 on the tensor cores; 16 rows of 16: 13.0 against
+// 15.2; 32 rows of 4 experts: 12.2 against 14.3, but from the L2 11.6 against
+// 10.3.  Hence at most 8 rows, where both favour it.
 //
 // Every CTA finds the touched groups itself (one load of the offsets), then
 // the warps of the grid take (group, rows of W) units in turn.  A lane loads

@@ -8,10 +8,10 @@
 // the gradient does: s1^3 would for rows of root mean square 1e13 (its digits go;
 // at 1e15 the whole term) or, where eps lets them be, 1e-13 (infinite).
 //
-// The weights' gradients are
-// summed in the threads' registers over the rows of a CTA, set aside in shared
-// memory every kNbPiece rows (equal terms round one way within a binade), and
-// the CTAs' sums joined in their order by a second kernel.
+// The weights' gradients are summed in the threads' registers over the rows of a
+// CTA, set aside every kNbPiece rows (equal terms round one way within a binade;
+// in shared memory, or where a CTA has one row at a time in its own part of the
+// workspace), and the CTAs' sums joined in their order by a second kernel.
 //
 // 16384 rows of 2048 columns (bf16, fp32 residual; us; at the copy's rate 89, and
 // about 4 for the join), as it was built: rows read once a pass 420; in
@@ -105,7 +105,9 @@ struct NormRing {
 template <typename R, int C>
 constexpr uint32_t kNbAside = R::kGroups == 1 ? 0 : 16 * C * R::kBlock * sizeof(float);
 
-// ROWS rows a step share a barrier, and hide each other's latencies.  VEC: rows
+// ROWS rows a step share a barrier, and hide each other's latencies (a row of one
+// warp has no barrier: two a step only cost registers, 65536 x 256 52 us with
+// one, 62 with two; 131072 x 64 67 and 85).  VEC: rows
 // of whole fours.  Others start and end within one; the copies take those
 // fours whole, and the columns of the rows beside are set to zero where a warp
 // has such (one column an access instead: 16384 x 1031 138 us, now 89; 8192 x
@@ -452,8 +454,10 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRows)
 }
 
 // (8192 rows of 4096 columns: 16 warps and two rows a step 106 us, one row 142,
-// 8 warps of 16 columns a thread 120; 4096 of 8192: 144, read once a pass 390;
-// 4096 of 6521, which is no whole number of fours: 176 and 327.)
+// 8 warps of 16 columns a thread 120; 4096 of 8192: 145, read once a pass 390;
+// 4096 of 6521, which is no whole number of fours: 175 and 327.  Longer rows,
+// from 8190 on where they are no whole fours: read once a pass, 4096 of 8190 400
+// us where 8189 take 198, 16 of 8196 150.)
 template <typename T, typename TR, int W, int C, bool VEC>
 cudaError_t run_rows(const NormBwdArgs& a, int* n, cudaStream_t s) {
     constexpr int ROWS = C == 1 && W > 1 ? 2 : 1;

@@ -7,7 +7,7 @@
 // one access take), so a token's row is read and written once however many
 // slots it has, and the loads of kSlAhead slots are under way together.
 // 2048 tokens of 8 slots, 2048 columns, bf16: combine 14.4 us (5.2 TB/s), spread
-// with the weights' gradients 26.5 (5.4); the gather of 16384 tokens into 65536
+// with the weights' gradients 25.6 (5.5); the gather of 16384 tokens into 65536
 // slots 51 (6.6).  1031 columns, V = 1: 23 and 34.
 #include "grouped.h"
 #include "rows.cuh"
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kSlThreads) k_slots_combine(SlotsArgs a, bool 
 // Block (bx, by) as above, but the threads of a token take its whole row: bx
 // up to 32 for several tokens a block, by = 1 above; grid.y pieces of their
 // slots.  DW: dweights too.
-// (Eight blocks an SM, 64 registers, where an access has eight columns: 26.5 us
+// (Eight blocks an SM, 64 registers, where an access has eight columns: 25.6 us
 // instead of 28.6 above; where it has one: 35 instead of 34.)
 template <typename T, int V, bool DW, bool LONG>
 __global__ void __launch_bounds__(kSlThreads, V == 8 ? 8 : 0) k_slots_spread(SlotsArgs a) {
@@ -198,7 +198,12 @@ template <typename T, int V>
 cudaError_t run_spread(const SlotsArgs& a, cudaStream_t s) {
     const int units = (a.H + V - 1) / V, bx = threads_along(units, kSlThreads);
     const int by = bx <= 32 ? kSlThreads / bx : 1;
-    // few tokens: their slots in pieces side by side (16 tokens of ten slots: 6.4 us in a row)
+    // Few tokens: their slots in pieces side by side.  (8 slots, 2048 columns, with
+    // the weights' gradients, us, side by side and in a row: 16 tokens 3.2 and 5.2,
+    // 304 5.0 and 7.7, 608 9.3 and 11.4, 1216 16.3 and 15.8, 2432 30.3 and 28.9; the
+    // gather 1.9 and 2.5, 3.6 and 3.8, 5.0 and 6.0, 8.2 and 8.5, 15.4 both, but 456
+    // tokens 4.2 and 3.7, of 5 slots 304 3.4 and 2.9, 456 3.8 and 3.0.  Hence two
+    // tokens an SM.)
     const int pieces = a.T <= device_info().sms * 2 ? (a.top_k + kSlAhead - 1) / kSlAhead : 1;
     const dim3 grid((a.T + by - 1) / by, pieces);
     if (!a.dweights) return row_launch(k_slots_spread<T, V, false, false>, grid, dim3(bx, by), s, a);
