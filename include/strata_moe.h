@@ -634,8 +634,8 @@ STRATA_API strata_status moe_norm_residual(int32_t dtype, int32_t resid_dtype, c
                                            float eps, void* resid_out_dev, void* x_dev,
                                            float* rstd_dev, void* stream);
 
-/* Its gradients from dx (by x; NULL: x was not taken) and dresid_out (by r'
- * from elsewhere; NULL: zeros; one of the two at least).  With
+/* Its gradients from dx (by x; NULL: x was not taken, or has none) and dresid_out
+ * (by r' from elsewhere; NULL: zeros; one of the two at least).  With
  *   D = dresid_out + s1 (dx w_pre - r' s1^2 mean(dx w_pre r'))
  *   dresid = alpha D          dgate[t] = beta sum(D n)       dn = beta gate D
  *   df = s0 (dn w_post - f s0^2 mean(dn w_post f))           (post_norm == 0: dn)
